@@ -86,7 +86,8 @@ typedef enum {
  * 4 metadata bytes per 16 stored values of a sparse-MFMA lane) and
  * accumulate into fp32. */
 typedef enum {
-    SSG_F16 = 0, SSG_BF16 = 1, SSG_I8 = 2, SSG_F32 = 3, SSG_I32 = 4, SSG_E4M3 = 5, SSG_E5M2 = 6, SSG_I4 = 7
+    SSG_F16 = 0, SSG_BF16 = 1, SSG_I8 = 2, SSG_F32 = 3, SSG_I32 = 4, SSG_E4M3 = 5, SSG_E5M2 = 6, SSG_I4 = 7,
+    SSG_MX4 = 8             /* 4-bit microscaled floats, see ssg_mx4_quantize */
 } ssg_dtype;
 
 /* SpMM algorithms.  AUTO picks by shape; the others force one kernel family
@@ -579,6 +580,89 @@ int ssg_mfma_probe(int form, int64_t workgroups, int64_t iters, uint32_t* sink, 
  * Errors: SSG_ERR_NULL for no offsets or sink, SSG_ERR_SHAPE for
  * non-positive counts or an offset that is misaligned or too large. */
 int ssg_lds_read_probe(const uint32_t* offsets, int64_t workgroups, int64_t iters, uint32_t* sink, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * 4-bit microscaled floats (mx4).  Along K, blocks of 32 elements share the
+ * scale 2^(s - 127), s a byte (255: the block is NaN); an element is an E2M1
+ * float (sign, two exponent bits, one fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6), two per byte, the even element in the low nibble.  A matrix [R, K] is
+ *   elems   [R, 16 * ceil(K / 32)] bytes, elements past K zero
+ *   scales  [R, ceil(K / 32)] bytes
+ * with row strides in bytes.
+ *
+ * ssg_mx4_quantize: each block's scale exponent is floor(log2 max|x|) - 2 (at
+ * least -127), each element x / scale rounded to the nearest code (ties to
+ * the even one), saturating at 6.  Infinities read back as infinities; a
+ * block with a NaN reads back as NaN.  ssg_mx4_dequantize rounds to nearest
+ * even where the type is narrower than the product element * scale.  Matrices
+ * of fp16, bf16 or fp32, any K, any row stride and alignment.
+ */
+int64_t ssg_mx4_elem_cols(int64_t K);
+int64_t ssg_mx4_scale_cols(int64_t K);
+int ssg_mx4_quantize(int dtype, int64_t R, int64_t K, const void* A, int64_t lda, uint8_t* elems,
+                     int64_t lde, uint8_t* scales, int64_t lds, void* stream);
+int ssg_mx4_dequantize(int dtype, int64_t R, int64_t K, const uint8_t* elems, int64_t lde,
+                       const uint8_t* scales, int64_t lds, void* D, int64_t ldd, void* stream);
+
+/* Y[n, m] = sum_k X[n, k] W[m, k]: token-major activations X [N, K] against
+ * mx4 weights W [M, K]; x is SSG_F16 or SSG_BF16 (xscales NULL) or SSG_MX4
+ * (X the elements, xscales the scales).  Y [N, M] is fp32 or x's type (any of
+ * fp32, fp16, bf16 for SSG_MX4); sums are fp32.  16-bit activations meet the
+ * weights' exact values.  Row strides of X: elements (bytes for SSG_MX4), of
+ * W, scales and xscales: bytes.
+ *
+ * The *_workspace_bytes call with the same operands gives the workspace a
+ * product needs (0 for few rows and for most aligned operands): partial sums
+ * where the contraction is split, copies of operands whose rows are not
+ * aligned to 16 bytes.  ws may be NULL where it is 0.
+ */
+size_t ssg_mm_mx4_workspace_bytes(int x, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+                                  const uint8_t* xscales, int64_t ldxs, const uint8_t* W, int64_t ldw,
+                                  const uint8_t* scales, int64_t lds);
+int ssg_mm_mx4(int x, int y, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+               const uint8_t* xscales, int64_t ldxs, const uint8_t* W, int64_t ldw, const uint8_t* scales,
+               int64_t lds, void* Y, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
+/* Products grouped by expert.  The rows of X [N, K] are sorted by expert; rows
+ * offs[e] .. offs[e + 1] - 1 meet the weight of expert e; offs has E + 1
+ * entries on the device.  Rows before offs[0] and from offs[E] on get zeros.
+ * offs has to ascend inside 0 .. N; the host cannot check it, and the kernels
+ * clamp it, so that other offsets give wrong results but no access out of
+ * range.  Weights W [E, M, K] with row stride ldw and expert stride stridew.
+ *   ssg_grouped_mm_mx4   Y[n, m] = sum_k X[n, k] W_e[m, k], mx4 weights
+ *   ssg_grouped_mm       the same, W and X both fp16 or both bf16
+ *   ssg_grouped_mm_dx    dX[n, k] = sum_m dY[n, m] W_e[m, k]
+ *   ssg_grouped_mm_dw    dW_e[m, k] = sum_{n of e} dY[n, m] X[n, k] (zeros for
+ *                        an expert without rows)
+ * Outputs are fp32 or the inputs' type; sums are fp32.  16-bit strides count
+ * elements, those of mx4 operands and scales bytes.
+ */
+size_t ssg_grouped_mm_mx4_workspace_bytes(int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* X,
+                                          int64_t ldx, const uint8_t* xscales, int64_t ldxs,
+                                          const uint8_t* W, int64_t ldw, int64_t stridew,
+                                          const uint8_t* scales, int64_t lds, int64_t strides,
+                                          const int32_t* offs);
+int ssg_grouped_mm_mx4(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+                       const uint8_t* xscales, int64_t ldxs, const uint8_t* W, int64_t ldw, int64_t stridew,
+                       const uint8_t* scales, int64_t lds, int64_t strides, const int32_t* offs, void* Y,
+                       int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+size_t ssg_grouped_mm_workspace_bytes(int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* X,
+                                      int64_t ldx, const void* W, int64_t ldw, int64_t stridew,
+                                      const int32_t* offs);
+int ssg_grouped_mm(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+                   const void* W, int64_t ldw, int64_t stridew, const int32_t* offs, void* Y, int64_t ldy,
+                   void* ws, size_t ws_bytes, void* stream);
+size_t ssg_grouped_mm_dx_workspace_bytes(int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* dY,
+                                         int64_t lddy, const void* W, int64_t ldw, int64_t stridew,
+                                         const int32_t* offs);
+int ssg_grouped_mm_dx(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy,
+                      const void* W, int64_t ldw, int64_t stridew, const int32_t* offs, void* dX,
+                      int64_t lddx, void* ws, size_t ws_bytes, void* stream);
+size_t ssg_grouped_mm_dw_workspace_bytes(int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* dY,
+                                         int64_t lddy, const void* X, int64_t ldx, const int32_t* offs);
+int ssg_grouped_mm_dw(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy,
+                      const void* X, int64_t ldx, const int32_t* offs, void* dW, int64_t lddw,
+                      int64_t stridedw, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

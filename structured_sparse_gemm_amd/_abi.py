@@ -12,7 +12,7 @@ LIB_PATH = os.path.join(PKG, "libssgemm.so")
 
 SSG_OK, SSG_ERR_NULL, SSG_ERR_SHAPE, SSG_ERR_STRIDE, SSG_ERR_DTYPE = 0, 1, 2, 3, 4
 SSG_ERR_FORMAT, SSG_ERR_WORKSPACE, SSG_ERR_HIP, SSG_ERR_ALGO = 5, 6, 7, 8
-SSG_F16, SSG_BF16, SSG_I8, SSG_F32, SSG_I32, SSG_E4M3, SSG_E5M2, SSG_I4 = 0, 1, 2, 3, 4, 5, 6, 7
+SSG_F16, SSG_BF16, SSG_I8, SSG_F32, SSG_I32, SSG_E4M3, SSG_E5M2, SSG_I4, SSG_MX4 = 0, 1, 2, 3, 4, 5, 6, 7, 8
 SSG_ALGO_AUTO, SSG_ALGO_GENERIC, SSG_ALGO_SMALL_N, SSG_ALGO_LARGE_N = 0, 1, 2, 3
 
 _i = ctypes.c_int
@@ -84,6 +84,26 @@ SIGNATURES = {
     "ssg_mfma_probe": (_i, [_i, _i64, _i64, _vp, _vp]),
     "ssg_lds_read_probe": (_i, [_vp, _i64, _i64, _vp, _vp]),
     "ssg_spmm_select_algo": (_i, [_i, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64]),
+    "ssg_mx4_elem_cols": (_i64, [_i64]),
+    "ssg_mx4_scale_cols": (_i64, [_i64]),
+    "ssg_mx4_quantize": (_i, [_i, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "ssg_mx4_dequantize": (_i, [_i, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "ssg_mm_mx4_workspace_bytes": (_sz, [_i, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64]),
+    "ssg_mm_mx4": (_i, [_i, _i, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _sz,
+          _vp]),
+    "ssg_grouped_mm_mx4_workspace_bytes": (_sz, [_i, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64,
+          _vp, _i64, _i64, _vp]),
+    "ssg_grouped_mm_mx4": (_i, [_i, _i, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64,
+          _i64, _vp, _vp, _i64, _vp, _sz, _vp]),
+    "ssg_grouped_mm_workspace_bytes": (_sz, [_i, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp]),
+    "ssg_grouped_mm": (_i, [_i, _i, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _sz,
+          _vp]),
+    "ssg_grouped_mm_dx_workspace_bytes": (_sz, [_i, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp]),
+    "ssg_grouped_mm_dx": (_i, [_i, _i, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _sz,
+          _vp]),
+    "ssg_grouped_mm_dw_workspace_bytes": (_sz, [_i, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "ssg_grouped_mm_dw": (_i, [_i, _i, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _sz,
+          _vp]),
 }
 
 _lock = threading.Lock()

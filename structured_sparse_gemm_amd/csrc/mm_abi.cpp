@@ -1,0 +1,414 @@
+// mm_abi.cpp -- the C ABI of the mx4 format and of the dense and grouped
+// matrix products: host-side checks, the choice of kernel, and the workspace
+// (partials of a split contraction, operands repacked into aligned rows).
+#include "ssgemm.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdarg>
+#include <cstdint>
+#include <cstdio>
+
+#include "mm_args.hpp"
+#include "ssg_abi.hpp"
+
+namespace {
+
+using ssg::MmArgs;
+
+int fail(int status, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    return ssg::abi_fail(status, buf);
+}
+
+int hip_status(hipError_t e, const char* what) {
+    return e == hipSuccess ? SSG_OK : fail(SSG_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+typedef long long ll;
+
+constexpr int64_t kMaxDim = (int64_t)1 << 31;
+constexpr int kCUs = 256;
+
+bool al(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+int64_t blocks(int64_t K) { return (K + ssg::kMxBlock - 1) / ssg::kMxBlock; }
+
+bool float16_type(int dt) { return dt == SSG_F16 || dt == SSG_BF16; }
+int64_t float_bytes(int dt) { return dt == SSG_F32 ? 4 : 2; }
+int to_dt(int dt) { return dt == SSG_F16 ? ssg::DT_F16 : ssg::DT_BF16; }
+int to_out(int dt) { return dt == SSG_F32 ? ssg::OUT_F32 : dt == SSG_F16 ? ssg::OUT_F16 : ssg::OUT_BF16; }
+
+// ------------------------------------------------------------------ the choice of kernel
+
+// Tile sizes of the tiled kernel, its workgroups a CU holds at once, and the
+// matrix rate of a full chip of them relative to the largest tile.
+struct Tile {
+    int q, p, per_cu;
+    double rate;
+};
+constexpr Tile kTiles[3] = {{256, 256, 1, 1.0}, {128, 128, 2, 0.7}, {128, 64, 3, 0.5}};
+
+struct Plan {
+    bool skinny;
+    int rt, nt;                        // skinny: 16-row groups of weights and tokens
+    int size, splits;                  // tiles
+    bool copy_q, copy_p, copy_qs, copy_ps;
+    int64_t at_q, at_p, at_qs, at_ps, at_part;   // workspace offsets
+    int64_t ldq, ldp, lds_q, lds_p;    // strides of the copies
+    size_t bytes;
+};
+
+// Rows and row bytes of an operand as stored.
+int64_t q_rows(const MmArgs& a) { return a.pt ? a.C : a.qt ? a.C : a.Q; }
+int64_t q_bytes(const MmArgs& a) {
+    if (a.mode != ssg::MM_16) return blocks(a.C) * 16;
+    return (a.qt ? a.Q : a.C) * 2;
+}
+int64_t p_rows(const MmArgs& a) { return a.pt ? a.C : a.P; }
+int64_t p_bytes(const MmArgs& a) {
+    if (a.mode == ssg::MM_MX4) return blocks(a.C) * 16;
+    return (a.pt ? a.P : a.C) * 2;
+}
+int64_t q_mats(const MmArgs& a) { return a.pt ? 1 : std::max<int64_t>(a.E, 1); }
+
+Plan plan(const MmArgs& a) {
+    Plan p{};
+    p.splits = 1;
+    const int64_t busy = a.offs && !a.pt ? std::max<int64_t>(1, std::min(a.E, a.P)) : 1;
+    const int64_t avg = (a.P + busy - 1) / busy;         // rows of an expert that has some
+    if (!a.qt && !a.pt && avg <= 32) {
+        p.skinny = true;
+        p.nt = avg <= 16 ? 1 : 2;
+        const int64_t tiles = a.P / (16 * p.nt) + busy;
+        p.rt = (a.Q + 31) / 32 * tiles >= 2 * kCUs ? 2 : 1;
+        return p;
+    }
+    // The tile: rounds of a full chip times what a round of that tile takes
+    double best = 0;
+    for (int k = 0; k < 3; ++k) {
+        const Tile& t = kTiles[k];
+        const double np = a.pt ? (double)((a.P + t.p - 1) / t.p) * a.E
+                               : a.offs ? (double)a.P / t.p + 0.5 * busy : (double)((a.P + t.p - 1) / t.p);
+        const double n = np * (double)((a.Q + t.q - 1) / t.q), slots = (double)kCUs * t.per_cu;
+        const double rounds = n <= slots ? 1 : n / slots + 0.5;
+        const double cost = rounds * t.per_cu * t.q * t.p / t.rate;
+        if (k == 0 || cost < best) {
+            best = cost;
+            p.size = k;
+            const int64_t stages = (a.C + (a.mode == ssg::MM_MX4 ? 255 : 63)) / (a.mode == ssg::MM_MX4 ? 256 : 64);
+            p.splits = a.pt ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({8, (int64_t)(slots / n), stages / 4}));
+        }
+    }
+    int64_t at = 0;
+    auto take = [&](int64_t n) {
+        const int64_t r = at;
+        at += up(n, 256);
+        return r;
+    };
+    const int64_t qb = q_bytes(a), pb = p_bytes(a), nb = blocks(a.C);
+    if (qb % 16 || !al(a.q, 16) || a.ldq % 16 || a.strideq % 16) {
+        p.copy_q = true;
+        p.ldq = up(qb, 16);
+        p.at_q = take(q_mats(a) * q_rows(a) * p.ldq);
+    }
+    if (pb % 16 || !al(a.p, 16) || a.ldp % 16) {
+        p.copy_p = true;
+        p.ldp = up(pb, 16);
+        p.at_p = take(p_rows(a) * p.ldp);
+    }
+    if (a.mode != ssg::MM_16 && (nb % 4 || !al(a.qs, 4) || a.ldqs % 4 || a.strideqs % 4)) {
+        p.copy_qs = true;
+        p.lds_q = up(nb, 16);
+        p.at_qs = take(q_mats(a) * a.Q * p.lds_q);
+    }
+    if (a.mode == ssg::MM_MX4 && (nb % 4 || !al(a.ps, 4) || a.ldps % 4)) {
+        p.copy_ps = true;
+        p.lds_p = up(nb, 16);
+        p.at_ps = take(a.P * p.lds_p);
+    }
+    if (p.splits > 1) p.at_part = take((int64_t)p.splits * a.P * a.Q * 4);
+    p.bytes = (size_t)at;
+    return p;
+}
+
+hipError_t repack(const uint8_t* src, int64_t mats, int64_t stride, int64_t rows, int64_t n, int64_t ld, uint8_t* dst,
+                  int64_t ldd, int fill, hipStream_t s) {
+    if (stride == rows * ld || mats == 1) return ssg::launch_mm_repack(src, mats * rows, n, ld, dst, ldd, fill, s);
+    for (int64_t e = 0; e < mats; ++e) {
+        const hipError_t r = ssg::launch_mm_repack(src + e * stride, rows, n, ld, dst + e * rows * ldd, ldd, fill, s);
+        if (r != hipSuccess) return r;
+    }
+    return hipSuccess;
+}
+
+int run(MmArgs a, void* ws, size_t ws_bytes, hipStream_t s) {
+    if (a.P == 0 || a.Q == 0 || (a.pt && a.E == 0)) return SSG_OK;
+    const Plan p = plan(a);
+    if (p.bytes > 0) {
+        if (!ws || ws_bytes < p.bytes)
+            return fail(SSG_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws ? ws_bytes : (size_t)0, p.bytes);
+        if (!al(ws, 16)) return fail(SSG_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+    }
+    if (p.skinny) return hip_status(ssg::launch_mm_skinny(a, p.rt, p.nt, s), "kernel launch");
+    uint8_t* const w = (uint8_t*)ws;
+    hipError_t e = hipSuccess;
+    if (p.copy_q) {
+        e = repack(a.q, q_mats(a), a.strideq, q_rows(a), q_bytes(a), a.ldq, w + p.at_q, p.ldq, 0, s);
+        a.q = w + p.at_q;
+        a.ldq = p.ldq;
+        a.strideq = q_rows(a) * p.ldq;
+    }
+    if (p.copy_p && e == hipSuccess) {
+        e = repack(a.p, 1, 0, p_rows(a), p_bytes(a), a.ldp, w + p.at_p, p.ldp, 0, s);
+        a.p = w + p.at_p;
+        a.ldp = p.ldp;
+    }
+    // scales past the row's blocks: 1.0, for elements that are zero
+    if (p.copy_qs && e == hipSuccess) {
+        e = repack(a.qs, q_mats(a), a.strideqs, a.Q, blocks(a.C), a.ldqs, w + p.at_qs, p.lds_q, 127, s);
+        a.qs = w + p.at_qs;
+        a.ldqs = p.lds_q;
+        a.strideqs = a.Q * p.lds_q;
+    }
+    if (p.copy_ps && e == hipSuccess) {
+        e = repack(a.ps, 1, 0, a.P, blocks(a.C), a.ldps, w + p.at_ps, p.lds_p, 127, s);
+        a.ps = w + p.at_ps;
+        a.ldps = p.lds_p;
+    }
+    a.splits = p.splits;
+    if (p.splits > 1) a.part = (float*)(w + p.at_part);
+    if (e == hipSuccess) e = ssg::launch_mm_tiles(a, p.size, s);
+    if (e == hipSuccess && p.splits > 1) e = ssg::launch_mm_reduce(a, s);
+    return hip_status(e, "kernel launch");
+}
+
+// ------------------------------------------------------------------ checks
+
+int check_sizes(int64_t E, int64_t M, int64_t N, int64_t K) {
+    if (E < 0 || M < 0 || N < 0 || K < 0)
+        return fail(SSG_ERR_SHAPE, "negative size E=%lld M=%lld N=%lld K=%lld", (ll)E, (ll)M, (ll)N, (ll)K);
+    if (E >= (1 << 20) || M >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
+        return fail(SSG_ERR_SHAPE, "size too large: E=%lld M=%lld N=%lld K=%lld", (ll)E, (ll)M, (ll)N, (ll)K);
+    return SSG_OK;
+}
+
+// A matrix of `rows` rows of `need` elements, `ld` apart; a tile's 256 rows have
+// to be addressable with 31 bits.
+int check_mat(const char* name, const void* p, int64_t rows, int64_t need, int64_t ld, int64_t es) {
+    if (rows > 0 && need > 0 && !p) return fail(SSG_ERR_NULL, "%s is NULL", name);
+    if (ld < need) return fail(SSG_ERR_STRIDE, "row stride of %s: %lld < %lld", name, (ll)ld, (ll)need);
+    if (ld * es >= (int64_t)1 << 22) return fail(SSG_ERR_STRIDE, "rows of %s are 2^22 bytes apart or more", name);
+    return SSG_OK;
+}
+
+int check_out(int x, int y) {
+    const bool ok = x == SSG_MX4 ? y == SSG_F32 || float16_type(y) : float16_type(x) && (y == SSG_F32 || y == x);
+    return ok ? SSG_OK : fail(SSG_ERR_DTYPE, "unsupported (input, output) types (%d, %d)", x, y);
+}
+
+int check_y(const char* name, const void* y, int64_t rows, int64_t cols, int64_t ld) {
+    if (rows > 0 && cols > 0 && !y) return fail(SSG_ERR_NULL, "%s is NULL", name);
+    if (ld < cols) return fail(SSG_ERR_STRIDE, "row stride of %s: %lld < %lld", name, (ll)ld, (ll)cols);
+    return SSG_OK;
+}
+
+// X [N, K] (16-bit or mx4) against mx4 weights [E][M, K].
+int mx4_args(int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const uint8_t* xs,
+             int64_t ldxs, const uint8_t* W, int64_t ldw, int64_t stridew, const uint8_t* S, int64_t lds,
+             int64_t strides, const int32_t* offs, bool grouped, MmArgs* out) {
+    if (x != SSG_MX4 && !float16_type(x)) return fail(SSG_ERR_DTYPE, "activations of type %d", x);
+    int rc = check_sizes(E, M, N, K);
+    if (rc) return rc;
+    const int64_t nb = blocks(K);
+    if ((rc = check_mat("X", X, N, x == SSG_MX4 ? nb * 16 : K, ldx, x == SSG_MX4 ? 1 : 2))) return rc;
+    if (x == SSG_MX4) {
+        if ((rc = check_mat("xscales", xs, N, nb, ldxs, 1))) return rc;
+    } else if (xs) {
+        return fail(SSG_ERR_FORMAT, "xscales with 16-bit activations");
+    }
+    if ((rc = check_mat("W", W, E * M, nb * 16, ldw, 1))) return rc;
+    if ((rc = check_mat("scales", S, E * M, nb, lds, 1))) return rc;
+    if (grouped && !offs) return fail(SSG_ERR_NULL, "offs is NULL");
+    MmArgs a{};
+    a.mode = x == SSG_MX4 ? ssg::MM_MX4 : ssg::MM_W4;
+    a.dt = to_dt(x);
+    a.Q = M; a.P = N; a.C = K;
+    a.q = W; a.ldq = ldw; a.strideq = stridew;
+    a.qs = S; a.ldqs = lds; a.strideqs = strides;
+    a.p = (const uint8_t*)X; a.ldp = x == SSG_MX4 ? ldx : ldx * 2;
+    a.ps = xs; a.ldps = ldxs;
+    a.E = E; a.offs = grouped ? offs : nullptr;
+    a.splits = 1;
+    *out = a;
+    return SSG_OK;
+}
+
+enum Kind { FORWARD, DX, DW };
+
+// The 16-bit products; A and B are (X, W), (dY, W) or (dY, X).
+int grouped_args(Kind kind, int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+                 const void* B, int64_t ldb, int64_t strideb, const int32_t* offs, MmArgs* out) {
+    if (!float16_type(x)) return fail(SSG_ERR_DTYPE, "operands of type %d", x);
+    int rc = check_sizes(E, M, N, K);
+    if (rc) return rc;
+    if ((rc = check_mat(kind == FORWARD ? "X" : "dY", A, N, kind == FORWARD ? K : M, lda, 2))) return rc;
+    if ((rc = check_mat(kind == DW ? "X" : "W", B, kind == DW ? N : E * M, K, ldb, 2))) return rc;
+    if (!offs) return fail(SSG_ERR_NULL, "offs is NULL");
+    MmArgs a{};
+    a.mode = ssg::MM_16;
+    a.dt = to_dt(x);
+    a.qt = kind != FORWARD;
+    a.pt = kind == DW;
+    a.Q = kind == FORWARD ? M : K;
+    a.P = kind == DW ? M : N;
+    a.C = kind == FORWARD ? K : kind == DX ? M : N;
+    a.q = (const uint8_t*)B; a.ldq = ldb * 2; a.strideq = kind == DW ? 0 : strideb * 2;
+    a.p = (const uint8_t*)A; a.ldp = lda * 2;
+    a.E = E; a.offs = offs;
+    a.splits = 1;
+    *out = a;
+    return SSG_OK;
+}
+
+size_t bytes_of(int rc, const MmArgs& a) {
+    if (rc || a.P == 0 || a.Q == 0) return 0;
+    return plan(a).bytes;
+}
+
+int check_mx4(int dtype, int64_t R, int64_t K, const void* A, int64_t lda, const void* elems, int64_t lde,
+              const void* scales, int64_t lds) {
+    if (dtype != SSG_F32 && !float16_type(dtype)) return fail(SSG_ERR_DTYPE, "element type %d", dtype);
+    if (R < 0 || K < 0 || K >= kMaxDim) return fail(SSG_ERR_SHAPE, "size R=%lld K=%lld", (ll)R, (ll)K);
+    if (R > 0 && K > 0 && (!A || !elems || !scales)) return fail(SSG_ERR_NULL, "a pointer is NULL");
+    if (lda < K) return fail(SSG_ERR_STRIDE, "row stride %lld < K=%lld", (ll)lda, (ll)K);
+    if (lde < blocks(K) * 16) return fail(SSG_ERR_STRIDE, "element row stride %lld < %lld", (ll)lde, (ll)blocks(K) * 16);
+    if (lds < blocks(K)) return fail(SSG_ERR_STRIDE, "scale row stride %lld < %lld", (ll)lds, (ll)blocks(K));
+    return SSG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t ssg_mx4_elem_cols(int64_t K) { return blocks(K) * 16; }
+int64_t ssg_mx4_scale_cols(int64_t K) { return blocks(K); }
+
+int ssg_mx4_quantize(int dtype, int64_t R, int64_t K, const void* A, int64_t lda, uint8_t* elems, int64_t lde,
+                     uint8_t* scales, int64_t lds, void* stream) {
+    const int rc = check_mx4(dtype, R, K, A, lda, elems, lde, scales, lds);
+    if (rc || R == 0 || K == 0) return rc;
+    return hip_status(ssg::launch_mx4_quantize(dtype == SSG_F32 ? 2 : dtype == SSG_F16 ? 0 : 1, R, K, A, lda, elems,
+                                               lde, scales, lds, (hipStream_t)stream), "kernel launch");
+}
+
+int ssg_mx4_dequantize(int dtype, int64_t R, int64_t K, const uint8_t* elems, int64_t lde, const uint8_t* scales,
+                       int64_t lds, void* D, int64_t ldd, void* stream) {
+    const int rc = check_mx4(dtype, R, K, D, ldd, elems, lde, scales, lds);
+    if (rc || R == 0 || K == 0) return rc;
+    return hip_status(ssg::launch_mx4_dequantize(dtype == SSG_F32 ? 2 : dtype == SSG_F16 ? 0 : 1, R, K, elems, lde,
+                                                 scales, lds, D, ldd, (hipStream_t)stream), "kernel launch");
+}
+
+size_t ssg_mm_mx4_workspace_bytes(int x, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+                                  const uint8_t* xscales, int64_t ldxs, const uint8_t* W, int64_t ldw,
+                                  const uint8_t* scales, int64_t lds) {
+    MmArgs a{};
+    return bytes_of(mx4_args(x, 1, M, N, K, X, ldx, xscales, ldxs, W, ldw, 0, scales, lds, 0, nullptr, false, &a), a);
+}
+
+int ssg_mm_mx4(int x, int y, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const uint8_t* xscales,
+               int64_t ldxs, const uint8_t* W, int64_t ldw, const uint8_t* scales, int64_t lds, void* Y, int64_t ldy,
+               void* ws, size_t ws_bytes, void* stream) {
+    MmArgs a{};
+    int rc = mx4_args(x, 1, M, N, K, X, ldx, xscales, ldxs, W, ldw, 0, scales, lds, 0, nullptr, false, &a);
+    if (rc || (rc = check_out(x, y)) || (rc = check_y("Y", Y, N, M, ldy))) return rc;
+    a.out = to_out(y);
+    a.y = Y;
+    a.ldy = ldy;
+    return run(a, ws, ws_bytes, (hipStream_t)stream);
+}
+
+size_t ssg_grouped_mm_mx4_workspace_bytes(int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* X,
+                                          int64_t ldx, const uint8_t* xscales, int64_t ldxs, const uint8_t* W,
+                                          int64_t ldw, int64_t stridew, const uint8_t* scales, int64_t lds,
+                                          int64_t strides, const int32_t* offs) {
+    MmArgs a{};
+    return bytes_of(mx4_args(x, E, M, N, K, X, ldx, xscales, ldxs, W, ldw, stridew, scales, lds, strides, offs, true, &a), a);
+}
+
+int ssg_grouped_mm_mx4(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+                       const uint8_t* xscales, int64_t ldxs, const uint8_t* W, int64_t ldw, int64_t stridew,
+                       const uint8_t* scales, int64_t lds, int64_t strides, const int32_t* offs, void* Y, int64_t ldy,
+                       void* ws, size_t ws_bytes, void* stream) {
+    MmArgs a{};
+    int rc = mx4_args(x, E, M, N, K, X, ldx, xscales, ldxs, W, ldw, stridew, scales, lds, strides, offs, true, &a);
+    if (rc || (rc = check_out(x, y)) || (rc = check_y("Y", Y, N, M, ldy))) return rc;
+    a.out = to_out(y);
+    a.y = Y;
+    a.ldy = ldy;
+    return run(a, ws, ws_bytes, (hipStream_t)stream);
+}
+
+size_t ssg_grouped_mm_workspace_bytes(int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+                                      const void* W, int64_t ldw, int64_t stridew, const int32_t* offs) {
+    MmArgs a{};
+    return bytes_of(grouped_args(FORWARD, x, E, M, N, K, X, ldx, W, ldw, stridew, offs, &a), a);
+}
+
+int ssg_grouped_mm(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const void* W,
+                   int64_t ldw, int64_t stridew, const int32_t* offs, void* Y, int64_t ldy, void* ws, size_t ws_bytes,
+                   void* stream) {
+    MmArgs a{};
+    int rc = grouped_args(FORWARD, x, E, M, N, K, X, ldx, W, ldw, stridew, offs, &a);
+    if (rc || (rc = check_out(x, y)) || (rc = check_y("Y", Y, N, M, ldy))) return rc;
+    a.out = to_out(y);
+    a.y = Y;
+    a.ldy = ldy;
+    return run(a, ws, ws_bytes, (hipStream_t)stream);
+}
+
+size_t ssg_grouped_mm_dx_workspace_bytes(int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* dY,
+                                         int64_t lddy, const void* W, int64_t ldw, int64_t stridew,
+                                         const int32_t* offs) {
+    MmArgs a{};
+    return bytes_of(grouped_args(DX, x, E, M, N, K, dY, lddy, W, ldw, stridew, offs, &a), a);
+}
+
+int ssg_grouped_mm_dx(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy,
+                      const void* W, int64_t ldw, int64_t stridew, const int32_t* offs, void* dX, int64_t lddx,
+                      void* ws, size_t ws_bytes, void* stream) {
+    MmArgs a{};
+    int rc = grouped_args(DX, x, E, M, N, K, dY, lddy, W, ldw, stridew, offs, &a);
+    if (rc || (rc = check_out(x, y)) || (rc = check_y("dX", dX, N, K, lddx))) return rc;
+    a.out = to_out(y);
+    a.y = dX;
+    a.ldy = lddx;
+    return run(a, ws, ws_bytes, (hipStream_t)stream);
+}
+
+size_t ssg_grouped_mm_dw_workspace_bytes(int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* dY,
+                                         int64_t lddy, const void* X, int64_t ldx, const int32_t* offs) {
+    MmArgs a{};
+    return bytes_of(grouped_args(DW, x, E, M, N, K, dY, lddy, X, ldx, 0, offs, &a), a);
+}
+
+int ssg_grouped_mm_dw(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy,
+                      const void* X, int64_t ldx, const int32_t* offs, void* dW, int64_t lddw, int64_t stridedw,
+                      void* ws, size_t ws_bytes, void* stream) {
+    MmArgs a{};
+    int rc = grouped_args(DW, x, E, M, N, K, dY, lddy, X, ldx, 0, offs, &a);
+    if (rc || (rc = check_out(x, y)) || (rc = check_y("dW", dW, E * M, K, lddw))) return rc;
+    a.out = to_out(y);
+    a.y = dW;
+    a.ldy = lddw;
+    a.stridey = stridedw;
+    return run(a, ws, ws_bytes, (hipStream_t)stream);
+}
+
+}  // extern "C"

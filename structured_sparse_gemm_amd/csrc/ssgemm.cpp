@@ -13,6 +13,7 @@
 #include <mutex>
 #include <string>
 
+#include "ssg_abi.hpp"
 #include "ssg_kernels.hpp"
 
 namespace {
@@ -185,6 +186,12 @@ ssg::SpmmArgs make_args(int ab, int64_t M, int64_t N, int64_t K, const void* val
 }
 
 }  // namespace
+
+namespace ssg {
+
+int abi_fail(int status, const char* text) { return fail(status, "%s", text); }
+
+}  // namespace ssg
 
 extern "C" {
 
