@@ -32,7 +32,7 @@ int hip_status(hipError_t e, const char* what) {
 
 typedef long long ll;
 
-constexpr int64_t kMaxDim = (int64_t)1 << 31;
+constexpr int64_t kMaxDim = (int64_t)1 << 29;   // rows: three scale planes are addressed with 31 bits
 constexpr int kCUs = 256;
 
 bool al(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -46,21 +46,13 @@ int to_out(int dt) { return dt == SSG_F32 ? ssg::OUT_F32 : dt == SSG_F16 ? ssg::
 
 // ------------------------------------------------------------------ the choice of kernel
 
-// Tile sizes of the tiled kernel, its workgroups a CU holds at once, and the
-// matrix rate of a full chip of them relative to the largest tile.
-struct Tile {
-    int q, p, per_cu;
-    double rate;
-};
-constexpr Tile kTiles[3] = {{256, 256, 1, 1.0}, {128, 128, 2, 0.7}, {128, 64, 3, 0.5}};
-
 struct Plan {
     bool skinny;
     int rt, nt;                        // skinny: 16-row groups of weights and tokens
     int size, splits;                  // tiles
-    bool copy_q, copy_p, copy_qs, copy_ps;
+    bool copy_q, copy_p;
     int64_t at_q, at_p, at_qs, at_ps, at_part;   // workspace offsets
-    int64_t ldq, ldp, lds_q, lds_p;    // strides of the copies
+    int64_t ldq, ldp, plane_q, plane_p;          // strides of the copies and the scale planes
     size_t bytes;
 };
 
@@ -92,17 +84,17 @@ Plan plan(const MmArgs& a) {
     // The tile: rounds of a full chip times what a round of that tile takes
     double best = 0;
     for (int k = 0; k < 3; ++k) {
-        const Tile& t = kTiles[k];
+        const ssg::MmTileSize& t = ssg::kMmTileSizes[k];
         const double np = a.pt ? (double)((a.P + t.p - 1) / t.p) * a.E
                                : a.offs ? (double)a.P / t.p + 0.5 * busy : (double)((a.P + t.p - 1) / t.p);
         const double n = np * (double)((a.Q + t.q - 1) / t.q), slots = (double)kCUs * t.per_cu;
-        const double rounds = n <= slots ? 1 : n / slots + 0.5;
+        const double rounds = n <= slots ? 1 : n / slots + (k == 0 ? 0.25 : 0.5);
         const double cost = rounds * t.per_cu * t.q * t.p / t.rate;
         if (k == 0 || cost < best) {
             best = cost;
             p.size = k;
-            const int64_t stages = (a.C + (a.mode == ssg::MM_MX4 ? 255 : 63)) / (a.mode == ssg::MM_MX4 ? 256 : 64);
-            p.splits = a.pt ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({8, (int64_t)(slots / n), stages / 4}));
+            const int64_t stages = (a.C + (a.mode == ssg::MM_MX4 ? 127 : 31)) / (a.mode == ssg::MM_MX4 ? 128 : 32);
+            p.splits = a.pt || k == 0 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({8, (int64_t)(slots / n), stages / 8}));
         }
     }
     int64_t at = 0;
@@ -122,15 +114,14 @@ Plan plan(const MmArgs& a) {
         p.ldp = up(pb, 16);
         p.at_p = take(p_rows(a) * p.ldp);
     }
-    if (a.mode != ssg::MM_16 && (nb % 4 || !al(a.qs, 4) || a.ldqs % 4 || a.strideqs % 4)) {
-        p.copy_qs = true;
-        p.lds_q = up(nb, 16);
-        p.at_qs = take(q_mats(a) * a.Q * p.lds_q);
+    // scale planes, padded so that the last tile's pieces stay inside
+    if (a.mode != ssg::MM_16) {
+        p.plane_q = up(a.Q, 256);
+        p.at_qs = take(a.E * up(nb, 4) * p.plane_q);
     }
-    if (a.mode == ssg::MM_MX4 && (nb % 4 || !al(a.ps, 4) || a.ldps % 4)) {
-        p.copy_ps = true;
-        p.lds_p = up(nb, 16);
-        p.at_ps = take(a.P * p.lds_p);
+    if (a.mode == ssg::MM_MX4) {
+        p.plane_p = up(a.P, 16) + 256;
+        p.at_ps = take(up(nb, 4) * p.plane_p);
     }
     if (p.splits > 1) p.at_part = take((int64_t)p.splits * a.P * a.Q * 4);
     p.bytes = (size_t)at;
@@ -138,10 +129,10 @@ Plan plan(const MmArgs& a) {
 }
 
 hipError_t repack(const uint8_t* src, int64_t mats, int64_t stride, int64_t rows, int64_t n, int64_t ld, uint8_t* dst,
-                  int64_t ldd, int fill, hipStream_t s) {
-    if (stride == rows * ld || mats == 1) return ssg::launch_mm_repack(src, mats * rows, n, ld, dst, ldd, fill, s);
+                  int64_t ldd, hipStream_t s) {
+    if (stride == rows * ld || mats == 1) return ssg::launch_mm_repack(src, mats * rows, n, ld, dst, ldd, s);
     for (int64_t e = 0; e < mats; ++e) {
-        const hipError_t r = ssg::launch_mm_repack(src + e * stride, rows, n, ld, dst + e * rows * ldd, ldd, fill, s);
+        const hipError_t r = ssg::launch_mm_repack(src + e * stride, rows, n, ld, dst + e * rows * ldd, ldd, s);
         if (r != hipSuccess) return r;
     }
     return hipSuccess;
@@ -159,27 +150,26 @@ int run(MmArgs a, void* ws, size_t ws_bytes, hipStream_t s) {
     uint8_t* const w = (uint8_t*)ws;
     hipError_t e = hipSuccess;
     if (p.copy_q) {
-        e = repack(a.q, q_mats(a), a.strideq, q_rows(a), q_bytes(a), a.ldq, w + p.at_q, p.ldq, 0, s);
+        e = repack(a.q, q_mats(a), a.strideq, q_rows(a), q_bytes(a), a.ldq, w + p.at_q, p.ldq, s);
         a.q = w + p.at_q;
         a.ldq = p.ldq;
         a.strideq = q_rows(a) * p.ldq;
     }
     if (p.copy_p && e == hipSuccess) {
-        e = repack(a.p, 1, 0, p_rows(a), p_bytes(a), a.ldp, w + p.at_p, p.ldp, 0, s);
+        e = repack(a.p, 1, 0, p_rows(a), p_bytes(a), a.ldp, w + p.at_p, p.ldp, s);
         a.p = w + p.at_p;
         a.ldp = p.ldp;
     }
-    // scales past the row's blocks: 1.0, for elements that are zero
-    if (p.copy_qs && e == hipSuccess) {
-        e = repack(a.qs, q_mats(a), a.strideqs, a.Q, blocks(a.C), a.ldqs, w + p.at_qs, p.lds_q, 127, s);
+    if (a.mode != ssg::MM_16 && e == hipSuccess) {
+        e = ssg::launch_mm_planes(a.qs, a.E, a.strideqs, a.Q, blocks(a.C), a.ldqs, w + p.at_qs, p.plane_q, s);
         a.qs = w + p.at_qs;
-        a.ldqs = p.lds_q;
-        a.strideqs = a.Q * p.lds_q;
+        a.ldqs = p.plane_q;
+        a.strideqs = up(blocks(a.C), 4) * p.plane_q;
     }
-    if (p.copy_ps && e == hipSuccess) {
-        e = repack(a.ps, 1, 0, a.P, blocks(a.C), a.ldps, w + p.at_ps, p.lds_p, 127, s);
+    if (a.mode == ssg::MM_MX4 && e == hipSuccess) {
+        e = ssg::launch_mm_planes(a.ps, 1, 0, a.P, blocks(a.C), a.ldps, w + p.at_ps, p.plane_p, s);
         a.ps = w + p.at_ps;
-        a.ldps = p.lds_p;
+        a.ldps = p.plane_p;
     }
     a.splits = p.splits;
     if (p.splits > 1) a.part = (float*)(w + p.at_part);

@@ -43,12 +43,22 @@ struct MmArgs {
 // end in a partial one.
 int64_t mm_tile_bound(const MmArgs& a, int T);
 hipError_t launch_mm_skinny(const MmArgs& a, int rt, int nt, hipStream_t s);
-// TQ x TP tiles: size 0 is 256 x 256, 1 is 128 x 128, 2 is 128 x 64.
+// Tile sizes of the tiled kernels, the workgroups a CU holds at once, and the
+// matrix rate of a chip full of them relative to the largest.
+struct MmTileSize {
+    int q, p, per_cu;
+    double rate;
+};
+constexpr MmTileSize kMmTileSizes[3] = {{256, 256, 1, 1.0}, {128, 128, 2, 0.7}, {128, 64, 3, 0.5}};
+// mx4 operands of the tiled kernels have their scales in planes
+// [expert][ceil(blocks / 4)][4][rows], ldqs / ldps bytes a plane.
+hipError_t launch_mm_planes(const uint8_t* src, int64_t mats, int64_t stride, int64_t rows, int64_t nb, int64_t ld,
+                            uint8_t* dst, int64_t plane, hipStream_t s);
 hipError_t launch_mm_tiles(const MmArgs& a, int size, hipStream_t s);
 // Y = the sum of the partials in split order, in the output type.
 hipError_t launch_mm_reduce(const MmArgs& a, hipStream_t s);
-// Rows of n bytes to rows of ldd bytes (a multiple of 16), `fill` past n.
-hipError_t launch_mm_repack(const void* src, int64_t rows, int64_t n, int64_t lds, void* dst, int64_t ldd, int fill,
+// Rows of n bytes to rows of ldd bytes (a multiple of 16), zeros past n.
+hipError_t launch_mm_repack(const void* src, int64_t rows, int64_t n, int64_t lds, void* dst, int64_t ldd,
                             hipStream_t s);
 hipError_t launch_mx4_quantize(int src, int64_t R, int64_t K, const void* A, int64_t lda, void* elems, int64_t lde,
                                void* scales, int64_t lds, hipStream_t s);
@@ -64,8 +74,14 @@ hipError_t launch_mx4_dequantize(int dst, int64_t R, int64_t K, const void* elem
 // ---------------------------------------------------------------------------
 struct MmTile {
     int e;                             // expert, or -1: rows that get zeros
-    int64_t r0, r1;                    // rows of this tile
+    int64_t r0, v0, r1;                // the tile begins at r0, its rows are v0 .. r1 - 1
 };
+
+// Tiles of an mx4 operand begin at multiples of 16 rows, where the pieces of
+// its scale planes are aligned; the rows before the segment are left out.
+__device__ __forceinline__ int64_t mm_align(const MmArgs& a, int64_t row) {
+    return a.mode == MM_MX4 ? row & ~(int64_t)15 : row;
+}
 
 __device__ __forceinline__ void mm_segment(const MmArgs& a, int64_t s, int64_t* lo, int64_t* hi) {
     auto at = [&](int64_t i) -> int64_t {
@@ -98,7 +114,7 @@ __device__ __forceinline__ int mm_count_tiles(const MmArgs& a, int T) {
     for (int64_t s0 = 0; s0 < a.E + 2; s0 += 64) {
         int64_t lo, hi;
         mm_segment(a, s0 + lane, &lo, &hi);
-        total += __builtin_amdgcn_readlane(wave_scan(hi > lo ? (int)((hi - lo + T - 1) / T) : 0), 63);
+        total += __builtin_amdgcn_readlane(wave_scan(hi > lo ? (int)((hi - mm_align(a, lo) + T - 1) / T) : 0), 63);
     }
     return total;
 }
@@ -107,7 +123,7 @@ __device__ __forceinline__ int mm_count_tiles(const MmArgs& a, int T) {
 __device__ __forceinline__ bool mm_find_tile(const MmArgs& a, int T, int t, MmTile* out) {
     if (!a.offs) {
         out->e = 0;
-        out->r0 = (int64_t)t * T;
+        out->r0 = out->v0 = (int64_t)t * T;
         out->r1 = out->r0 + T < a.P ? out->r0 + T : a.P;
         return out->r0 < a.P;
     }
@@ -116,7 +132,7 @@ __device__ __forceinline__ bool mm_find_tile(const MmArgs& a, int T, int t, MmTi
     for (int64_t s0 = 0; s0 < a.E + 2; s0 += 64) {
         int64_t lo, hi;
         mm_segment(a, s0 + lane, &lo, &hi);
-        const int n = hi > lo ? (int)((hi - lo + T - 1) / T) : 0;
+        const int n = hi > lo ? (int)((hi - mm_align(a, lo) + T - 1) / T) : 0;
         const int inc = wave_scan(n);
         const uint64_t hit = __ballot(t < before + inc);
         if (hit) {
@@ -125,7 +141,8 @@ __device__ __forceinline__ bool mm_find_tile(const MmArgs& a, int T, int t, MmTi
             const int slo = __builtin_amdgcn_readlane((int)lo, l), shi = __builtin_amdgcn_readlane((int)hi, l);
             const int64_t s = s0 + l;
             out->e = s == 0 || s == a.E + 1 ? -1 : (int)(s - 1);
-            out->r0 = slo + (int64_t)(t - first) * T;
+            out->r0 = mm_align(a, slo) + (int64_t)(t - first) * T;
+            out->v0 = out->r0 > slo ? out->r0 : slo;
             out->r1 = out->r0 + T < shi ? out->r0 + T : shi;
             return true;
         }

@@ -1,5 +1,6 @@
 // mm_prep.hip -- the passes beside the tiled products: the sum of a split
-// contraction's partials, and operands repacked into 16-byte aligned rows.
+// contraction's partials, operands repacked into 16-byte aligned rows, and
+// scales brought into planes.
 #include <algorithm>
 
 #include "mm_args.hpp"
@@ -34,7 +35,7 @@ __global__ void __launch_bounds__(kThreads) k_mm_reduce(MmArgs a) {
 
 // One 16-byte chunk a thread.
 __global__ void __launch_bounds__(kThreads) k_mm_repack(const uint8_t* src, int64_t rows, int64_t n, int64_t lds,
-                                                        uint8_t* dst, int64_t ldd, int fill) {
+                                                        uint8_t* dst, int64_t ldd) {
     const int64_t cpr = ldd / 16, total = rows * cpr;
     for (int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x; t < total; t += (int64_t)gridDim.x * kThreads) {
         const int64_t r = t / cpr, b = (t - r * cpr) * 16;
@@ -44,9 +45,48 @@ __global__ void __launch_bounds__(kThreads) k_mm_repack(const uint8_t* src, int6
             __builtin_memcpy(v, at, 16);
         } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = b + j < n ? at[j] : (uint8_t)fill;
+            for (int j = 0; j < 16; ++j) v[j] = b + j < n ? at[j] : (uint8_t)0;
         }
         *reinterpret_cast<uint4*>(dst + r * ldd + b) = *reinterpret_cast<uint4*>(v);
+    }
+}
+
+// Scales [rows][nb] to planes [blocks / 4][4][plane]: a thread takes 4 rows by
+// 16 blocks, transposes them in registers, and writes 16 dwords of 4 rows each,
+// consecutive threads consecutive rows.  Rows and blocks past the end get 127
+// (1.0): their elements are zeros.
+__global__ void __launch_bounds__(kThreads) k_mm_planes(const uint8_t* src, int64_t stride, int64_t rows, int64_t nb,
+                                                        int64_t ld, uint8_t* dst, int64_t plane, int64_t planes,
+                                                        int64_t per_mat, int64_t total) {
+    const int64_t r4 = plane / 4;
+    for (int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x; t < total; t += (int64_t)gridDim.x * kThreads) {
+        const int64_t e = t / per_mat, u = t - e * per_mat, c = u / r4, r = (u - c * r4) * 4, b = c * 16;
+        uint32_t v[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint8_t* at = src + e * stride + (r + k) * ld + b;
+            uint4 w = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            if (r + k < rows) {
+                if (b + 16 <= nb) {
+                    __builtin_memcpy(&w, at, 16);
+                } else {
+                    uint8_t x[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[j] = b + j < nb ? at[j] : 127;
+                    __builtin_memcpy(&w, x, 16);
+                }
+            }
+            v[k][0] = w.x; v[k][1] = w.y; v[k][2] = w.z; v[k][3] = w.w;
+        }
+        uint8_t* out = dst + (e * planes + b) * plane + r;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            if (b + j >= planes) break;
+            uint32_t w = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w |= ((v[k][j >> 2] >> (8 * (j & 3))) & 0xFFu) << (8 * k);
+            *reinterpret_cast<uint32_t*>(out + j * plane) = w;
+        }
     }
 }
 
@@ -66,11 +106,20 @@ hipError_t launch_mm_reduce(const MmArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_mm_repack(const void* src, int64_t rows, int64_t n, int64_t lds, void* dst, int64_t ldd, int fill,
+hipError_t launch_mm_repack(const void* src, int64_t rows, int64_t n, int64_t lds, void* dst, int64_t ldd,
                             hipStream_t s) {
     if (rows * ldd == 0) return hipSuccess;
     hipLaunchKernelGGL(k_mm_repack, dim3(grid_of(rows * (ldd / 16))), dim3(kThreads), 0, s, (const uint8_t*)src, rows,
-                       n, lds, (uint8_t*)dst, ldd, fill);
+                       n, lds, (uint8_t*)dst, ldd);
+    return hipGetLastError();
+}
+
+hipError_t launch_mm_planes(const uint8_t* src, int64_t mats, int64_t stride, int64_t rows, int64_t nb, int64_t ld,
+                            uint8_t* dst, int64_t plane, hipStream_t s) {
+    const int64_t planes = (nb + 3) / 4 * 4, per_mat = plane / 4 * ((planes + 15) / 16), total = mats * per_mat;
+    if (total == 0) return hipSuccess;
+    hipLaunchKernelGGL(k_mm_planes, dim3(grid_of(total)), dim3(kThreads), 0, s, src, stride, rows, nb, ld, dst, plane,
+                       planes, per_mat, total);
     return hipGetLastError();
 }
 

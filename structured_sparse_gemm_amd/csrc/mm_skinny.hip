@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) k_mm_skinny(MmArgs a, uint32_t nq) {
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const int64_t row = std::min<int64_t>(tile.r0 + 16 * t + k.i, tile.r1 - 1);
+        const int64_t row = std::max(tile.v0, std::min<int64_t>(tile.r0 + 16 * t + k.i, tile.r1 - 1));
         k.prow[t] = a.p + row * a.ldp;
         if constexpr (MODE == MM_MX4) k.psrow[t] = a.ps + row * a.ldps;
     }
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) k_mm_skinny(MmArgs a, uint32_t nq) {
         for (int w = 1; w < kWaves; ++w) v += red[w][o];
         const int l = o & 63, r = (o >> 6) / NT, t = (o >> 6) % NT;
         const int64_t p = tile.r0 + 16 * t + (l & 15), q = q0 + 16 * r + 4 * (l >> 4);
-        if (p < tile.r1 && q < a.Q) {
+        if (p >= tile.v0 && p < tile.r1 && q < a.Q) {
             const int64_t left = a.Q - q;
             const bool vec = a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
             mm_store4(a.y, a.out, p * a.ldy + q, left < 4 ? (int)left : 4, vec, v);
@@ -265,7 +265,9 @@ hipError_t pick(const MmArgs& a, int rt, int nt, hipStream_t s) {
 }  // namespace
 
 int64_t mm_tile_bound(const MmArgs& a, int T) {
-    return a.offs ? a.P / T + a.E + 2 : (a.P + T - 1) / T;
+    if (!a.offs) return (a.P + T - 1) / T;
+    // a segment's partial tile, and the rows an mx4 tile begins before it
+    return (a.P + (a.mode == MM_MX4 ? 15 * (a.E + 2) : 0)) / T + a.E + 2;
 }
 
 hipError_t launch_mm_skinny(const MmArgs& a, int rt, int nt, hipStream_t s) {

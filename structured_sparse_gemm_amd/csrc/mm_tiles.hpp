@@ -3,35 +3,45 @@
 // 16-bit activations; dense or grouped by expert.
 //
 // Bound by the matrix cores.  A workgroup owns a TQ x TP tile of one expert's
-// Y; both operands stream through LDS in stages of 128 bytes per row (64
-// 16-bit elements, 256 mx4 elements), two stages, brought by direct-to-LDS
-// loads whose out-of-range offsets read as zero, so ragged edges need no
-// branch.  Every wave multiplies 16-row fragments out of registers while the
-// reads of the next half-stage are in flight; one barrier a stage.
+// Y; both operands stream through LDS in stages of 64 bytes per row (32 16-bit
+// elements, 128 mx4 elements), brought by direct-to-LDS loads whose
+// out-of-range offsets read as zero, so ragged edges need no branch.  A wave
+// reads the 16-row fragments of stage i + 1 into registers while it multiplies
+// those of stage i, so stage i's slot is free as soon as the barrier that opens
+// stage i has passed: with a ring of kRing = 4 slots the loads run up to four
+// stages ahead, which covers their latency (two whole stages of 128 bytes a
+// row, the same LDS, left it exposed: bf16 8 x 4096 x 4096 with 8192 tokens
+// took 345 us).
 //
-// * Operand stored along the contraction ([row][c]): 16-byte chunk c of tile
-//   row r sits at chunk c ^ ((r / 2) % 8) of the row's 128 bytes, so the 16
-//   lanes an LDS cycle serves (16 rows, one chunk) meet 16 different 16-byte
-//   bank groups.
+// * Operand stored along the contraction ([row][c]): of a group of 64 tile
+//   rows, row 4 i + f is row i of fragment f.  A lane then holds 16
+//   consecutive columns of Y (whole 16-byte stores), and the scale bytes of
+//   its four fragments are one dword.  16-byte chunk c of fragment row i sits
+//   at chunk c ^ mm_swz(i) of its 64 bytes; the permutation is the fastest of
+//   all parity pairs of row bits under the LDS read probe (as fast as a
+//   lane-contiguous read).
 // * Operand stored across it ([c][row], the weights of the input gradient and
-//   both operands of the weight gradient): 64 contraction rows of T columns;
+//   both operands of the weight gradient): 32 contraction rows of T columns;
 //   the transposing reads (ds_read_b64_tr_b16) hand each lane 4 consecutive
 //   contraction elements of its column.  A read touches 32 bytes of 8
 //   contraction rows per cycle; 32-byte unit u of row c sits at unit
 //   u ^ (c % 4 + 4 * ((c / 8) % 2)), which spreads those 8 over all banks.
-// * mx4 x mx4: the lane group g of a fragment takes the 32-element blocks
-//   2g and 2g + 1 of a stage, one per half-stage, so that its two scale bytes
-//   are one 16-bit read and the MFMA's byte select picks between them.
-// * mx4 x 16-bit: a stage's 32 weight bytes a row stay 4-bit in LDS; a wave
-//   widens its fragment (4 conversions) on the way into the MFMA, scaled
-//   where the scale is in the type's safe range, else unscaled with the
-//   product's fp32 sum scaled instead.
+// * mx4 x mx4: lane group g of a fragment takes block g of the stage; the
+//   scales were brought into planes [stage][g][row] beforehand, so a stage's
+//   are 1 KiB an operand in contiguous pieces (read from their rows they are
+//   four bytes a row and triple the number of memory requests: 357 us against
+//   the products' own time at 28672 x 8192 x 2048).
+// * mx4 x 16-bit: weights come 64 bytes a row (128 elements) every fourth
+//   stage and stay 4-bit in LDS; a wave widens its fragment (4 conversions) on
+//   the way into the MFMA.
 //
 // Workgroups are dealt round-robin to the 8 XCDs; tile numbers are dealt so
 // that each XCD gets a contiguous range, walked 8 row tiles at a time, which
 // keeps the operand panels of the tiles in flight in its L2.  The number of
 // tiles of a grouped product is known on the device only: the grid covers the
-// worst case and surplus workgroups leave after counting.
+// worst case and surplus workgroups leave after counting.  The tiles of the
+// last, partly filled round of the chip's 256 CUs are cut in two or in four
+// where that many fit in one round.
 #pragma once
 
 #include <type_traits>
@@ -41,26 +51,10 @@
 namespace ssg {
 
 constexpr int kMmGroupP = 8;           // row tiles walked together
+constexpr int kMmCUs = 256;
+constexpr int kRing = 4;
 
-template <int MODE, int TQ, int TP, int WQ, int WP>
-struct MmLay {
-    static constexpr int NW = WQ * WP;
-    static constexpr int FQ = TQ / WQ / 16, FP = TP / WP / 16;       // fragments per wave
-    static constexpr int CE = MODE == MM_MX4 ? 256 : 64;             // contraction elements per stage
-    static constexpr int QROW = MODE == MM_W4 ? 32 : 128;            // bytes per row per stage
-    static constexpr int Q_BYTES = TQ * QROW, P_BYTES = TP * 128;
-    static constexpr int QS_BYTES = MODE == MM_MX4 ? TQ * 8 : MODE == MM_W4 ? TQ * 4 : 0;
-    static constexpr int PS_BYTES = MODE == MM_MX4 ? TP * 8 : 0;
-    static constexpr int P_AT = Q_BYTES, QS_AT = P_AT + P_BYTES, PS_AT = QS_AT + QS_BYTES;
-    static constexpr int STAGE = PS_AT + PS_BYTES;
-    static constexpr int LDS = 2 * STAGE;
-    // loads per wave and stage; scales of small tiles are loaded by several waves alike
-    static constexpr int QL = Q_BYTES / 1024 / NW, PL = P_BYTES / 1024 / NW;
-    static constexpr int up(int bytes) { return bytes == 0 ? 0 : bytes / 256 >= NW ? bytes / 256 / NW : 1; }
-    static constexpr int QSL = up(QS_BYTES), PSL = up(PS_BYTES);
-    static_assert(QL >= 1 && PL >= 1 && Q_BYTES % (1024 * NW) == 0 && P_BYTES % (1024 * NW) == 0, "loads");
-    static_assert(LDS <= 160 * 1024, "LDS");
-};
+__device__ __forceinline__ int mm_swz(int i) { return ((i ^ (i >> 1)) & 1) | ((i >> 1) & 2); }
 
 typedef __attribute__((address_space(3))) i16x4 mm_lds_i16x4;
 
@@ -72,92 +66,65 @@ __device__ __forceinline__ const uint8_t* mm_uniform(const uint8_t* p) {
     return reinterpret_cast<const uint8_t*>(((uint64_t)hi << 32) | lo);
 }
 
-// One operand's loads.  T rows (or columns, TR) of the tile.
-template <bool TR, int T, int ROWB, int L>
+// A tile of T rows by 64 bytes (TR: 32 contraction rows by T columns) as
+// 1 KiB loads, L a wave.
+template <bool TR, int T, int L>
 struct MmLoad {
     const uint8_t* base;               // tile origin at the first stage
     int64_t ld;                        // row bytes
     int64_t left;                      // bytes (TR: rows) of the contraction from the first stage on
     uint32_t off[L];
 
-    __device__ __forceinline__ static int swz_row(int r) { return ROWB == 128 ? (r >> 1) & 7 : 0; }
+    // tile row of an LDS fragment row, and back-to-front of the chunk order
+    __device__ __forceinline__ static int row_of(int slot) { return (slot & ~63) + 4 * (slot & 15) + ((slot >> 4) & 3); }
     __device__ __forceinline__ static int swz_c(int c) { return ((c & 3) | ((c >> 1) & 4)) & (T / 16 - 1); }
 
-    // rows: valid rows of the tile (TR: valid bytes of a row, a multiple of 16 or past them whole chunks)
-    __device__ __forceinline__ void init(int wave, int lane, int64_t rows) {
+    // first .. rows - 1: the tile's rows that exist (TR: bytes of a row that do)
+    __device__ __forceinline__ void init(int wave, int lane, int64_t first, int64_t rows) {
 #pragma unroll
         for (int j = 0; j < L; ++j) {
-            const int slot = (wave * L + j) * 64 + lane;
+            const int unit = (wave * L + j) * 64 + lane;
             if constexpr (TR) {
                 constexpr int CPR = T / 8;
-                const int c = slot / CPR, pos = slot % CPR;
+                const int c = unit / CPR, pos = unit % CPR;
                 const int chunk = (((pos >> 1) ^ swz_c(c)) << 1) | (pos & 1);
                 off[j] = 16 * chunk < rows ? (uint32_t)(c * ld + 16 * chunk) : kOob;
             } else {
-                constexpr int CPR = ROWB / 16;
-                const int r = slot / CPR, chunk = (slot % CPR) ^ swz_row(r);
-                off[j] = r < rows ? (uint32_t)(r * ld + 16 * chunk) : kOob;
+                const int slot = unit >> 2, r = row_of(slot), chunk = (unit & 3) ^ mm_swz(slot & 15);
+                off[j] = r >= first && r < rows ? (uint32_t)(r * ld + 16 * chunk) : kOob;
             }
         }
     }
 
     // Bring stage `it` (counted from the first) to LDS address dst.
     __device__ __forceinline__ void issue(int64_t it, uint32_t dst, int wave, int lane) const {
-        const int64_t at = TR ? it * 64 * ld : it * ROWB;
-        const int64_t rem64 = left - (TR ? it * 64 : it * ROWB);
+        const int64_t at = TR ? it * 32 * ld : it * 64;
+        const int64_t rem64 = left - it * (TR ? 32 : 64);
         const int rem = rem64 > 0x10000 ? 0x10000 : (int)rem64;
         const __amdgpu_buffer_rsrc_t r = rsrc(mm_uniform(base + at), 0x7fffffff);
 #pragma unroll
         for (int j = 0; j < L; ++j) {
-            const int slot = (wave * L + j) * 64 + lane;
+            const int unit = (wave * L + j) * 64 + lane;
             bool ok;
-            if constexpr (TR) ok = slot / (T / 8) < rem;
-            else ok = 16 * ((slot % (ROWB / 16)) ^ swz_row(slot / (ROWB / 16))) < rem;
+            if constexpr (TR) ok = unit / (T / 8) < rem;
+            else ok = 16 * ((unit & 3) ^ mm_swz((unit >> 2) & 15)) < rem;
             dma<16>(r, dst + (wave * L + j) * 1024, ok ? off[j] : kOob);
         }
     }
 };
 
-// Scale dwords of T rows, W dwords a row, dword arrays [w][row].  Rows past
-// the tile's last repeat it, so that every scale a wave meets is a real one.
-template <int T, int W, int L>
+// The scale planes of T rows, 4 a stage: T / 16 lanes of 16 bytes a plane,
+// one load for the workgroup (every wave that calls it brings the same bytes).
+template <int T>
 struct MmScales {
-    const uint8_t* base;
-    int64_t left;                      // scale bytes of a row from the first stage on
-    uint32_t off[L];
-
-    __device__ __forceinline__ void init(int wave, int lane, int64_t rows, int64_t ld) {
-#pragma unroll
-        for (int j = 0; j < L; ++j) {
-            const int slot = ((wave * L + j) * 64 + lane) % (T * W);
-            const int w = slot / T, r = slot % T;
-            off[j] = (uint32_t)((r < rows ? r : rows - 1) * ld + 4 * w);
-        }
-    }
-
-    // `at`: byte of the row, a multiple of 4 like the row's length
-    __device__ __forceinline__ void issue(int64_t at, uint32_t dst, int wave, int lane) const {
-        const int64_t rem64 = left - at;
-        const int rem = rem64 > 0x10000 ? 0x10000 : (int)rem64;
-        const __amdgpu_buffer_rsrc_t r = rsrc(mm_uniform(base + at), 0x7fffffff);
-#pragma unroll
-        for (int j = 0; j < L; ++j) {
-            const int piece = (wave * L + j) % (T * W / 64);
-            const int w = (piece * 64 + lane) / T;
-            dma<4>(r, dst + piece * 256, 4 * w < rem ? off[j] : kOob);
-        }
+    const uint8_t* base;               // plane 0 of the first stage, at the tile's first row
+    int64_t plane;                     // bytes of a plane
+    __device__ __forceinline__ void issue(int64_t it, uint32_t dst, int lane) const {
+        const __amdgpu_buffer_rsrc_t r = rsrc(mm_uniform(base + it * 4 * plane), 0x7fffffff);
+        const int pl = lane / (T / 16), at = lane % (T / 16);
+        dma<16>(r, dst, pl < 4 ? (uint32_t)(pl * plane + 16 * at) : kOob);
     }
 };
-
-// Two bytes of each of N fragments (64 LDS bytes apart), two fragments a register.
-template <int N>
-__device__ __forceinline__ void read_u16s(const uint8_t* at, uint32_t* out) {
-#pragma unroll
-    for (int x = 0; x < N; x += 2) {
-        out[x / 2] = *reinterpret_cast<const uint16_t*>(at + x * 64);
-        if (x + 1 < N) out[x / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(at + (x + 1) * 64) << 16;
-    }
-}
 
 // f(0), .., f(N - 1) with constant arguments.
 template <int N, int I = 0, typename F>
@@ -168,6 +135,7 @@ __device__ __forceinline__ void mm_for(F&& f) {
     }
 }
 
+// One MFMA, then one LDS read, until the reads are placed.
 template <int NM, int ND>
 __device__ __forceinline__ void mm_interleave() {
     if constexpr (NM > 0) {
@@ -177,105 +145,119 @@ __device__ __forceinline__ void mm_interleave() {
     }
 }
 
+// What a workgroup computes: rows [v0, r1) of the tile that begins at row r0
+// and column q0, of expert e (-1: zeros), over stages [st0, st0 + nst) of the
+// contraction that begins at c_at and is c_len long.
+struct MmWork {
+    int e, split;
+    int64_t r0, v0, r1, q0, c_at, c_len, st0;
+    int nst;
+};
+
+template <int MODE, int TQ, int TP, int WQ, int WP>
+struct MmLay {
+    static constexpr int NW = WQ * WP;
+    static constexpr int FQ = TQ / WQ / 16, FP = TP / WP / 16;       // fragments per wave
+    static constexpr bool W4 = MODE == MM_W4, MX = MODE == MM_MX4;
+    static constexpr int Q_BYTES = TQ * 64, P_BYTES = TP * 64;
+    static constexpr int QS_BYTES = MX || W4 ? 1024 : 0, PS_BYTES = MX ? 1024 : 0;
+    // a ring slot holds a stage's P (and Q); mx4 weights against 16-bit
+    // activations have two slots of their own, each for four stages
+    static constexpr int P_AT = W4 ? 0 : Q_BYTES, QS_AT = P_AT + P_BYTES, PS_AT = QS_AT + (W4 ? 0 : QS_BYTES);
+    static constexpr int STAGE = PS_AT + PS_BYTES;
+    static constexpr int W_AT = kRing * STAGE, W_SLOT = Q_BYTES + QS_BYTES;
+    static constexpr int LDS = kRing * STAGE + (W4 ? 2 * W_SLOT : 0);
+    static constexpr int QL = Q_BYTES / 1024 / NW, PL = P_BYTES / 1024 / NW;
+    static constexpr int VM = W4 ? PL : QL + PL + (MX ? 1 : 0);      // loads per wave and stage
+    static constexpr int VMW = W4 ? QL + 1 : 0;                       // and per four stages of weights
+    static_assert(QL >= 1 && PL >= 1 && Q_BYTES % (1024 * NW) == 0 && P_BYTES % (1024 * NW) == 0, "loads");
+    static_assert(FQ % 4 == 0 && (FP % 4 == 0 || FP == 2 || FP == 1), "fragments");
+    static_assert(LDS <= 160 * 1024, "LDS");
+};
+
+// Sixteen (n) consecutive outputs.
+__device__ __forceinline__ void mm_store16(void* y, int out, int64_t at, int n, bool vec, const f32x4 (&v)[4]) {
+    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    if (out != OUT_F32 && vec && n >= 16) {
+        union { f16x4 h[4]; bf16x4 b[4]; uint4 u[2]; } w;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (out == OUT_F16) w.h[k] = __builtin_convertvector(v[k], f16x4);
+            else w.b[k] = __builtin_convertvector(v[k], bf16x4);
+        }
+        uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(y) + at);
+        d[0] = w.u[0];
+        d[1] = w.u[1];
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (n > 4 * k) mm_store4(y, out, at + 4 * k, n - 4 * k, vec, v[k]);
+}
+
 template <int MODE, int DT, bool QT, bool PT, int TQ, int TP, int WQ, int WP>
-__global__ void __launch_bounds__(WQ* WP * 64, 2) k_mm_tiles(MmArgs a, uint32_t nq, uint32_t np) {
+__device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_t* lds) {
     using L = MmLay<MODE, TQ, TP, WQ, WP>;
-    constexpr bool GC = PT;            // the experts divide the contraction (weight gradient)
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[L::LDS];
+    constexpr bool W4 = L::W4, MX = L::MX;
     const uint32_t lds32 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_void*)lds);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i = lane & 15, g = lane >> 4;
-
-    // which tile
-    const uint32_t rows = GC ? np : a.offs ? (uint32_t)mm_count_tiles(a, TP) : np;
-    const uint32_t per_split = rows * nq * (GC ? (uint32_t)a.E : 1u), total = per_split * (uint32_t)a.splits;
-    const uint32_t chunk = (total + 7) / 8;
-    uint32_t id = (blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= chunk || id >= total) return;
-    const int split = (int)(id / per_split);
-    id -= split * per_split;
-    uint32_t e_gc = 0;
-    if constexpr (GC) {
-        e_gc = id / (rows * nq);
-        id -= e_gc * rows * nq;
-    }
-    const uint32_t grp = id / (kMmGroupP * nq), in = id - grp * kMmGroupP * nq;
-    const uint32_t gsz = rows - grp * kMmGroupP < (uint32_t)kMmGroupP ? rows - grp * kMmGroupP : (uint32_t)kMmGroupP;
-    const uint32_t qt = in / gsz, pt = grp * kMmGroupP + in - qt * gsz;
-
-    MmTile tile;
-    int64_t c_at = 0, c_len = a.C;     // this expert's part of the contraction (GC: token rows)
-    if constexpr (GC) {
-        int64_t lo = 0, hi = a.C;
-        if (a.offs) {
-            const int64_t v0 = a.offs[e_gc], v1 = a.offs[e_gc + 1];
-            lo = v0 < 0 ? 0 : (v0 > a.C ? a.C : v0);
-            hi = v1 < lo ? lo : (v1 > a.C ? a.C : v1);
-        }
-        c_at = lo;
-        c_len = hi - lo;
-        tile.e = (int)e_gc;
-        tile.r0 = (int64_t)pt * TP;
-        tile.r1 = tile.r0 + TP < a.P ? tile.r0 + TP : a.P;
-    } else {
-        if (!mm_find_tile(a, TP, (int)pt, &tile)) return;
-    }
-    const int64_t q0 = (int64_t)qt * TQ, e = tile.e < 0 ? 0 : tile.e;
-    const int64_t nst_all = (c_len + L::CE - 1) / L::CE;
-    const int64_t st0 = nst_all * split / a.splits, st1 = nst_all * (split + 1) / a.splits;
-    const int nst = tile.e < 0 ? 0 : (int)(st1 - st0);
-
+    const int64_t e = w.e < 0 ? 0 : w.e;
+    const int64_t nb = (a.C + kMxBlock - 1) / kMxBlock;
     constexpr int ES = 2;
-    const int64_t rowb = MODE == MM_MX4 ? (a.C + kMxBlock - 1) / kMxBlock * 16 : a.C * ES;   // contraction bytes, [row][c]
-    MmLoad<QT, TQ, L::QROW, L::QL> lq;
-    MmLoad<PT, TP, 128, L::PL> lp;
+
+    MmLoad<QT, TQ, L::QL> lq;
+    MmLoad<PT, TP, L::PL> lp;
     lq.ld = a.ldq;
     lp.ld = a.ldp;
     if constexpr (QT) {
-        lq.base = a.q + (GC ? c_at * a.ldq : e * a.strideq + st0 * 64 * a.ldq) + q0 * ES;
-        lq.left = GC ? c_len : c_len - st0 * 64;
-        lq.init(wave, lane, (a.Q - q0) * ES);
+        lq.base = a.q + (PT ? w.c_at * a.ldq : e * a.strideq) + w.st0 * 32 * a.ldq + w.q0 * ES;
+        lq.left = w.c_len - w.st0 * 32;
+        lq.init(wave, lane, 0, (a.Q - w.q0) * ES);
     } else {
-        const int64_t qrowb = MODE == MM_W4 ? (a.C + kMxBlock - 1) / kMxBlock * 16 : rowb;
-        lq.base = a.q + e * a.strideq + q0 * a.ldq + st0 * L::QROW;
-        lq.left = qrowb - st0 * L::QROW;
-        lq.init(wave, lane, a.Q - q0);
+        const int64_t at = W4 ? w.st0 / 4 * 64 : w.st0 * 64;         // W4: splits begin at whole groups of four stages
+        lq.base = a.q + e * a.strideq + w.q0 * a.ldq + at;
+        lq.left = (MX || W4 ? nb * 16 : a.C * ES) - at;
+        lq.init(wave, lane, 0, a.Q - w.q0);
     }
+    const int64_t prow = MX ? nb * 16 : a.C * ES;
     if constexpr (PT) {
-        lp.base = a.p + c_at * a.ldp + tile.r0 * ES;
-        lp.left = c_len;
-        lp.init(wave, lane, (a.P - tile.r0) * ES);
+        lp.base = a.p + (w.c_at + w.st0 * 32) * a.ldp + w.r0 * ES;
+        lp.left = w.c_len - w.st0 * 32;
+        lp.init(wave, lane, 0, (a.P - w.r0) * ES);
     } else {
-        lp.base = a.p + tile.r0 * a.ldp + st0 * 128;
-        lp.left = rowb - st0 * 128;
-        lp.init(wave, lane, tile.r1 - tile.r0);
+        lp.base = a.p + w.r0 * a.ldp + w.st0 * 64;
+        lp.left = prow - w.st0 * 64;
+        lp.init(wave, lane, w.v0 - w.r0, w.r1 - w.r0);
     }
-    constexpr int QSW = MODE == MM_MX4 ? 2 : 1;
-    MmScales<TQ, QSW, MODE == MM_16 ? 1 : L::QSL> lqs;
-    MmScales<TP, 2, MODE == MM_MX4 ? L::PSL : 1> lps;
-    const int64_t nb = (a.C + kMxBlock - 1) / kMxBlock;
-    if constexpr (MODE != MM_16) {
-        lqs.base = a.qs + e * a.strideqs + q0 * a.ldqs;
-        lqs.left = nb;
-        lqs.init(wave, lane, a.Q - q0, a.ldqs);
+    MmScales<TQ> lqs;
+    MmScales<TP> lps;
+    if constexpr (MX || W4) {
+        lqs.plane = a.ldqs;
+        lqs.base = a.qs + e * a.strideqs + (W4 ? w.st0 / 4 : w.st0) * 4 * a.ldqs + w.q0;
     }
-    if constexpr (MODE == MM_MX4) {
-        lps.base = a.ps + tile.r0 * a.ldps;
-        lps.left = nb;
-        lps.init(wave, lane, tile.r1 - tile.r0, a.ldps);
+    if constexpr (MX) {
+        lps.plane = a.ldps;
+        lps.base = a.ps + w.st0 * 4 * a.ldps + w.r0;
     }
-    constexpr int VM = L::QL + L::PL + L::QSL + L::PSL;
-    // stage `it` of this split into slot it % 2; one past the last writes zeros that nobody reads
+    // stage `it` of this workgroup into its ring slot; stages past the last write zeros that nobody reads
     auto issue = [&](int it) {
-        const uint32_t dst = lds32 + (it & 1) * L::STAGE;
-        lq.issue(it, dst, wave, lane);
+        const uint32_t dst = lds32 + (it & (kRing - 1)) * L::STAGE;
+        if constexpr (!W4) lq.issue(it, dst, wave, lane);
         lp.issue(it, dst + L::P_AT, wave, lane);
-        if constexpr (MODE == MM_MX4) {
-            lqs.issue((st0 + it) * 8, dst + L::QS_AT, wave, lane);
-            lps.issue((st0 + it) * 8, dst + L::PS_AT, wave, lane);
+        if constexpr (MX) {
+            // the two scale loads are shared out over the waves; past the last stage they repeat it
+            const int s = it < w.nst ? it : w.nst - 1;
+            if (wave & 1) lps.issue(s, dst + L::PS_AT, lane);
+            else lqs.issue(s, dst + L::QS_AT, lane);
         }
-        // 16-bit activations: a stage needs 2 scale bytes; its dword holds those of two stages
-        if constexpr (MODE == MM_W4) lqs.issue((st0 + it) / 2 * 4, dst + L::QS_AT, wave, lane);
+    };
+    auto issue_w = [&](int grp) {
+        const uint32_t dst = lds32 + L::W_AT + (grp & 1) * L::W_SLOT;
+        lq.issue(grp, dst, wave, lane);
+        const int last = (w.nst + 3) / 4 - 1;
+        lqs.issue(grp < last ? grp : last, dst + L::Q_BYTES, lane);
     };
 
     const int wq = wave % WQ, wp = wave / WQ;
@@ -286,117 +268,144 @@ __global__ void __launch_bounds__(WQ* WP * 64, 2) k_mm_tiles(MmArgs a, uint32_t 
 #pragma unroll
         for (int y = 0; y < L::FP; ++y) acc[x][y] = f32x4{0, 0, 0, 0};
 
+    constexpr int SQ = MX || W4 ? L::FQ / 4 : 1, SP = MX ? (L::FP + 3) / 4 : 1;
     struct Ops {
-        uint4 q[MODE == MM_W4 ? 1 : L::FQ];
-        uint32_t qd[MODE == MM_W4 ? L::FQ : 1];
+        uint4 q[W4 ? 1 : L::FQ];
+        uint32_t qd[W4 ? L::FQ : 1];
         uint4 p[L::FP];
+        uint32_t qs[SQ], ps[SP];       // scale bytes, four fragments a register
     };
-    struct Sc {
-        uint32_t q[(L::FQ + 1) / 2], p[(L::FP + 1) / 2];   // two bytes a fragment, two fragments a register
+    auto frag_row = [&](const uint8_t* at, int f) -> uint4 {
+        return *reinterpret_cast<const uint4*>(at + f * 1024 + i * 64 + ((g ^ mm_swz(i)) << 4));
     };
-    auto frag_row = [&](const uint8_t* at, int f, int s) -> uint4 {
-        const int c = MODE == MM_MX4 ? 2 * g + s : 4 * s + g;
-        return *reinterpret_cast<const uint4*>(at + f * 2048 + i * 128 + ((c ^ ((i >> 1) & 7)) << 4));
-    };
-    auto frag_tr = [&](const uint8_t* at, int f, int s, auto tc) -> uint4 {
+    auto frag_tr = [&](const uint8_t* at, int f, auto tc) -> uint4 {
         constexpr int T = decltype(tc)::value;
         const int fx = (((i >> 2) & 3) | ((g & 1) << 2)) & (T / 16 - 1);
-        const uint8_t* p = at + (32 * s + 8 * g + (i >> 2)) * (T * 2) + ((f ^ fx) << 5) + ((i & 3) << 3);
+        const uint8_t* p = at + (8 * g + (i >> 2)) * (T * 2) + ((f ^ fx) << 5) + ((i & 3) << 3);
         union { i16x4 v[2]; uint4 u; } r;
         r.v[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((mm_lds_i16x4*)(p));
         r.v[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((mm_lds_i16x4*)(p + 4 * T * 2));
         return r.u;
     };
-    auto read_ops = [&](const uint8_t* st, int s, Ops& o) {
+    auto read_ops = [&](int it, Ops& o) {
+        const uint8_t* st = lds + (it & (kRing - 1)) * L::STAGE;
+        const uint8_t* ws = lds + L::W_AT + ((it >> 2) & 1) * L::W_SLOT;   // W4 only
+        if constexpr (W4) {
+            const int b = it & 3;
 #pragma unroll
-        for (int x = 0; x < L::FQ; ++x) {
-            if constexpr (MODE == MM_W4)
-                o.qd[x] = *reinterpret_cast<const uint32_t*>(st + ((fq0 + x) * 16 + i) * 32 + s * 16 + g * 4);
-            else if constexpr (QT) o.q[x] = frag_tr(st, fq0 + x, s, std::integral_constant<int, TQ>{});
-            else o.q[x] = frag_row(st, fq0 + x, s);
+            for (int x = 0; x < L::FQ; ++x)
+                o.qd[x] = *reinterpret_cast<const uint32_t*>(ws + (fq0 + x) * 1024 + i * 64 + ((b ^ mm_swz(i)) << 4) + g * 4);
+#pragma unroll
+            for (int x = 0; x < SQ; ++x)
+                o.qs[x] = *reinterpret_cast<const uint32_t*>(ws + L::Q_BYTES + b * TQ + (fq0 + 4 * x) * 16 + 4 * i);
+        } else {
+#pragma unroll
+            for (int x = 0; x < L::FQ; ++x) {
+                if constexpr (QT) o.q[x] = frag_tr(st, fq0 + x, std::integral_constant<int, TQ>{});
+                else o.q[x] = frag_row(st, fq0 + x);
+            }
+        }
+        if constexpr (MX) {
+#pragma unroll
+            for (int x = 0; x < SQ; ++x)
+                o.qs[x] = *reinterpret_cast<const uint32_t*>(st + L::QS_AT + g * TQ + (fq0 + 4 * x) * 16 + 4 * i);
+#pragma unroll
+            for (int y = 0; y < SP; ++y) {
+                o.ps[y] = *reinterpret_cast<const uint32_t*>(st + L::PS_AT + g * TP + ((fp0 + 4 * y) & ~3) * 16 + 4 * i);
+                if constexpr (L::FP < 4) o.ps[y] >>= 8 * (fp0 & 3);
+            }
         }
 #pragma unroll
         for (int y = 0; y < L::FP; ++y) {
-            if constexpr (PT) o.p[y] = frag_tr(st + L::P_AT, fp0 + y, s, std::integral_constant<int, TP>{});
-            else o.p[y] = frag_row(st + L::P_AT, fp0 + y, s);
+            if constexpr (PT) o.p[y] = frag_tr(st + L::P_AT, fp0 + y, std::integral_constant<int, TP>{});
+            else o.p[y] = frag_row(st + L::P_AT, fp0 + y);
         }
     };
-    auto read_sc = [&](const uint8_t* st, int64_t stage, Sc& o) {
-        if constexpr (MODE == MM_MX4) {
-            const uint8_t* at = st + (g >> 1) * (TQ * 4) + (g & 1) * 2 + L::QS_AT + i * 4;
-            read_u16s<L::FQ>(at + fq0 * 64, o.q);
-            at = st + (g >> 1) * (TP * 4) + (g & 1) * 2 + L::PS_AT + i * 4;
-            read_u16s<L::FP>(at + fp0 * 64, o.p);
-        }
-        if constexpr (MODE == MM_W4) {
-            const uint8_t* at = st + L::QS_AT + i * 4 + (stage & 1) * 2;
-            read_u16s<L::FQ>(at + fq0 * 64, o.q);
-        }
-    };
-    bool odd = false;                  // MM_W4: this lane met a scale outside the safe range
-    auto mmas = [&](const Ops& o, const Sc& sc, auto half) {
-        constexpr int S = decltype(half)::value;
-        if constexpr (MODE == MM_16) {
-#pragma unroll
-            for (int y = 0; y < L::FP; ++y)
-#pragma unroll
-                for (int x = 0; x < L::FQ; ++x) acc[x][y] = mfma16<DT>(o.q[x], o.p[y], acc[x][y]);
-        } else if constexpr (MODE == MM_MX4) {
+    bool odd = false;                  // W4: this lane met a scale outside the safe range
+    auto mmas = [&](const Ops& o) {
+        if constexpr (MX) {
             mm_for<L::FP>([&](auto yc) {
                 mm_for<L::FQ>([&](auto xc) {
                     constexpr int x = decltype(xc)::value, y = decltype(yc)::value;
-                    acc[x][y] = mfma_mx4<2 * (x & 1) + S, 2 * (y & 1) + S>(o.q[x], o.p[y], acc[x][y], sc.q[x / 2],
-                                                                           sc.p[y / 2]);
+                    acc[x][y] = mfma_mx4<x % 4, y % 4>(o.q[x], o.p[y], acc[x][y], o.qs[x / 4], o.ps[y / 4]);
                 });
             });
-        } else {
-            uint4 w[L::FQ];
+        } else if constexpr (W4) {
+            uint4 v[L::FQ];
 #pragma unroll
             for (int x = 0; x < L::FQ; ++x) {
-                const uint32_t v = (sc.q[x / 2] >> (16 * (x & 1) + 8 * S)) & 0xFFu;
-                odd |= v - kSafeLo<DT> > kSafeHi<DT> - kSafeLo<DT>;
-                w[x] = mx4_widen<DT>(o.qd[x], __uint_as_float(v << 23));
+                const uint32_t s = (o.qs[x / 4] >> (8 * (x % 4))) & 0xFFu;
+                odd |= s - kSafeLo<DT> > kSafeHi<DT> - kSafeLo<DT>;
+                v[x] = mx4_widen<DT>(o.qd[x], __uint_as_float(s << 23));
             }
 #pragma unroll
             for (int y = 0; y < L::FP; ++y)
 #pragma unroll
-                for (int x = 0; x < L::FQ; ++x) acc[x][y] = mfma16<DT>(w[x], o.p[y], acc[x][y]);
+                for (int x = 0; x < L::FQ; ++x) acc[x][y] = mfma16<DT>(v[x], o.p[y], acc[x][y]);
+        } else {
+#pragma unroll
+            for (int y = 0; y < L::FP; ++y)
+#pragma unroll
+                for (int x = 0; x < L::FQ; ++x) acc[x][y] = mfma16<DT>(o.q[x], o.p[y], acc[x][y]);
         }
     };
     constexpr int NMMA = L::FQ * L::FP;
-    constexpr int NRD = L::FQ * (QT ? 2 : 1) + L::FP * (PT ? 2 : 1);
-    constexpr int NSC = MODE == MM_MX4 ? L::FQ + L::FP : 0;
+    constexpr int NRD = L::FQ * (QT ? 2 : 1) + L::FP * (PT ? 2 : 1) + (MX ? SQ + SP : 0);
 
-    if (nst > 0) {
-        using H0 = std::integral_constant<int, 0>;
-        using H1 = std::integral_constant<int, 1>;
-        issue(0);
-        issue(1);
-        wait_vm<VM>();
+    if (w.nst > 0) {
+        if constexpr (W4) {
+            issue_w(0);
+            issue_w(1);
+        }
+#pragma unroll
+        for (int s = 0; s < kRing; ++s) issue(s);
+        wait_vm<(kRing - 1) * L::VM>();
         lds_barrier();
-        Ops o0, o1;
-        Sc sc, sn;
-        read_ops(lds, 0, o0);
-        read_sc(lds, st0, sc);
-        for (int it = 0; it < nst; ++it) {
-            read_ops(lds + (it & 1) * L::STAGE, 1, o1);
-            mmas(o0, sc, H0{});
-            if constexpr (MODE != MM_W4) mm_interleave<NMMA, NRD>();
-            // stage it + 1 has landed, and this wave has read all of stage it
-            wait_vm<0>();
+        Ops o[2];
+        read_ops(0, o[0]);
+        // one stage: stage it + 1 has landed and every wave has read stage it
+        constexpr int V = (kRing - 2) * L::VM;
+        auto stage = [&](int it, Ops& cur, Ops& nxt, bool more) {
+            if (W4 && more) wait_vm<V + L::VMW>();
+            else wait_vm<V>();
             lds_barrier();
-            issue(it + 2);
-            const uint8_t* nx = lds + ((it + 1) & 1) * L::STAGE;
-            read_ops(nx, 0, o0);
-            read_sc(nx, st0 + it + 1, sn);
-            mmas(o1, sc, H1{});
-            if constexpr (MODE != MM_W4) mm_interleave<NMMA, NRD + NSC>();
-            sc = sn;
+            if constexpr (W4) {
+                if ((it & 3) == 3) {
+                    issue(it + kRing);
+                    issue_w((it >> 2) + 2);
+                } else {
+                    issue(it + kRing);
+                }
+            } else {
+                issue(it + kRing);
+            }
+            read_ops(it + 1, nxt);
+            mmas(cur);
+            if constexpr (!W4) mm_interleave<NMMA, NRD>();
+        };
+        if constexpr (W4) {
+            // the weights of group gr + 1 are issued after the activations of
+            // stage 4 gr + 3, so they may be outstanding in the first three
+            // stages of group gr; group 1's came before all activations
+            const int groups = (w.nst + 3) / 4;
+            for (int gr = 0; gr < groups; ++gr) {
+                stage(4 * gr, o[0], o[1], gr > 0);
+                stage(4 * gr + 1, o[1], o[0], gr > 0);
+                stage(4 * gr + 2, o[0], o[1], gr > 0);
+                stage(4 * gr + 3, o[1], o[0], false);
+            }
+        } else {
+            int it = 0;
+            for (; it + 2 <= w.nst; it += 2) {
+                stage(it, o[0], o[1], false);
+                stage(it + 1, o[1], o[0], false);
+            }
+            if (it < w.nst) mmas(o[0]);
         }
         wait_vm<0>();                  // no load of this workgroup may land after it ends
     }
 
-    if constexpr (MODE == MM_W4) {
+    if constexpr (W4) {
         // Scales that the 16-bit type cannot hold (they never come from weights
         // of ordinary magnitude): this wave's products once more, a block at a
         // time from memory, unscaled, each sum scaled in fp32.  Kept out of the
@@ -406,70 +415,195 @@ __global__ void __launch_bounds__(WQ* WP * 64, 2) k_mm_tiles(MmArgs a, uint32_t 
             for (int x = 0; x < L::FQ; ++x)
 #pragma unroll
                 for (int y = 0; y < L::FP; ++y) acc[x][y] = f32x4{0, 0, 0, 0};
-            const int64_t b1 = st1 * 2 < nb ? st1 * 2 : nb;
-            for (int64_t b = st0 * 2; b < b1; ++b) {
+            const int64_t b1 = w.st0 + w.nst < nb ? w.st0 + w.nst : nb;
+            for (int64_t b = w.st0; b < b1; ++b) {
                 uint4 pv[L::FP];
 #pragma unroll
                 for (int y = 0; y < L::FP; ++y) {
-                    const int64_t r = tile.r0 + (fp0 + y) * 16 + i, at = b * 64 + g * 16;
+                    const int64_t r = w.r0 + (fp0 + y) / 4 * 64 + 4 * i + (fp0 + y) % 4, at = b * 64 + g * 16;
                     pv[y] = make_uint4(0, 0, 0, 0);
-                    if (r < tile.r1 && at < rowb) pv[y] = *reinterpret_cast<const uint4*>(a.p + r * a.ldp + at);
+                    if (r < w.r1 && at < prow) pv[y] = *reinterpret_cast<const uint4*>(a.p + r * a.ldp + at);
                 }
 #pragma unroll
                 for (int x = 0; x < L::FQ; ++x) {
-                    const int64_t r = q0 + (fq0 + x) * 16 + i, row = r < a.Q ? r : a.Q - 1;
+                    const int64_t r = w.q0 + (fq0 + x) / 4 * 64 + 4 * i + x % 4, row = r < a.Q ? r : a.Q - 1;
                     const uint32_t d = *reinterpret_cast<const uint32_t*>(a.q + e * a.strideq + row * a.ldq + b * 16 + g * 4);
-                    const uint32_t sv = a.qs[e * a.strideqs + row * a.ldqs + b];
-                    const uint4 w = mx4_widen<DT>(d, 1.0f);
+                    const uint32_t sv = a.qs[e * a.strideqs + b * a.ldqs + row];
+                    const uint4 v = mx4_widen<DT>(d, 1.0f);
                     f32x4 f;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) f[k] = e8m0_to_f32((uint32_t)__shfl((int)sv, 4 * g + k));
 #pragma unroll
-                    for (int y = 0; y < L::FP; ++y) acc[x][y] += f * mfma16<DT>(w, pv[y], f32x4{0, 0, 0, 0});
+                    for (int y = 0; y < L::FP; ++y) acc[x][y] += f * mfma16<DT>(v, pv[y], f32x4{0, 0, 0, 0});
                 }
             }
         }
     }
 
-    // lane (i, g), register r: row p = i, column q = 4g + r of its fragment pair
-    const bool vec = a.part ? a.Q % 4 == 0 : a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0 &&
-                                                 (a.stridey % 4 == 0);
+    // lane (i, g), register r of fragments (x, y): row 16 y + i of the wave's rows
+    // (PT) or 4 i + y % 4 of 64, column 16 x + 4 g + r (QT) or 16 g + 4 r + x % 4 of 64
+    const bool vec = a.part ? a.Q % 4 == 0 : a.ldy % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0 &&
+                                                 a.stridey % 8 == 0;
+    void* const out = a.part ? (void*)(a.part + (int64_t)w.split * a.P * a.Q) : a.y;
+    const int64_t ldo = a.part ? a.Q : a.ldy, oat = PT && !a.part ? e * a.stridey : 0;
+    const int kind = a.part ? (int)OUT_F32 : a.out;
 #pragma unroll
     for (int y = 0; y < L::FP; ++y) {
-        const int64_t p = tile.r0 + (fp0 + y) * 16 + i;
-        if (p >= tile.r1) continue;
+        const int fy = fp0 + y;
+        const int64_t p = w.r0 + (PT ? fy * 16 + i : fy / 4 * 64 + 4 * i + fy % 4);
+        if (p < w.v0 || p >= w.r1) continue;
 #pragma unroll
-        for (int x = 0; x < L::FQ; ++x) {
-            const int64_t q = q0 + (fq0 + x) * 16 + 4 * g;
-            if (q >= a.Q) continue;
-            const int n = a.Q - q < 4 ? (int)(a.Q - q) : 4;
-            if (a.part) mm_store4(a.part, OUT_F32, ((int64_t)split * a.P + p) * a.Q + q, n, vec, acc[x][y]);
-            else mm_store4(a.y, a.out, (GC ? e * a.stridey : 0) + p * a.ldy + q, n, vec, acc[x][y]);
+        for (int x = 0; x < L::FQ; x += 4) {
+            if constexpr (QT) {
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const int64_t q = w.q0 + (fq0 + x + f) * 16 + 4 * g;
+                    if (q < a.Q) mm_store4(out, kind, oat + p * ldo + q, a.Q - q < 4 ? (int)(a.Q - q) : 4, vec, acc[x + f][y]);
+                }
+            } else {
+                const int64_t q = w.q0 + (fq0 + x) * 16 + 16 * g;
+                if (q < a.Q) {
+                    f32x4 v[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        v[r] = f32x4{acc[x][y][r], acc[x + 1][y][r], acc[x + 2][y][r], acc[x + 3][y][r]};
+                    mm_store16(out, kind, oat + p * ldo + q, a.Q - q < 16 ? (int)(a.Q - q) : 16, vec, v);
+                }
+            }
         }
     }
 }
 
+// Tile (pt, qt) of T.p x T.q tiles, walked kMmGroupP row tiles at a time.
+__device__ __forceinline__ void mm_walk(uint32_t id, uint32_t np, uint32_t nq, uint32_t* pt, uint32_t* qt) {
+    const uint32_t grp = id / (kMmGroupP * nq), in = id - grp * kMmGroupP * nq;
+    const uint32_t left = np - grp * kMmGroupP, gsz = left < (uint32_t)kMmGroupP ? left : (uint32_t)kMmGroupP;
+    *qt = in / gsz;
+    *pt = grp * kMmGroupP + in - *qt * gsz;
+}
+
+// The work of tile `id` of TQ x TP tiles; false if it is none.
+template <bool GC, int TQ, int TP>
+__device__ __forceinline__ bool mm_work(const MmArgs& a, uint32_t id, uint32_t np, uint32_t nq, int split, int ce,
+                                        MmWork* w) {
+    uint32_t pt, qt;
+    w->c_at = 0;
+    w->c_len = a.C;
+    if constexpr (GC) {
+        const uint32_t e = id / (np * nq);
+        mm_walk(id - e * np * nq, np, nq, &pt, &qt);
+        int64_t lo = 0, hi = a.C;
+        if (a.offs) {
+            const int64_t v0 = a.offs[e], v1 = a.offs[e + 1];
+            lo = v0 < 0 ? 0 : (v0 > a.C ? a.C : v0);
+            hi = v1 < lo ? lo : (v1 > a.C ? a.C : v1);
+        }
+        w->e = (int)e;
+        w->c_at = lo;
+        w->c_len = hi - lo;
+        w->r0 = w->v0 = (int64_t)pt * TP;
+        w->r1 = w->r0 + TP < a.P ? w->r0 + TP : a.P;
+    } else {
+        mm_walk(id, np, nq, &pt, &qt);
+        MmTile t;
+        if (!mm_find_tile(a, TP, (int)pt, &t)) return false;
+        w->e = t.e;
+        w->r0 = t.r0;
+        w->v0 = t.v0;
+        w->r1 = t.r1;
+    }
+    w->q0 = (int64_t)qt * TQ;
+    const int64_t n = (w->c_len + ce - 1) / ce;
+    const int64_t u = a.mode == MM_W4 ? 4 : 1, nu = (n + u - 1) / u;   // splits of whole groups
+    w->split = split;
+    w->st0 = nu * split / a.splits * u;
+    const int64_t st1 = nu * (split + 1) / a.splits * u;
+    w->nst = w->e < 0 ? 0 : (int)((st1 < n ? st1 : n) - w->st0);
+    return true;
+}
+
+// Tile number of this workgroup among n, so that an XCD (every eighth
+// workgroup) has a contiguous range; false for the surplus.
+__device__ __forceinline__ bool mm_xcd(uint32_t b, uint32_t n, uint32_t* id) {
+    const uint32_t chunk = (n + 7) / 8;
+    *id = (b & 7) * chunk + (b >> 3);
+    return (b >> 3) < chunk && *id < n;
+}
+
+// Large products: 256 x 256 tiles, the last round's cut where they fit.
+template <int MODE, int DT, bool QT, bool PT>
+__global__ void __launch_bounds__(512, 2) k_mm_large(MmArgs a, uint32_t nq, uint32_t np) {
+    constexpr bool GC = PT;
+    // 128 x 64 a wave holds fewer 16-bit fragments of mx4 weights than 64 x 128
+    constexpr int WQ = MODE == MM_W4 ? 2 : 4, WP = 8 / WQ;
+    using A = MmLay<MODE, 256, 256, WQ, WP>;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[A::LDS];
+    constexpr int CE = MODE == MM_MX4 ? 128 : 32;
+    const uint32_t rows = GC || !a.offs ? np : (uint32_t)mm_count_tiles(a, 256);
+    const uint32_t total = rows * nq * (GC ? (uint32_t)a.E : 1u);
+    const uint32_t full = total / kMmCUs * kMmCUs, rem = total - full;
+    const uint32_t cut = rem <= kMmCUs / 4 ? 4 : rem <= kMmCUs / 2 ? 2 : 1;
+    uint32_t id, part = 0, parts = 1;
+    if (blockIdx.x < full) {
+        if (!mm_xcd(blockIdx.x, full, &id)) return;
+    } else {
+        if (!mm_xcd(blockIdx.x - full, rem * cut, &id)) return;
+        parts = cut;
+        part = id % cut;
+        id = full + id / cut;
+    }
+    MmWork w;
+    if (!mm_work<GC, 256, 256>(a, id, rows, nq, 0, CE, &w)) return;
+    if (parts > 1) {
+        // rows of the upper or lower half, and (in four) columns of one half
+        const int64_t mid = w.r0 + 128;
+        if (part & 1) {
+            w.r0 = mid;
+            w.v0 = w.v0 > mid ? w.v0 : mid;
+        } else {
+            w.r1 = w.r1 < mid ? w.r1 : mid;
+        }
+        if (part & 2) w.q0 += 128;
+        if (w.v0 >= w.r1 || w.q0 >= a.Q) return;
+    }
+    if (parts == 4) mm_tile<MODE, DT, QT, PT, 128, 128, 2, 4>(a, w, lds);
+    else if (parts == 2 || w.r1 - w.r0 <= 128) mm_tile<MODE, DT, QT, PT, 256, 128, 4, 2>(a, w, lds);
+    else mm_tile<MODE, DT, QT, PT, 256, 256, WQ, WP>(a, w, lds);
+}
+
+// Small products: one tile size, the contraction split where tiles are few.
 template <int MODE, int DT, bool QT, bool PT, int TQ, int TP, int WQ, int WP>
-hipError_t mm_tiles_go(const MmArgs& a, hipStream_t s) {
-    const int64_t nq = (a.Q + TQ - 1) / TQ, np = (a.P + TP - 1) / TP;
-    const int64_t tiles = PT ? np * a.E : mm_tile_bound(a, TP);
-    const int64_t total = tiles * nq * a.splits;
-    if (total >= (int64_t)1 << 31) return hipErrorInvalidValue;
-    const unsigned grid = (unsigned)((total + 7) / 8 * 8);
-    hipLaunchKernelGGL((k_mm_tiles<MODE, DT, QT, PT, TQ, TP, WQ, WP>), dim3(grid), dim3(WQ * WP * 64), 0, s, a,
-                       (uint32_t)nq, (uint32_t)np);
-    return hipGetLastError();
+__global__ void __launch_bounds__(WQ* WP * 64, 2) k_mm_tiles(MmArgs a, uint32_t nq, uint32_t np) {
+    constexpr bool GC = PT;
+    using L = MmLay<MODE, TQ, TP, WQ, WP>;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[L::LDS];
+    constexpr int CE = MODE == MM_MX4 ? 128 : 32;
+    const uint32_t rows = GC || !a.offs ? np : (uint32_t)mm_count_tiles(a, TP);
+    const uint32_t per = rows * nq * (GC ? (uint32_t)a.E : 1u);
+    uint32_t id;
+    if (!mm_xcd(blockIdx.x, per * (uint32_t)a.splits, &id)) return;
+    const int split = (int)(id / per);
+    MmWork w;
+    if (!mm_work<GC, TQ, TP>(a, id - split * per, rows, nq, split, CE, &w)) return;
+    mm_tile<MODE, DT, QT, PT, TQ, TP, WQ, WP>(a, w, lds);
 }
 
 template <int MODE, int DT, bool QT, bool PT>
 hipError_t mm_tiles_size(const MmArgs& a, int size, hipStream_t s) {
+    const MmTileSize t = kMmTileSizes[size];
+    const int64_t nq = (a.Q + t.q - 1) / t.q, np = (a.P + t.p - 1) / t.p;
+    const int64_t tiles = PT ? np * a.E : mm_tile_bound(a, t.p);
+    // cutting the last round adds at most 3 workgroups for each of 64 tiles
+    const int64_t total = tiles * nq * a.splits + (size == 0 ? 3 * kMmCUs / 4 : 0);
+    if (total >= (int64_t)1 << 31) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)((total + 7) / 8 * 8));
+    const uint32_t q = (uint32_t)nq, p = (uint32_t)np;
     switch (size) {
-        // mx4 weights stay 4-bit until a wave multiplies them: 128 x 64 a wave holds
-        // fewer 16-bit fragments than 64 x 128, which would spill
-        case 0: return mm_tiles_go<MODE, DT, QT, PT, 256, 256, MODE == MM_W4 ? 2 : 4, MODE == MM_W4 ? 4 : 2>(a, s);
-        case 1: return mm_tiles_go<MODE, DT, QT, PT, 128, 128, 2, 2>(a, s);
-        default: return mm_tiles_go<MODE, DT, QT, PT, 128, 64, 4, 1>(a, s);
+        case 0: hipLaunchKernelGGL((k_mm_large<MODE, DT, QT, PT>), grid, dim3(512), 0, s, a, q, p); break;
+        case 1: hipLaunchKernelGGL((k_mm_tiles<MODE, DT, QT, PT, 128, 128, 2, 2>), grid, dim3(256), 0, s, a, q, p); break;
+        default: hipLaunchKernelGGL((k_mm_tiles<MODE, DT, QT, PT, 128, 64, 2, 2>), grid, dim3(256), 0, s, a, q, p); break;
     }
+    return hipGetLastError();
 }
 
 }  // namespace ssg
