@@ -67,20 +67,32 @@ __device__ __forceinline__ const uint8_t* mm_uniform(const uint8_t* p) {
 }
 
 // A tile of T rows by 64 bytes (TR: 32 contraction rows by T columns) as
-// 1 KiB loads, L a wave.
+// 1 KiB loads, L a wave.  Stages are issued in order; `next` is the origin of
+// the one to come.
 template <bool TR, int T, int L>
 struct MmLoad {
-    const uint8_t* base;               // tile origin at the first stage
-    int64_t ld;                        // row bytes
-    int64_t left;                      // bytes (TR: rows) of the contraction from the first stage on
+    const uint8_t* next;
+    int64_t step;                      // bytes from a stage to the next
+    int last, ragged, tail;            // stages; the one that ends inside its 64 bytes (TR: 32 rows), and where
+    int at;                            // this lane's place in a stage (TR: of load 0)
     uint32_t off[L];
 
-    // tile row of an LDS fragment row, and back-to-front of the chunk order
+    // tile row of an LDS fragment row
     __device__ __forceinline__ static int row_of(int slot) { return (slot & ~63) + 4 * (slot & 15) + ((slot >> 4) & 3); }
     __device__ __forceinline__ static int swz_c(int c) { return ((c & 3) | ((c >> 1) & 4)) & (T / 16 - 1); }
 
-    // first .. rows - 1: the tile's rows that exist (TR: bytes of a row that do)
-    __device__ __forceinline__ void init(int wave, int lane, int64_t first, int64_t rows) {
+    // first .. rows - 1: the tile's rows that exist (TR: bytes of a row that
+    // do); left: bytes of a row (TR: rows) of the contraction from the first
+    // stage on; nst: stages of this workgroup
+    __device__ __forceinline__ void init(const uint8_t* base, int64_t ld, int64_t left, int nst, int wave, int lane,
+                                         int64_t first, int64_t rows) {
+        next = mm_uniform(base);
+        step = TR ? 32 * ld : 64;
+        last = nst;
+        constexpr int U = TR ? 32 : 64;
+        ragged = left < (int64_t)nst * U ? nst - 1 : -1;
+        tail = (int)(left - (int64_t)(nst - 1) * U < U ? left - (int64_t)(nst - 1) * U : U);
+        at = TR ? (wave * L * 64 + lane) / (T / 8) : 16 * ((lane & 3) ^ mm_swz(lane >> 2));
 #pragma unroll
         for (int j = 0; j < L; ++j) {
             const int unit = (wave * L + j) * 64 + lane;
@@ -96,33 +108,41 @@ struct MmLoad {
         }
     }
 
-    // Bring stage `it` (counted from the first) to LDS address dst.
-    __device__ __forceinline__ void issue(int64_t it, uint32_t dst, int wave, int lane) const {
-        const int64_t at = TR ? it * 32 * ld : it * 64;
-        const int64_t rem64 = left - it * (TR ? 32 : 64);
-        const int rem = rem64 > 0x10000 ? 0x10000 : (int)rem64;
-        const __amdgpu_buffer_rsrc_t r = rsrc(mm_uniform(base + at), 0x7fffffff);
-#pragma unroll
-        for (int j = 0; j < L; ++j) {
-            const int unit = (wave * L + j) * 64 + lane;
-            bool ok;
-            if constexpr (TR) ok = unit / (T / 8) < rem;
-            else ok = 16 * ((unit & 3) ^ mm_swz((unit >> 2) & 15)) < rem;
-            dma<16>(r, dst + (wave * L + j) * 1024, ok ? off[j] : kOob);
-        }
+    // Buffer of stage `it`, empty past the last.
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t open(int it) {
+        const uint8_t* p = next;
+        next += step;
+        return rsrc(p, it < last ? 0x7fffffff : 0);
+    }
+    // Load J of stage `it` to LDS address dst (the stage's).  No branch: it
+    // would cut the block that the products are scheduled in.
+    template <int J>
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int it, uint32_t dst, int wave) const {
+        const int lim = (it == ragged ? tail : 64) - (TR ? J * (64 / (T / 8)) : 0);
+        dma<16>(r, dst + (wave * L + J) * 1024, at < lim ? off[J] : kOob);
     }
 };
 
 // The scale planes of T rows, 4 a stage: T / 16 lanes of 16 bytes a plane,
-// one load for the workgroup (every wave that calls it brings the same bytes).
-template <int T>
+// one load for the workgroup (every wave that issues it brings the same bytes).
 struct MmScales {
-    const uint8_t* base;               // plane 0 of the first stage, at the tile's first row
-    int64_t plane;                     // bytes of a plane
-    __device__ __forceinline__ void issue(int64_t it, uint32_t dst, int lane) const {
-        const __amdgpu_buffer_rsrc_t r = rsrc(mm_uniform(base + it * 4 * plane), 0x7fffffff);
+    const uint8_t* next;
+    int64_t step;
+    int last;
+    uint32_t off;
+
+    __device__ __forceinline__ void init(const uint8_t* base, int64_t plane, int T, int nst, int lane) {
+        next = mm_uniform(base);
+        step = 4 * plane;
+        last = nst;
         const int pl = lane / (T / 16), at = lane % (T / 16);
-        dma<16>(r, dst, pl < 4 ? (uint32_t)(pl * plane + 16 * at) : kOob);
+        off = pl < 4 ? (uint32_t)(pl * plane + 16 * at) : kOob;
+    }
+    // past the last stage: zeros, for elements that are zeros
+    __device__ __forceinline__ void issue(int it, uint32_t dst) {
+        const uint8_t* p = next;
+        next += step;
+        dma<16>(rsrc(p, it < last ? 0x7fffffff : 0), dst, off);
     }
 };
 
@@ -132,16 +152,6 @@ __device__ __forceinline__ void mm_for(F&& f) {
     if constexpr (I < N) {
         f(std::integral_constant<int, I>{});
         mm_for<N, I + 1>(f);
-    }
-}
-
-// One MFMA, then one LDS read, until the reads are placed.
-template <int NM, int ND>
-__device__ __forceinline__ void mm_interleave() {
-    if constexpr (NM > 0) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if constexpr (ND > 0) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        mm_interleave<NM - 1, ND - 1>();
     }
 }
 
@@ -209,55 +219,51 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
 
     MmLoad<QT, TQ, L::QL> lq;
     MmLoad<PT, TP, L::PL> lp;
-    lq.ld = a.ldq;
-    lp.ld = a.ldp;
+    const int groups = (w.nst + 3) / 4;              // W4: a load of weights covers four stages
     if constexpr (QT) {
-        lq.base = a.q + (PT ? w.c_at * a.ldq : e * a.strideq) + w.st0 * 32 * a.ldq + w.q0 * ES;
-        lq.left = w.c_len - w.st0 * 32;
-        lq.init(wave, lane, 0, (a.Q - w.q0) * ES);
+        lq.init(a.q + (PT ? w.c_at * a.ldq : e * a.strideq) + w.st0 * 32 * a.ldq + w.q0 * ES, a.ldq,
+                w.c_len - w.st0 * 32, w.nst, wave, lane, 0, (a.Q - w.q0) * ES);
     } else {
         const int64_t at = W4 ? w.st0 / 4 * 64 : w.st0 * 64;         // W4: splits begin at whole groups of four stages
-        lq.base = a.q + e * a.strideq + w.q0 * a.ldq + at;
-        lq.left = (MX || W4 ? nb * 16 : a.C * ES) - at;
-        lq.init(wave, lane, 0, a.Q - w.q0);
+        lq.init(a.q + e * a.strideq + w.q0 * a.ldq + at, a.ldq, (MX || W4 ? nb * 16 : a.C * ES) - at,
+                W4 ? groups : w.nst, wave, lane, 0, a.Q - w.q0);
     }
     const int64_t prow = MX ? nb * 16 : a.C * ES;
-    if constexpr (PT) {
-        lp.base = a.p + (w.c_at + w.st0 * 32) * a.ldp + w.r0 * ES;
-        lp.left = w.c_len - w.st0 * 32;
-        lp.init(wave, lane, 0, (a.P - w.r0) * ES);
-    } else {
-        lp.base = a.p + w.r0 * a.ldp + w.st0 * 64;
-        lp.left = prow - w.st0 * 64;
-        lp.init(wave, lane, w.v0 - w.r0, w.r1 - w.r0);
-    }
-    MmScales<TQ> lqs;
-    MmScales<TP> lps;
+    if constexpr (PT)
+        lp.init(a.p + (w.c_at + w.st0 * 32) * a.ldp + w.r0 * ES, a.ldp, w.c_len - w.st0 * 32, w.nst, wave, lane, 0,
+                (a.P - w.r0) * ES);
+    else
+        lp.init(a.p + w.r0 * a.ldp + w.st0 * 64, a.ldp, prow - w.st0 * 64, w.nst, wave, lane, w.v0 - w.r0, w.r1 - w.r0);
+    // one scale load a wave: mx4 x mx4, those of Q from even waves and of P from odd ones
+    MmScales ls;
+    const bool odd_wave = MX && (wave & 1);
     if constexpr (MX || W4) {
-        lqs.plane = a.ldqs;
-        lqs.base = a.qs + e * a.strideqs + (W4 ? w.st0 / 4 : w.st0) * 4 * a.ldqs + w.q0;
+        const uint8_t* const qs = a.qs + e * a.strideqs + (W4 ? w.st0 / 4 : w.st0) * 4 * a.ldqs + w.q0;
+        const uint8_t* const ps = a.ps + w.st0 * 4 * a.ldps + w.r0;
+        ls.init(odd_wave ? ps : qs, odd_wave ? a.ldps : a.ldqs, odd_wave ? TP : TQ, W4 ? groups : w.nst, lane);
     }
-    if constexpr (MX) {
-        lps.plane = a.ldps;
-        lps.base = a.ps + w.st0 * 4 * a.ldps + w.r0;
-    }
-    // stage `it` of this workgroup into its ring slot; stages past the last write zeros that nobody reads
-    auto issue = [&](int it) {
+    const int sdst = odd_wave ? L::PS_AT : L::QS_AT;
+    // load U of stage `it` into its ring slot; stages past the last write zeros that nobody reads
+    __amdgpu_buffer_rsrc_t rq, rp;
+    auto load = [&](auto uc, int it) {
+        constexpr int U = decltype(uc)::value, NQ = W4 ? 0 : L::QL;
         const uint32_t dst = lds32 + (it & (kRing - 1)) * L::STAGE;
-        if constexpr (!W4) lq.issue(it, dst, wave, lane);
-        lp.issue(it, dst + L::P_AT, wave, lane);
-        if constexpr (MX) {
-            // the two scale loads are shared out over the waves; past the last stage they repeat it
-            const int s = it < w.nst ? it : w.nst - 1;
-            if (wave & 1) lps.issue(s, dst + L::PS_AT, lane);
-            else lqs.issue(s, dst + L::QS_AT, lane);
+        if constexpr (U < NQ) {
+            if constexpr (U == 0) rq = lq.open(it);
+            lq.template load<U>(rq, it, dst, wave);
+        } else if constexpr (U < NQ + L::PL) {
+            if constexpr (U == NQ) rp = lp.open(it);
+            lp.template load<U - NQ>(rp, it, dst + L::P_AT, wave);
+        } else if constexpr (MX) {
+            ls.issue(it, dst + sdst);
         }
     };
+    auto issue = [&](int it) { mm_for<L::VM>([&](auto u) { load(u, it); }); };
     auto issue_w = [&](int grp) {
         const uint32_t dst = lds32 + L::W_AT + (grp & 1) * L::W_SLOT;
-        lq.issue(grp, dst, wave, lane);
-        const int last = (w.nst + 3) / 4 - 1;
-        lqs.issue(grp < last ? grp : last, dst + L::Q_BYTES, lane);
+        rq = lq.open(grp);
+        mm_for<L::QL>([&](auto u) { lq.template load<decltype(u)::value>(rq, grp, dst, wave); });
+        ls.issue(grp, dst + L::Q_BYTES);
     };
 
     const int wq = wave % WQ, wp = wave / WQ;
@@ -287,120 +293,112 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
         r.v[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((mm_lds_i16x4*)(p + 4 * T * 2));
         return r.u;
     };
-    auto read_ops = [&](int it, Ops& o) {
+    // read U of stage `it`'s operands: scales, Q fragments, P fragments
+    constexpr int NS = MX || W4 ? SQ + (MX ? SP : 0) : 0, NRD = NS + L::FQ + L::FP;
+    auto read = [&](auto uc, int it, Ops& o) {
+        constexpr int U = decltype(uc)::value;
         const uint8_t* st = lds + (it & (kRing - 1)) * L::STAGE;
         const uint8_t* ws = lds + L::W_AT + ((it >> 2) & 1) * L::W_SLOT;   // W4 only
-        if constexpr (W4) {
-            const int b = it & 3;
-#pragma unroll
-            for (int x = 0; x < L::FQ; ++x)
-                o.qd[x] = *reinterpret_cast<const uint32_t*>(ws + (fq0 + x) * 1024 + i * 64 + ((b ^ mm_swz(i)) << 4) + g * 4);
-#pragma unroll
-            for (int x = 0; x < SQ; ++x)
-                o.qs[x] = *reinterpret_cast<const uint32_t*>(ws + L::Q_BYTES + b * TQ + (fq0 + 4 * x) * 16 + 4 * i);
+        const int b = it & 3;                                              // W4: block of the group
+        if constexpr (U < NS) {
+            if constexpr (W4)
+                o.qs[U] = *reinterpret_cast<const uint32_t*>(ws + L::Q_BYTES + b * TQ + (fq0 + 4 * U) * 16 + 4 * i);
+            else if constexpr (U < SQ)
+                o.qs[U] = *reinterpret_cast<const uint32_t*>(st + L::QS_AT + g * TQ + (fq0 + 4 * U) * 16 + 4 * i);
+            else {
+                constexpr int Y = U - SQ;
+                o.ps[Y] = *reinterpret_cast<const uint32_t*>(st + L::PS_AT + g * TP + ((fp0 + 4 * Y) & ~3) * 16 + 4 * i);
+                if constexpr (L::FP < 4) o.ps[Y] >>= 8 * (fp0 & 3);
+            }
+        } else if constexpr (U < NS + L::FQ) {
+            constexpr int X = U - NS;
+            if constexpr (W4)
+                o.qd[X] = *reinterpret_cast<const uint32_t*>(ws + (fq0 + X) * 1024 + i * 64 + ((b ^ mm_swz(i)) << 4) + g * 4);
+            else if constexpr (QT) o.q[X] = frag_tr(st, fq0 + X, std::integral_constant<int, TQ>{});
+            else o.q[X] = frag_row(st, fq0 + X);
         } else {
-#pragma unroll
-            for (int x = 0; x < L::FQ; ++x) {
-                if constexpr (QT) o.q[x] = frag_tr(st, fq0 + x, std::integral_constant<int, TQ>{});
-                else o.q[x] = frag_row(st, fq0 + x);
-            }
-        }
-        if constexpr (MX) {
-#pragma unroll
-            for (int x = 0; x < SQ; ++x)
-                o.qs[x] = *reinterpret_cast<const uint32_t*>(st + L::QS_AT + g * TQ + (fq0 + 4 * x) * 16 + 4 * i);
-#pragma unroll
-            for (int y = 0; y < SP; ++y) {
-                o.ps[y] = *reinterpret_cast<const uint32_t*>(st + L::PS_AT + g * TP + ((fp0 + 4 * y) & ~3) * 16 + 4 * i);
-                if constexpr (L::FP < 4) o.ps[y] >>= 8 * (fp0 & 3);
-            }
-        }
-#pragma unroll
-        for (int y = 0; y < L::FP; ++y) {
-            if constexpr (PT) o.p[y] = frag_tr(st + L::P_AT, fp0 + y, std::integral_constant<int, TP>{});
-            else o.p[y] = frag_row(st + L::P_AT, fp0 + y);
+            constexpr int Y = U - NS - L::FQ;
+            if constexpr (PT) o.p[Y] = frag_tr(st + L::P_AT, fp0 + Y, std::integral_constant<int, TP>{});
+            else o.p[Y] = frag_row(st + L::P_AT, fp0 + Y);
         }
     };
     bool odd = false;                  // W4: this lane met a scale outside the safe range
-    auto mmas = [&](const Ops& o) {
-        if constexpr (MX) {
-            mm_for<L::FP>([&](auto yc) {
-                mm_for<L::FQ>([&](auto xc) {
-                    constexpr int x = decltype(xc)::value, y = decltype(yc)::value;
-                    acc[x][y] = mfma_mx4<x % 4, y % 4>(o.q[x], o.p[y], acc[x][y], o.qs[x / 4], o.ps[y / 4]);
-                });
-            });
-        } else if constexpr (W4) {
-            uint4 v[L::FQ];
-#pragma unroll
-            for (int x = 0; x < L::FQ; ++x) {
-                const uint32_t s = (o.qs[x / 4] >> (8 * (x % 4))) & 0xFFu;
-                odd |= s - kSafeLo<DT> > kSafeHi<DT> - kSafeLo<DT>;
-                v[x] = mx4_widen<DT>(o.qd[x], __uint_as_float(s << 23));
-            }
-#pragma unroll
-            for (int y = 0; y < L::FP; ++y)
-#pragma unroll
-                for (int x = 0; x < L::FQ; ++x) acc[x][y] = mfma16<DT>(v[x], o.p[y], acc[x][y]);
-        } else {
-#pragma unroll
-            for (int y = 0; y < L::FP; ++y)
-#pragma unroll
-                for (int x = 0; x < L::FQ; ++x) acc[x][y] = mfma16<DT>(o.q[x], o.p[y], acc[x][y]);
-        }
+    // the products of one P fragment with every Q fragment
+    auto mmas = [&](auto yc, const Ops& o, const uint4 (&v)[W4 ? L::FQ : 1]) {
+        constexpr int Y = decltype(yc)::value;
+        mm_for<L::FQ>([&](auto xc) {
+            constexpr int X = decltype(xc)::value;
+            if constexpr (MX) acc[X][Y] = mfma_mx4<X % 4, Y % 4>(o.q[X], o.p[Y], acc[X][Y], o.qs[X / 4], o.ps[Y / 4]);
+            else if constexpr (W4) acc[X][Y] = mfma16<DT>(v[X], o.p[Y], acc[X][Y]);
+            else acc[X][Y] = mfma16<DT>(o.q[X], o.p[Y], acc[X][Y]);
+        });
     };
-    constexpr int NMMA = L::FQ * L::FP;
-    constexpr int NRD = L::FQ * (QT ? 2 : 1) + L::FP * (PT ? 2 : 1) + (MX ? SQ + SP : 0);
 
     if (w.nst > 0) {
-        if constexpr (W4) {
-            issue_w(0);
-            issue_w(1);
-        }
+        if constexpr (W4) issue_w(0);
 #pragma unroll
         for (int s = 0; s < kRing; ++s) issue(s);
-        wait_vm<(kRing - 1) * L::VM>();
+        if constexpr (W4) issue_w(1);
+        wait_vm<(kRing - 1) * L::VM + L::VMW>();
         lds_barrier();
         Ops o[2];
-        read_ops(0, o[0]);
-        // one stage: stage it + 1 has landed and every wave has read stage it
+        mm_for<NRD>([&](auto u) { read(u, 0, o[0]); });
+        // One stage: stage it + 1 has landed and every wave has read stage it.
+        // Its products in FP groups, the first half of which also read the next
+        // stage's operands, and all of which share the loads of stage it + kRing:
+        // issued in one burst after the barrier, the loads' scalar instructions
+        // kept the matrix unit waiting in all waves at once.
         constexpr int V = (kRing - 2) * L::VM;
-        auto stage = [&](int it, Ops& cur, Ops& nxt, bool more) {
-            if (W4 && more) wait_vm<V + L::VMW>();
-            else wait_vm<V>();
+        constexpr int RPG = (NRD + (L::FP + 1) / 2 - 1) / ((L::FP + 1) / 2), LPG = (L::VM + L::FP - 1) / L::FP;
+        auto stage = [&](int it, Ops& cur, Ops& nxt, auto more) {
+            constexpr bool last_of_4 = W4 && decltype(more)::value == 0;
+            wait_vm<V + decltype(more)::value>();
             lds_barrier();
+            uint4 v[W4 ? L::FQ : 1];
             if constexpr (W4) {
-                if ((it & 3) == 3) {
-                    issue(it + kRing);
-                    issue_w((it >> 2) + 2);
-                } else {
-                    issue(it + kRing);
+#pragma unroll
+                for (int x = 0; x < L::FQ; ++x) {
+                    const uint32_t s = (cur.qs[x / 4] >> (8 * (x % 4))) & 0xFFu;
+                    odd |= s - kSafeLo<DT> > kSafeHi<DT> - kSafeLo<DT>;
+                    v[x] = mx4_widen<DT>(cur.qd[x], __uint_as_float(s << 23));
                 }
-            } else {
-                issue(it + kRing);
             }
-            read_ops(it + 1, nxt);
-            mmas(cur);
-            if constexpr (!W4) mm_interleave<NMMA, NRD>();
+            mm_for<L::FP>([&](auto yc) {
+                constexpr int Y = decltype(yc)::value;
+                mmas(yc, cur, v);
+                mm_for<RPG>([&](auto k) {
+                    constexpr int U = Y * RPG + decltype(k)::value;
+                    if constexpr (U < NRD) read(std::integral_constant<int, U>{}, it + 1, nxt);
+                });
+                mm_for<LPG>([&](auto k) {
+                    constexpr int U = Y * LPG + decltype(k)::value;
+                    if constexpr (U < L::VM) load(std::integral_constant<int, U>{}, it + kRing);
+                });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            if constexpr (last_of_4) issue_w((it >> 2) + 2);
         };
         if constexpr (W4) {
             // the weights of group gr + 1 are issued after the activations of
             // stage 4 gr + 3, so they may be outstanding in the first three
-            // stages of group gr; group 1's came before all activations
-            const int groups = (w.nst + 3) / 4;
+            // stages of group gr
+            using More = std::integral_constant<int, L::VMW>;
             for (int gr = 0; gr < groups; ++gr) {
-                stage(4 * gr, o[0], o[1], gr > 0);
-                stage(4 * gr + 1, o[1], o[0], gr > 0);
-                stage(4 * gr + 2, o[0], o[1], gr > 0);
-                stage(4 * gr + 3, o[1], o[0], false);
+                stage(4 * gr, o[0], o[1], More{});
+                stage(4 * gr + 1, o[1], o[0], More{});
+                stage(4 * gr + 2, o[0], o[1], More{});
+                stage(4 * gr + 3, o[1], o[0], std::integral_constant<int, 0>{});
             }
         } else {
             int it = 0;
             for (; it + 2 <= w.nst; it += 2) {
-                stage(it, o[0], o[1], false);
-                stage(it + 1, o[1], o[0], false);
+                stage(it, o[0], o[1], std::integral_constant<int, 0>{});
+                stage(it + 1, o[1], o[0], std::integral_constant<int, 0>{});
             }
-            if (it < w.nst) mmas(o[0]);
+            if (it < w.nst) {
+                const uint4 none[1] = {};
+                mm_for<L::FP>([&](auto yc) { mmas(yc, o[0], none); });
+            }
         }
         wait_vm<0>();                  // no load of this workgroup may land after it ends
     }
