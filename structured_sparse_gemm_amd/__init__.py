@@ -794,28 +794,47 @@ def _bytes(t: torch.Tensor, name: str) -> None:
         raise SsgError(_abi.SSG_ERR_DTYPE, "%s must be uint8, got %s" % (name, t.dtype))
 
 
-def _offsets(offs: torch.Tensor, E: int):
+def _need(ok: bool, what: str, *tensors) -> None:
+    if not ok:
+        raise SsgError(_abi.SSG_ERR_SHAPE, "%s: %s" % (what, ", ".join(str(tuple(t.shape)) for t in tensors)))
+
+
+def _on_device(t: torch.Tensor, name: str) -> Optional[int]:
+    """Address of a non-empty device tensor."""
+    if not t.is_cuda:
+        raise SsgError(_abi.SSG_ERR_NULL, "%s must be a ROCm device tensor (got %s)" % (name, t.device))
+    return t.data_ptr() or None
+
+
+def _mat(t: torch.Tensor, name: str) -> Tuple[Optional[int], int]:
+    """(address, row stride) of a matrix with unit column stride."""
+    if t.dim() != 2:
+        raise SsgError(_abi.SSG_ERR_SHAPE, "%s must be 2-D, got shape %s" % (name, tuple(t.shape)))
+    R, C = t.shape
+    ld, unit = t.stride()
+    if unit != 1 and C > 1:
+        raise SsgError(_abi.SSG_ERR_STRIDE, "%s must have unit column stride" % name)
+    return _on_device(t, name), (ld if R > 1 and ld > C else C)
+
+
+def _stack(t: torch.Tensor, name: str) -> Tuple[Optional[int], int, int]:
+    """(address, row stride, expert stride) of a stack [E, R, C] with unit column stride."""
+    if t.dim() != 3:
+        raise SsgError(_abi.SSG_ERR_SHAPE, "%s must be 3-D, got shape %s" % (name, tuple(t.shape)))
+    E, R, C = t.shape
+    stride, ld, unit = t.stride()
+    if unit != 1 and C > 1:
+        raise SsgError(_abi.SSG_ERR_STRIDE, "%s must have unit column stride" % name)
+    ld = ld if R > 1 and ld > C else C
+    return _on_device(t, name), ld, (stride if E > 1 else R * ld)
+
+
+def _offsets(offs: torch.Tensor, E: int) -> Optional[int]:
     if offs.dtype != torch.int32:
         raise SsgError(_abi.SSG_ERR_DTYPE, "offs must be int32, got %s" % (offs.dtype,))
     if offs.dim() != 1 or offs.shape[0] != E + 1 or not offs.is_contiguous():
         raise SsgError(_abi.SSG_ERR_SHAPE, "offs must be a contiguous vector of %d entries" % (E + 1))
-    return _ptr(offs, "offs")
-
-
-def _mats(t: torch.Tensor, name: str) -> Tuple[int, int]:
-    """(row stride, expert stride) of a stack [E, R, C] with unit column stride."""
-    if t.dim() != 3:
-        raise SsgError(_abi.SSG_ERR_SHAPE, "%s must be 3-D, got shape %s" % (name, tuple(t.shape)))
-    E, R, C = t.shape
-    if C > 1 and t.stride(2) != 1:
-        raise SsgError(_abi.SSG_ERR_STRIDE, "%s must have unit column stride" % name)
-    ld = max(t.stride(1), C) if R > 1 else C
-    return ld, t.stride(0) if E > 1 else R * ld
-
-
-def _shape(ok: bool, what: str, *tensors) -> None:
-    if not ok:
-        raise SsgError(_abi.SSG_ERR_SHAPE, "%s: %s" % (what, ", ".join(str(tuple(t.shape)) for t in tensors)))
+    return _on_device(offs, "offs")
 
 
 def _same_device(*tensors) -> None:
@@ -825,9 +844,17 @@ def _same_device(*tensors) -> None:
             raise SsgError(_abi.SSG_ERR_NULL, "operands on different devices (%s, %s)" % (d, t.device))
 
 
+def _raw_stream(t: torch.Tensor, stream) -> Optional[int]:
+    """_stream without building a stream object: these calls may take less
+    time on the GPU than that."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.device.index) or None
+    return _stream(t, stream)
+
+
 def _empty(shape, dtype, like: torch.Tensor, stream):
     """A new tensor, allocated on the stream the kernels run on."""
-    if stream is None or like.device.type != "cuda":    # host tensors fail in _ptr
+    if stream is None or like.device.type != "cuda":    # host tensors are refused later
         return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(_torch_stream(like, stream)):
         return torch.empty(shape, dtype=dtype, device=like.device)
@@ -838,81 +865,78 @@ def _run_with_workspace(name: str, operands, y: torch.Tensor, out, ws, stream) -
     that it needs a workspace and the caller gave none, ask for its size,
     allocate it on the stream and call again."""
     fn = getattr(_lib(), name)
-    x, rest = operands[0], operands[1:]
-    ydt, s = _float(y), _stream(y, stream)
+    ydt, s = _float(y), _raw_stream(y, stream)
     if ws is not None:
-        _check(fn(x, ydt, *rest, *out, _ptr(ws, "ws"), ws.numel() * ws.element_size(), s), name)
+        _check(fn(operands[0], ydt, *operands[1:], *out, _on_device(ws, "ws"), ws.numel() * ws.element_size(), s), name)
         return
-    rc = fn(x, ydt, *rest, *out, None, 0, s)
+    rc = fn(operands[0], ydt, *operands[1:], *out, None, 0, s)
     if rc == _abi.SSG_ERR_WORKSPACE:
         need = int(getattr(_lib(), name + "_workspace_bytes")(*operands))
         ws = _empty(need, torch.uint8, y, stream)
-        rc = fn(x, ydt, *rest, *out, ws.data_ptr(), need, s)
-    _check(rc, name)
+        rc = fn(operands[0], ydt, *operands[1:], *out, ws.data_ptr(), need, s)
+    if rc:
+        _check(rc, name)
 
 
 def ssg_mx4_quantize(A: torch.Tensor, elems: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
-    R, K = A.shape
+    dt = _float(A)
+    a, e, s = _mat(A, "A"), _mat(elems, "elems"), _mat(scales, "scales")
     _bytes(elems, "elems")
     _bytes(scales, "scales")
     _same_device(A, elems, scales)
-    nb = ssg_mx4_scale_cols(K)
-    _shape(elems.shape == (R, 16 * nb) and scales.shape == (R, nb), "shapes of A, elems, scales", A, elems, scales)
-    _check(_lib().ssg_mx4_quantize(_float(A), R, K, _ptr(A, "A"), _ld(A, "A"), _ptr(elems, "elems"),
-                                   _ld(elems, "elems"), _ptr(scales, "scales"), _ld(scales, "scales"),
-                                   _stream(A, stream)), "ssg_mx4_quantize")
+    R, K = A.shape
+    nb = (K + 31) // 32
+    _need(elems.shape == (R, 16 * nb) and scales.shape == (R, nb), "shapes of A, elems, scales", A, elems, scales)
+    _check(_lib().ssg_mx4_quantize(dt, R, K, *a, *e, *s, _raw_stream(A, stream)), "ssg_mx4_quantize")
 
 
 def ssg_mx4_dequantize(elems: torch.Tensor, scales: torch.Tensor, D: torch.Tensor, stream=None) -> None:
-    R, K = D.shape
+    dt = _float(D)
+    d, e, s = _mat(D, "D"), _mat(elems, "elems"), _mat(scales, "scales")
     _bytes(elems, "elems")
     _bytes(scales, "scales")
     _same_device(D, elems, scales)
-    nb = ssg_mx4_scale_cols(K)
-    _shape(elems.shape == (R, 16 * nb) and scales.shape == (R, nb), "shapes of elems, scales, D", elems, scales, D)
-    _check(_lib().ssg_mx4_dequantize(_float(D), R, K, _ptr(elems, "elems"), _ld(elems, "elems"),
-                                     _ptr(scales, "scales"), _ld(scales, "scales"), _ptr(D, "D"), _ld(D, "D"),
-                                     _stream(D, stream)), "ssg_mx4_dequantize")
+    R, K = D.shape
+    nb = (K + 31) // 32
+    _need(elems.shape == (R, 16 * nb) and scales.shape == (R, nb), "shapes of elems, scales, D", elems, scales, D)
+    _check(_lib().ssg_mx4_dequantize(dt, R, K, *e, *s, *d, _raw_stream(D, stream)), "ssg_mx4_dequantize")
 
 
-def _mx4_activations(X, xscales, K):
+def _mx4_activations(X, xscales, nb):
     """(type, pointers and strides) of X: 16-bit, or the elements of mx4 rows
     whose scales are xscales."""
     if xscales is None:
         if X.dtype not in (torch.float16, torch.bfloat16):
             raise SsgError(_abi.SSG_ERR_DTYPE, "X must be fp16, bf16, or mx4 elements with xscales; got %s" % (X.dtype,))
-        return _FLOAT[X.dtype], (_ptr(X, "X"), _ld(X, "X"), None, 0)
+        return _FLOAT[X.dtype], (*_mat(X, "X"), None, 0)
     _bytes(X, "X")
     _bytes(xscales, "xscales")
-    _shape(xscales.dim() == 2 and xscales.shape == (X.shape[0], ssg_mx4_scale_cols(K)), "shapes of X, xscales", X, xscales)
-    return _abi.SSG_MX4, (_ptr(X, "X"), _ld(X, "X"), _ptr(xscales, "xscales"), _ld(xscales, "xscales"))
+    _need(xscales.shape == (X.shape[0], nb), "shapes of X, xscales", X, xscales)
+    return _abi.SSG_MX4, (*_mat(X, "X"), *_mat(xscales, "xscales"))
 
 
 def _mm_mx4_operands(X, W, scales, xscales):
     _bytes(W, "W")
     _bytes(scales, "scales")
-    _same_device(X, W, scales, xscales)
-    _shape(X.dim() == 2 and W.dim() == 2 and scales.dim() == 2, "X, W and scales must be 2-D", X, W, scales)
+    _need(X.dim() == 2 and W.dim() == 2 and scales.dim() == 2, "X, W and scales must be 2-D", X, W, scales)
     K = X.shape[1] if xscales is None else 2 * X.shape[1]
-    M, N, nb = W.shape[0], X.shape[0], (K + 31) // 32
-    _shape(W.shape[1] == 16 * nb and scales.shape == (M, nb), "shapes of X, W, scales", X, W, scales)
-    x, xa = _mx4_activations(X, xscales, K)
-    return (x, M, N, K, *xa, _ptr(W, "W"), _ld(W, "W"), _ptr(scales, "scales"), _ld(scales, "scales"))
+    M, nb = W.shape[0], (K + 31) // 32
+    _need(W.shape[1] == 16 * nb and scales.shape == (M, nb), "shapes of X, W, scales", X, W, scales)
+    x, xa = _mx4_activations(X, xscales, nb)
+    _same_device(X, W, scales, xscales)
+    return (x, M, X.shape[0], K, *xa, *_mat(W, "W"), *_mat(scales, "scales"))
 
 
 def _grouped_mm_mx4_operands(X, W, scales, offs, xscales):
     _bytes(W, "W")
     _bytes(scales, "scales")
-    _same_device(X, W, scales, offs, xscales)
-    ldw, stridew = _mats(W, "W")
-    lds, strides = _mats(scales, "scales")
-    _shape(X.dim() == 2, "X must be 2-D", X)
+    _need(X.dim() == 2 and W.dim() == 3 and scales.dim() == 3, "X must be 2-D, W and scales 3-D", X, W, scales)
     K = X.shape[1] if xscales is None else 2 * X.shape[1]
     E, M, nb = W.shape[0], W.shape[1], (K + 31) // 32
-    _shape(W.shape[2] == 16 * nb and scales.shape == (E, M, nb), "shapes of X, W, scales", X, W, scales)
-    x, xa = _mx4_activations(X, xscales, K)
-    return (x, E, M, X.shape[0], K, *xa, _ptr(W, "W"), ldw, stridew, _ptr(scales, "scales"), lds, strides,
-            _offsets(offs, E))
+    _need(W.shape[2] == 16 * nb and scales.shape == (E, M, nb), "shapes of X, W, scales", X, W, scales)
+    x, xa = _mx4_activations(X, xscales, nb)
+    _same_device(X, W, scales, offs, xscales)
+    return (x, E, M, X.shape[0], K, *xa, *_stack(W, "W"), *_stack(scales, "scales"), _offsets(offs, E))
 
 
 def _pair(a: torch.Tensor, b: torch.Tensor) -> int:
@@ -922,35 +946,34 @@ def _pair(a: torch.Tensor, b: torch.Tensor) -> int:
 
 
 def _grouped_mm_operands(X, W, offs):
-    _same_device(X, W, offs)
-    ldw, stridew = _mats(W, "W")
+    x = _pair(X, W)
+    _need(X.dim() == 2 and W.dim() == 3 and X.shape[1] == W.shape[2], "shapes of X, W", X, W)
     E, M, K = W.shape
-    _shape(X.dim() == 2 and X.shape[1] == K, "shapes of X, W", X, W)
-    return (_pair(X, W), E, M, X.shape[0], K, _ptr(X, "X"), _ld(X, "X"), _ptr(W, "W"), ldw, stridew, _offsets(offs, E))
+    _same_device(X, W, offs)
+    return (x, E, M, X.shape[0], K, *_mat(X, "X"), *_stack(W, "W"), _offsets(offs, E))
 
 
 def _grouped_mm_dx_operands(dY, W, offs):
-    _same_device(dY, W, offs)
-    ldw, stridew = _mats(W, "W")
+    x = _pair(dY, W)
+    _need(dY.dim() == 2 and W.dim() == 3 and dY.shape[1] == W.shape[1], "shapes of dY, W", dY, W)
     E, M, K = W.shape
-    _shape(dY.dim() == 2 and dY.shape[1] == M, "shapes of dY, W", dY, W)
-    return (_pair(dY, W), E, M, dY.shape[0], K, _ptr(dY, "dY"), _ld(dY, "dY"), _ptr(W, "W"), ldw, stridew,
-            _offsets(offs, E))
+    _same_device(dY, W, offs)
+    return (x, E, M, dY.shape[0], K, *_mat(dY, "dY"), *_stack(W, "W"), _offsets(offs, E))
 
 
 def _grouped_mm_dw_operands(dY, X, offs):
+    x = _pair(dY, X)
+    _need(dY.dim() == 2 and X.dim() == 2 and dY.shape[0] == X.shape[0], "shapes of dY, X", dY, X)
+    _need(offs.dim() == 1 and offs.shape[0] > 0, "offs must be a vector of E + 1 entries", offs)
     _same_device(dY, X, offs)
-    _shape(dY.dim() == 2 and X.dim() == 2 and dY.shape[0] == X.shape[0], "shapes of dY, X", dY, X)
-    E = offs.shape[0] - 1 if offs.dim() == 1 else -1
-    _shape(E >= 0, "offs must be a vector", offs)
-    return (_pair(dY, X), E, dY.shape[1], X.shape[0], X.shape[1], _ptr(dY, "dY"), _ld(dY, "dY"), _ptr(X, "X"),
-            _ld(X, "X"), _offsets(offs, E))
+    E = offs.shape[0] - 1
+    return (x, E, dY.shape[1], X.shape[0], X.shape[1], *_mat(dY, "dY"), *_mat(X, "X"), _offsets(offs, E))
 
 
-def _out2(Y, name: str, shape, like):
-    _same_device(Y, like)
-    _shape(Y.shape == shape, "%s must be %s" % (name, tuple(shape)), Y)
-    return _ptr(Y, name), _ld(Y, name)
+def _out(Y, name: str, rows: int, cols: int, like):
+    _same_device(like, Y)
+    _need(Y.shape == (rows, cols), "%s must be [%d, %d]" % (name, rows, cols), Y)
+    return _mat(Y, name)
 
 
 def ssg_mm_mx4_workspace_bytes(X, W, scales, xscales=None) -> int:
@@ -975,30 +998,29 @@ def ssg_grouped_mm_dw_workspace_bytes(dY, X, offs) -> int:
 
 def ssg_mm_mx4(X, W, scales, Y, xscales=None, ws=None, stream=None) -> None:
     ops = _mm_mx4_operands(X, W, scales, xscales)
-    _run_with_workspace("ssg_mm_mx4", ops, Y, _out2(Y, "Y", (X.shape[0], W.shape[0]), X), ws, stream)
+    _run_with_workspace("ssg_mm_mx4", ops, Y, _out(Y, "Y", X.shape[0], W.shape[0], X), ws, stream)
 
 
 def ssg_grouped_mm_mx4(X, W, scales, offs, Y, xscales=None, ws=None, stream=None) -> None:
     ops = _grouped_mm_mx4_operands(X, W, scales, offs, xscales)
-    _run_with_workspace("ssg_grouped_mm_mx4", ops, Y, _out2(Y, "Y", (X.shape[0], W.shape[1]), X), ws, stream)
+    _run_with_workspace("ssg_grouped_mm_mx4", ops, Y, _out(Y, "Y", X.shape[0], W.shape[1], X), ws, stream)
 
 
 def ssg_grouped_mm(X, W, offs, Y, ws=None, stream=None) -> None:
     ops = _grouped_mm_operands(X, W, offs)
-    _run_with_workspace("ssg_grouped_mm", ops, Y, _out2(Y, "Y", (X.shape[0], W.shape[1]), X), ws, stream)
+    _run_with_workspace("ssg_grouped_mm", ops, Y, _out(Y, "Y", X.shape[0], W.shape[1], X), ws, stream)
 
 
 def ssg_grouped_mm_dx(dY, W, offs, dX, ws=None, stream=None) -> None:
     ops = _grouped_mm_dx_operands(dY, W, offs)
-    _run_with_workspace("ssg_grouped_mm_dx", ops, dX, _out2(dX, "dX", (dY.shape[0], W.shape[2]), dY), ws, stream)
+    _run_with_workspace("ssg_grouped_mm_dx", ops, dX, _out(dX, "dX", dY.shape[0], W.shape[2], dY), ws, stream)
 
 
 def ssg_grouped_mm_dw(dY, X, offs, dW, ws=None, stream=None) -> None:
     ops = _grouped_mm_dw_operands(dY, X, offs)
     _same_device(dY, dW)
-    _shape(dW.shape == (offs.shape[0] - 1, dY.shape[1], X.shape[1]), "shapes of dY, X, dW", dY, X, dW)
-    lddw, stridedw = _mats(dW, "dW")
-    _run_with_workspace("ssg_grouped_mm_dw", ops, dW, (_ptr(dW, "dW"), lddw, stridedw), ws, stream)
+    _need(dW.shape == (offs.shape[0] - 1, dY.shape[1], X.shape[1]), "shapes of dY, X, dW", dY, X, dW)
+    _run_with_workspace("ssg_grouped_mm_dw", ops, dW, _stack(dW, "dW"), ws, stream)
 
 
 def mx4_quantize(A: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -1007,8 +1029,8 @@ def mx4_quantize(A: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tens
     if A.dim() == 3:
         e, s = mx4_quantize(A.reshape(-1, A.shape[2]), stream)
         return e.view(*A.shape[:2], -1), s.view(*A.shape[:2], -1)
-    _shape(A.dim() == 2, "A must be 2-D or 3-D", A)
-    nb = ssg_mx4_scale_cols(A.shape[1])
+    _need(A.dim() == 2, "A must be 2-D or 3-D", A)
+    nb = (A.shape[1] + 31) // 32
     elems = _empty((A.shape[0], 16 * nb), torch.uint8, A, stream)
     scales = _empty((A.shape[0], nb), torch.uint8, A, stream)
     ssg_mx4_quantize(A, elems, scales, stream)
@@ -1021,7 +1043,7 @@ def mx4_dequantize(elems: torch.Tensor, scales: torch.Tensor, K: int, dtype: tor
     if elems.dim() == 3:
         d = mx4_dequantize(elems.reshape(-1, elems.shape[2]), scales.reshape(-1, scales.shape[2]), K, dtype, stream)
         return d.view(*elems.shape[:2], K)
-    _shape(elems.dim() == 2, "elems must be 2-D or 3-D", elems)
+    _need(elems.dim() == 2, "elems must be 2-D or 3-D", elems)
     D = _empty((elems.shape[0], K), dtype, elems, stream)
     ssg_mx4_dequantize(elems, scales, D, stream)
     return D
@@ -1039,7 +1061,7 @@ def grouped_mm_mx4(X, W, scales, offs, xscales=None, out_dtype: torch.dtype = to
                    stream=None) -> torch.Tensor:
     """Rows offs[e] .. offs[e + 1] - 1 of X times W[e]^T, mx4 weights W [E, M, K]
     (see mm_mx4); rows of no expert are zero."""
-    _shape(W.dim() == 3, "W must be 3-D", W)
+    _need(W.dim() == 3, "W must be 3-D", W)
     Y = _empty((X.shape[0], W.shape[1]), out_dtype, X, stream)
     ssg_grouped_mm_mx4(X, W, scales, offs, Y, xscales=xscales, stream=stream)
     return Y
@@ -1049,7 +1071,7 @@ def grouped_mm(X, W, offs, out_dtype: Optional[torch.dtype] = None, stream=None)
     """Rows offs[e] .. offs[e + 1] - 1 of X [N, K] times W[e]^T, W [E, M, K]; both
     fp16 or both bf16.  Returns [N, M] in out_dtype (X's type or fp32; None:
     X's type); rows of no expert are zero."""
-    _shape(W.dim() == 3, "W must be 3-D", W)
+    _need(W.dim() == 3, "W must be 3-D", W)
     Y = _empty((X.shape[0], W.shape[1]), out_dtype or X.dtype, X, stream)
     ssg_grouped_mm(X, W, offs, Y, stream=stream)
     return Y
@@ -1057,7 +1079,7 @@ def grouped_mm(X, W, offs, out_dtype: Optional[torch.dtype] = None, stream=None)
 
 def grouped_mm_dx(dY, W, offs, out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
     """Gradient of grouped_mm with respect to X: rows of dY [N, M] times W[e]."""
-    _shape(W.dim() == 3, "W must be 3-D", W)
+    _need(W.dim() == 3, "W must be 3-D", W)
     dX = _empty((dY.shape[0], W.shape[2]), out_dtype or dY.dtype, dY, stream)
     ssg_grouped_mm_dx(dY, W, offs, dX, stream=stream)
     return dX
@@ -1066,7 +1088,7 @@ def grouped_mm_dx(dY, W, offs, out_dtype: Optional[torch.dtype] = None, stream=N
 def grouped_mm_dw(dY, X, offs, out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
     """Gradient of grouped_mm with respect to W: [E, M, K], for each expert the
     sum over its rows of dY[n] X[n]^T (zeros for an expert without rows)."""
-    _shape(dY.dim() == 2 and X.dim() == 2 and offs.dim() == 1 and offs.shape[0] > 0, "shapes of dY, X, offs", dY, X, offs)
+    _need(dY.dim() == 2 and X.dim() == 2 and offs.dim() == 1 and offs.shape[0] > 0, "shapes of dY, X, offs", dY, X, offs)
     dW = _empty((offs.shape[0] - 1, dY.shape[1], X.shape[1]), out_dtype or dY.dtype, dY, stream)
     ssg_grouped_mm_dw(dY, X, offs, dW, stream=stream)
     return dW

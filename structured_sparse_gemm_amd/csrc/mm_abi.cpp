@@ -50,9 +50,9 @@ struct Plan {
     bool skinny;
     int rt, nt;                        // skinny: 16-row groups of weights and tokens
     int size, splits;                  // tiles
-    bool copy_q, copy_p;
+    bool copy_q, copy_p, copy_s;
     int64_t at_q, at_p, at_qs, at_ps, at_part;   // workspace offsets
-    int64_t ldq, ldp, plane_q, plane_p;          // strides of the copies and the scale planes
+    int64_t ldq, ldp, lds, plane_q, plane_p;     // strides of the copies and the scale planes
     size_t bytes;
 };
 
@@ -114,12 +114,16 @@ Plan plan(const MmArgs& a) {
         p.ldp = up(pb, 16);
         p.at_p = take(p_rows(a) * p.ldp);
     }
+    // scales against 16-bit activations: whole dwords
+    if (a.mode == ssg::MM_W4 && (nb % 4 || !al(a.qs, 4) || a.ldqs % 4 || a.strideqs % 4)) {
+        p.copy_s = true;
+        p.lds = up(nb, 16);
+        p.at_qs = take(a.E * a.Q * p.lds);
+    }
     // scale planes, padded so that the last tile's pieces stay inside
-    if (a.mode != ssg::MM_16) {
+    if (a.mode == ssg::MM_MX4) {
         p.plane_q = up(a.Q, 256);
         p.at_qs = take(a.E * up(nb, 4) * p.plane_q);
-    }
-    if (a.mode == ssg::MM_MX4) {
         p.plane_p = up(a.P, 16) + 256;
         p.at_ps = take(up(nb, 4) * p.plane_p);
     }
@@ -129,10 +133,10 @@ Plan plan(const MmArgs& a) {
 }
 
 hipError_t repack(const uint8_t* src, int64_t mats, int64_t stride, int64_t rows, int64_t n, int64_t ld, uint8_t* dst,
-                  int64_t ldd, hipStream_t s) {
-    if (stride == rows * ld || mats == 1) return ssg::launch_mm_repack(src, mats * rows, n, ld, dst, ldd, s);
+                  int64_t ldd, int fill, hipStream_t s) {
+    if (stride == rows * ld || mats == 1) return ssg::launch_mm_repack(src, mats * rows, n, ld, dst, ldd, fill, s);
     for (int64_t e = 0; e < mats; ++e) {
-        const hipError_t r = ssg::launch_mm_repack(src + e * stride, rows, n, ld, dst + e * rows * ldd, ldd, s);
+        const hipError_t r = ssg::launch_mm_repack(src + e * stride, rows, n, ld, dst + e * rows * ldd, ldd, fill, s);
         if (r != hipSuccess) return r;
     }
     return hipSuccess;
@@ -150,24 +154,30 @@ int run(MmArgs a, void* ws, size_t ws_bytes, hipStream_t s) {
     uint8_t* const w = (uint8_t*)ws;
     hipError_t e = hipSuccess;
     if (p.copy_q) {
-        e = repack(a.q, q_mats(a), a.strideq, q_rows(a), q_bytes(a), a.ldq, w + p.at_q, p.ldq, s);
+        e = repack(a.q, q_mats(a), a.strideq, q_rows(a), q_bytes(a), a.ldq, w + p.at_q, p.ldq, 0, s);
         a.q = w + p.at_q;
         a.ldq = p.ldq;
         a.strideq = q_rows(a) * p.ldq;
     }
     if (p.copy_p && e == hipSuccess) {
-        e = repack(a.p, 1, 0, p_rows(a), p_bytes(a), a.ldp, w + p.at_p, p.ldp, s);
+        e = repack(a.p, 1, 0, p_rows(a), p_bytes(a), a.ldp, w + p.at_p, p.ldp, 0, s);
         a.p = w + p.at_p;
         a.ldp = p.ldp;
     }
-    if (a.mode != ssg::MM_16 && e == hipSuccess) {
-        e = ssg::launch_mm_planes(a.qs, a.E, a.strideqs, a.Q, blocks(a.C), a.ldqs, w + p.at_qs, p.plane_q, s);
+    if (p.copy_s && e == hipSuccess) {
+        // past the row's blocks: 1.0, for elements that are zero
+        e = repack(a.qs, a.E, a.strideqs, a.Q, blocks(a.C), a.ldqs, w + p.at_qs, p.lds, 127, s);
         a.qs = w + p.at_qs;
-        a.ldqs = p.plane_q;
-        a.strideqs = up(blocks(a.C), 4) * p.plane_q;
+        a.ldqs = p.lds;
+        a.strideqs = a.Q * p.lds;
     }
     if (a.mode == ssg::MM_MX4 && e == hipSuccess) {
-        e = ssg::launch_mm_planes(a.ps, 1, 0, a.P, blocks(a.C), a.ldps, w + p.at_ps, p.plane_p, s);
+        const int64_t nb = blocks(a.C);
+        e = ssg::launch_mm_planes({a.qs, a.E, a.strideqs, a.Q, nb, a.ldqs, w + p.at_qs, p.plane_q},
+                                  {a.ps, 1, 0, a.P, nb, a.ldps, w + p.at_ps, p.plane_p}, s);
+        a.qs = w + p.at_qs;
+        a.ldqs = p.plane_q;
+        a.strideqs = up(nb, 4) * p.plane_q;
         a.ps = w + p.at_ps;
         a.ldps = p.plane_p;
     }

@@ -50,15 +50,21 @@ struct MmTileSize {
     double rate;
 };
 constexpr MmTileSize kMmTileSizes[3] = {{256, 256, 1, 1.0}, {128, 128, 2, 0.7}, {128, 64, 3, 0.5}};
-// mx4 operands of the tiled kernels have their scales in planes
-// [expert][ceil(blocks / 4)][4][rows], ldqs / ldps bytes a plane.
-hipError_t launch_mm_planes(const uint8_t* src, int64_t mats, int64_t stride, int64_t rows, int64_t nb, int64_t ld,
-                            uint8_t* dst, int64_t plane, hipStream_t s);
+// Scales [mats][rows][nb], ld bytes a row, to planes [mats][ceil(nb / 4)][4][plane]
+// for the tiled products of two mx4 operands (which take the planes' size as
+// ldqs / ldps).
+struct MmPlanes {
+    const uint8_t* src;
+    int64_t mats, stride, rows, nb, ld;
+    uint8_t* dst;
+    int64_t plane;
+};
+hipError_t launch_mm_planes(const MmPlanes& q, const MmPlanes& p, hipStream_t s);
 hipError_t launch_mm_tiles(const MmArgs& a, int size, hipStream_t s);
 // Y = the sum of the partials in split order, in the output type.
 hipError_t launch_mm_reduce(const MmArgs& a, hipStream_t s);
-// Rows of n bytes to rows of ldd bytes (a multiple of 16), zeros past n.
-hipError_t launch_mm_repack(const void* src, int64_t rows, int64_t n, int64_t lds, void* dst, int64_t ldd,
+// Rows of n bytes to rows of ldd bytes (a multiple of 16), `fill` past n.
+hipError_t launch_mm_repack(const void* src, int64_t rows, int64_t n, int64_t lds, void* dst, int64_t ldd, int fill,
                             hipStream_t s);
 hipError_t launch_mx4_quantize(int src, int64_t R, int64_t K, const void* A, int64_t lda, void* elems, int64_t lde,
                                void* scales, int64_t lds, hipStream_t s);

@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kThreads) k_mm_reduce(MmArgs a) {
 
 // One 16-byte chunk a thread.
 __global__ void __launch_bounds__(kThreads) k_mm_repack(const uint8_t* src, int64_t rows, int64_t n, int64_t lds,
-                                                        uint8_t* dst, int64_t ldd) {
+                                                        uint8_t* dst, int64_t ldd, int fill) {
     const int64_t cpr = ldd / 16, total = rows * cpr;
     for (int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x; t < total; t += (int64_t)gridDim.x * kThreads) {
         const int64_t r = t / cpr, b = (t - r * cpr) * 16;
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kThreads) k_mm_repack(const uint8_t* src, int6
             __builtin_memcpy(v, at, 16);
         } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = b + j < n ? at[j] : (uint8_t)0;
+            for (int j = 0; j < 16; ++j) v[j] = b + j < n ? at[j] : (uint8_t)fill;
         }
         *reinterpret_cast<uint4*>(dst + r * ldd + b) = *reinterpret_cast<uint4*>(v);
     }
@@ -55,11 +55,13 @@ __global__ void __launch_bounds__(kThreads) k_mm_repack(const uint8_t* src, int6
 // 16 blocks, transposes them in registers, and writes 16 dwords of 4 rows each,
 // consecutive threads consecutive rows.  Rows and blocks past the end get 127
 // (1.0): their elements are zeros.
-__global__ void __launch_bounds__(kThreads) k_mm_planes(const uint8_t* src, int64_t stride, int64_t rows, int64_t nb,
-                                                        int64_t ld, uint8_t* dst, int64_t plane, int64_t planes,
-                                                        int64_t per_mat, int64_t total) {
-    const int64_t r4 = plane / 4;
-    for (int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x; t < total; t += (int64_t)gridDim.x * kThreads) {
+__global__ void __launch_bounds__(kThreads) k_mm_planes(MmPlanes jq, MmPlanes jp, int64_t nq, int64_t total) {
+    for (int64_t n = (int64_t)blockIdx.x * kThreads + threadIdx.x; n < total; n += (int64_t)gridDim.x * kThreads) {
+        const MmPlanes& j = n < nq ? jq : jp;
+        const uint8_t* const src = j.src;
+        uint8_t* const dst = j.dst;
+        const int64_t t = n < nq ? n : n - nq, nb = j.nb, ld = j.ld, rows = j.rows, stride = j.stride, plane = j.plane;
+        const int64_t r4 = plane / 4, planes = (nb + 3) / 4 * 4, per_mat = r4 * ((planes + 15) / 16);
         const int64_t e = t / per_mat, u = t - e * per_mat, c = u / r4, r = (u - c * r4) * 4, b = c * 16;
         uint32_t v[4][4];
 #pragma unroll
@@ -106,20 +108,19 @@ hipError_t launch_mm_reduce(const MmArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_mm_repack(const void* src, int64_t rows, int64_t n, int64_t lds, void* dst, int64_t ldd,
+hipError_t launch_mm_repack(const void* src, int64_t rows, int64_t n, int64_t lds, void* dst, int64_t ldd, int fill,
                             hipStream_t s) {
     if (rows * ldd == 0) return hipSuccess;
     hipLaunchKernelGGL(k_mm_repack, dim3(grid_of(rows * (ldd / 16))), dim3(kThreads), 0, s, (const uint8_t*)src, rows,
-                       n, lds, (uint8_t*)dst, ldd);
+                       n, lds, (uint8_t*)dst, ldd, fill);
     return hipGetLastError();
 }
 
-hipError_t launch_mm_planes(const uint8_t* src, int64_t mats, int64_t stride, int64_t rows, int64_t nb, int64_t ld,
-                            uint8_t* dst, int64_t plane, hipStream_t s) {
-    const int64_t planes = (nb + 3) / 4 * 4, per_mat = plane / 4 * ((planes + 15) / 16), total = mats * per_mat;
+hipError_t launch_mm_planes(const MmPlanes& q, const MmPlanes& p, hipStream_t s) {
+    auto threads = [](const MmPlanes& j) { return j.mats * (j.plane / 4) * (((j.nb + 3) / 4 * 4 + 15) / 16); };
+    const int64_t nq = threads(q), total = nq + threads(p);
     if (total == 0) return hipSuccess;
-    hipLaunchKernelGGL(k_mm_planes, dim3(grid_of(total)), dim3(kThreads), 0, s, src, stride, rows, nb, ld, dst, plane,
-                       planes, per_mat, total);
+    hipLaunchKernelGGL(k_mm_planes, dim3(grid_of(total)), dim3(kThreads), 0, s, q, p, nq, total);
     return hipGetLastError();
 }
 

@@ -31,9 +31,9 @@
 //   are 1 KiB an operand in contiguous pieces (read from their rows they are
 //   four bytes a row and triple the number of memory requests: 357 us against
 //   the products' own time at 28672 x 8192 x 2048).
-// * mx4 x 16-bit: weights come 64 bytes a row (128 elements) every fourth
-//   stage and stay 4-bit in LDS; a wave widens its fragment (4 conversions) on
-//   the way into the MFMA.
+// * mx4 x 16-bit: weights come 64 bytes and one dword of scales a row (128
+//   elements) every fourth stage and stay 4-bit in LDS; a wave widens its
+//   fragment (4 conversions) on the way into the MFMA.
 //
 // Workgroups are dealt round-robin to the 8 XCDs; tile numbers are dealt so
 // that each XCD gets a contiguous range, walked 8 row tiles at a time, which
@@ -146,6 +146,29 @@ struct MmScales {
     }
 };
 
+// mx4 weights against 16-bit activations: one dword of scales of each of T
+// rows, in fragment order, for four stages; a wave brings 64 rows.
+template <int T>
+struct MmRowScales {
+    const uint8_t* next;
+    int last;
+    uint32_t off, dst;
+
+    // rows past the last repeat it, so that every scale a wave meets is a real one
+    __device__ __forceinline__ void init(const uint8_t* base, int64_t ld, int groups, int wave, int lane, int64_t rows) {
+        next = mm_uniform(base);
+        last = groups;
+        const int piece = wave % (T / 64), r = piece * 64 + 4 * (lane & 15) + (lane >> 4);
+        off = (uint32_t)((r < rows ? r : rows - 1) * ld);
+        dst = piece * 256;
+    }
+    __device__ __forceinline__ void issue(int grp, uint32_t at) {
+        const uint8_t* p = next;
+        next += 4;
+        dma<4>(rsrc(p, grp < last ? 0x7fffffff : 0), at + dst, off);
+    }
+};
+
 // f(0), .., f(N - 1) with constant arguments.
 template <int N, int I = 0, typename F>
 __device__ __forceinline__ void mm_for(F&& f) {
@@ -236,12 +259,15 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
         lp.init(a.p + w.r0 * a.ldp + w.st0 * 64, a.ldp, prow - w.st0 * 64, w.nst, wave, lane, w.v0 - w.r0, w.r1 - w.r0);
     // one scale load a wave: mx4 x mx4, those of Q from even waves and of P from odd ones
     MmScales ls;
+    MmRowScales<TQ> lw;
     const bool odd_wave = MX && (wave & 1);
-    if constexpr (MX || W4) {
-        const uint8_t* const qs = a.qs + e * a.strideqs + (W4 ? w.st0 / 4 : w.st0) * 4 * a.ldqs + w.q0;
+    if constexpr (MX) {
+        const uint8_t* const qs = a.qs + e * a.strideqs + w.st0 * 4 * a.ldqs + w.q0;
         const uint8_t* const ps = a.ps + w.st0 * 4 * a.ldps + w.r0;
-        ls.init(odd_wave ? ps : qs, odd_wave ? a.ldps : a.ldqs, odd_wave ? TP : TQ, W4 ? groups : w.nst, lane);
+        ls.init(odd_wave ? ps : qs, odd_wave ? a.ldps : a.ldqs, odd_wave ? TP : TQ, w.nst, lane);
     }
+    if constexpr (W4)
+        lw.init(a.qs + e * a.strideqs + w.q0 * a.ldqs + w.st0, a.ldqs, groups, wave, lane, a.Q - w.q0);
     const int sdst = odd_wave ? L::PS_AT : L::QS_AT;
     // load U of stage `it` into its ring slot; stages past the last write zeros that nobody reads
     __amdgpu_buffer_rsrc_t rq, rp;
@@ -263,7 +289,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
         const uint32_t dst = lds32 + L::W_AT + (grp & 1) * L::W_SLOT;
         rq = lq.open(grp);
         mm_for<L::QL>([&](auto u) { lq.template load<decltype(u)::value>(rq, grp, dst, wave); });
-        ls.issue(grp, dst + L::Q_BYTES);
+        lw.issue(grp, dst + L::Q_BYTES);
     };
 
     const int wq = wave % WQ, wp = wave / WQ;
@@ -274,13 +300,14 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
 #pragma unroll
         for (int y = 0; y < L::FP; ++y) acc[x][y] = f32x4{0, 0, 0, 0};
 
-    constexpr int SQ = MX || W4 ? L::FQ / 4 : 1, SP = MX ? (L::FP + 3) / 4 : 1;
+    constexpr int SQ = W4 ? L::FQ : MX ? L::FQ / 4 : 1, SP = MX ? (L::FP + 3) / 4 : 1;
     struct Ops {
         uint4 q[W4 ? 1 : L::FQ];
         uint32_t qd[W4 ? L::FQ : 1];
         uint4 p[L::FP];
-        uint32_t qs[SQ], ps[SP];       // scale bytes, four fragments a register
+        uint32_t qs[MX ? SQ : 1], ps[SP];   // scale bytes, four fragments a register
     };
+    uint32_t wsc[W4 ? L::FQ : 1];      // W4: scale bytes of a fragment's rows, four stages a register
     auto frag_row = [&](const uint8_t* at, int f) -> uint4 {
         return *reinterpret_cast<const uint4*>(at + f * 1024 + i * 64 + ((g ^ mm_swz(i)) << 4));
     };
@@ -294,16 +321,14 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
         return r.u;
     };
     // read U of stage `it`'s operands: scales, Q fragments, P fragments
-    constexpr int NS = MX || W4 ? SQ + (MX ? SP : 0) : 0, NRD = NS + L::FQ + L::FP;
+    constexpr int NS = MX ? SQ + SP : 0, NRD = NS + L::FQ + L::FP;
     auto read = [&](auto uc, int it, Ops& o) {
         constexpr int U = decltype(uc)::value;
         const uint8_t* st = lds + (it & (kRing - 1)) * L::STAGE;
         const uint8_t* ws = lds + L::W_AT + ((it >> 2) & 1) * L::W_SLOT;   // W4 only
         const int b = it & 3;                                              // W4: block of the group
         if constexpr (U < NS) {
-            if constexpr (W4)
-                o.qs[U] = *reinterpret_cast<const uint32_t*>(ws + L::Q_BYTES + b * TQ + (fq0 + 4 * U) * 16 + 4 * i);
-            else if constexpr (U < SQ)
+            if constexpr (U < SQ)
                 o.qs[U] = *reinterpret_cast<const uint32_t*>(st + L::QS_AT + g * TQ + (fq0 + 4 * U) * 16 + 4 * i);
             else {
                 constexpr int Y = U - SQ;
@@ -322,16 +347,32 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
             else o.p[Y] = frag_row(st + L::P_AT, fp0 + Y);
         }
     };
+    auto row_scales = [&](int it, int x) -> uint32_t {   // W4
+        return *reinterpret_cast<const uint32_t*>(lds + L::W_AT + ((it >> 2) & 1) * L::W_SLOT + L::Q_BYTES +
+                                                  (fq0 + x) * 64 + i * 4);
+    };
     bool odd = false;                  // W4: this lane met a scale outside the safe range
-    // the products of one P fragment with every Q fragment
-    auto mmas = [&](auto yc, const Ops& o, const uint4 (&v)[W4 ? L::FQ : 1]) {
-        constexpr int Y = decltype(yc)::value;
-        mm_for<L::FQ>([&](auto xc) {
-            constexpr int X = decltype(xc)::value;
-            if constexpr (MX) acc[X][Y] = mfma_mx4<X % 4, Y % 4>(o.q[X], o.p[Y], acc[X][Y], o.qs[X / 4], o.ps[Y / 4]);
-            else if constexpr (W4) acc[X][Y] = mfma16<DT>(v[X], o.p[Y], acc[X][Y]);
-            else acc[X][Y] = mfma16<DT>(o.q[X], o.p[Y], acc[X][Y]);
-        });
+    // a stage's products in NG groups: those of one P fragment with every Q
+    // fragment, or (W4) those of one Q fragment, widened a group ahead
+    constexpr int NG = W4 ? L::FQ : L::FP;
+    auto widen = [&](auto xc, int b, const Ops& o) -> uint4 {
+        constexpr int X = decltype(xc)::value;
+        const uint32_t s = (wsc[X] >> (8 * b)) & 0xFFu;
+        odd |= s - kSafeLo<DT> > kSafeHi<DT> - kSafeLo<DT>;
+        return mx4_widen<DT>(o.qd[X], __uint_as_float(s << 23));
+    };
+    auto mmas = [&](auto gc, const Ops& o, uint4 v) {
+        constexpr int G = decltype(gc)::value;
+        if constexpr (W4) {
+#pragma unroll
+            for (int y = 0; y < L::FP; ++y) acc[G][y] = mfma16<DT>(v, o.p[y], acc[G][y]);
+        } else {
+            mm_for<L::FQ>([&](auto xc) {
+                constexpr int X = decltype(xc)::value;
+                if constexpr (MX) acc[X][G] = mfma_mx4<X % 4, G % 4>(o.q[X], o.p[G], acc[X][G], o.qs[X / 4], o.ps[G / 4]);
+                else acc[X][G] = mfma16<DT>(o.q[X], o.p[G], acc[X][G]);
+            });
+        }
     };
 
     if (w.nst > 0) {
@@ -343,51 +384,55 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
         lds_barrier();
         Ops o[2];
         mm_for<NRD>([&](auto u) { read(u, 0, o[0]); });
+        if constexpr (W4) {
+#pragma unroll
+            for (int x = 0; x < L::FQ; ++x) wsc[x] = row_scales(0, x);
+        }
         // One stage: stage it + 1 has landed and every wave has read stage it.
         // Its products in FP groups, the first half of which also read the next
         // stage's operands, and all of which share the loads of stage it + kRing:
         // issued in one burst after the barrier, the loads' scalar instructions
         // kept the matrix unit waiting in all waves at once.
         constexpr int V = (kRing - 2) * L::VM;
-        constexpr int RPG = (NRD + (L::FP + 1) / 2 - 1) / ((L::FP + 1) / 2), LPG = (L::VM + L::FP - 1) / L::FP;
-        auto stage = [&](int it, Ops& cur, Ops& nxt, auto more) {
-            constexpr bool last_of_4 = W4 && decltype(more)::value == 0;
-            wait_vm<V + decltype(more)::value>();
+        constexpr int RPG = (NRD + (NG + 1) / 2 - 1) / ((NG + 1) / 2), LPG = (L::VM + NG - 1) / NG;
+        auto stage = [&](int it, Ops& cur, Ops& nxt, auto bc) {
+            constexpr int B = decltype(bc)::value;   // W4: stage of the group
+            constexpr bool last_of_4 = W4 && B == 3;
+            wait_vm<V + (B < 3 ? L::VMW : 0)>();
             lds_barrier();
-            uint4 v[W4 ? L::FQ : 1];
-            if constexpr (W4) {
-#pragma unroll
-                for (int x = 0; x < L::FQ; ++x) {
-                    const uint32_t s = (cur.qs[x / 4] >> (8 * (x % 4))) & 0xFFu;
-                    odd |= s - kSafeLo<DT> > kSafeHi<DT> - kSafeLo<DT>;
-                    v[x] = mx4_widen<DT>(cur.qd[x], __uint_as_float(s << 23));
-                }
-            }
-            mm_for<L::FP>([&](auto yc) {
-                constexpr int Y = decltype(yc)::value;
-                mmas(yc, cur, v);
+            uint4 v = make_uint4(0, 0, 0, 0), vn = v;
+            if constexpr (W4) v = widen(std::integral_constant<int, 0>{}, B, cur);
+            mm_for<NG>([&](auto gc) {
+                constexpr int G = decltype(gc)::value;
+                mmas(gc, cur, v);
+                if constexpr (W4 && G + 1 < NG) vn = widen(std::integral_constant<int, G + 1>{}, B, cur);
                 mm_for<RPG>([&](auto k) {
-                    constexpr int U = Y * RPG + decltype(k)::value;
+                    constexpr int U = G * RPG + decltype(k)::value;
                     if constexpr (U < NRD) read(std::integral_constant<int, U>{}, it + 1, nxt);
                 });
                 mm_for<LPG>([&](auto k) {
-                    constexpr int U = Y * LPG + decltype(k)::value;
+                    constexpr int U = G * LPG + decltype(k)::value;
                     if constexpr (U < L::VM) load(std::integral_constant<int, U>{}, it + kRing);
                 });
+                v = vn;
                 __builtin_amdgcn_sched_barrier(0);
             });
+            if constexpr (last_of_4) {
+                // every scale of this group is used: those of the next
+#pragma unroll
+                for (int x = 0; x < L::FQ; ++x) wsc[x] = row_scales(it + 1, x);
+            }
             if constexpr (last_of_4) issue_w((it >> 2) + 2);
         };
         if constexpr (W4) {
             // the weights of group gr + 1 are issued after the activations of
             // stage 4 gr + 3, so they may be outstanding in the first three
             // stages of group gr
-            using More = std::integral_constant<int, L::VMW>;
             for (int gr = 0; gr < groups; ++gr) {
-                stage(4 * gr, o[0], o[1], More{});
-                stage(4 * gr + 1, o[1], o[0], More{});
-                stage(4 * gr + 2, o[0], o[1], More{});
-                stage(4 * gr + 3, o[1], o[0], std::integral_constant<int, 0>{});
+                stage(4 * gr, o[0], o[1], std::integral_constant<int, 0>{});
+                stage(4 * gr + 1, o[1], o[0], std::integral_constant<int, 1>{});
+                stage(4 * gr + 2, o[0], o[1], std::integral_constant<int, 2>{});
+                stage(4 * gr + 3, o[1], o[0], std::integral_constant<int, 3>{});
             }
         } else {
             int it = 0;
@@ -396,8 +441,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
                 stage(it + 1, o[1], o[0], std::integral_constant<int, 0>{});
             }
             if (it < w.nst) {
-                const uint4 none[1] = {};
-                mm_for<L::FP>([&](auto yc) { mmas(yc, o[0], none); });
+                mm_for<NG>([&](auto gc) { mmas(gc, o[0], make_uint4(0, 0, 0, 0)); });
             }
         }
         wait_vm<0>();                  // no load of this workgroup may land after it ends
@@ -426,7 +470,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
                 for (int x = 0; x < L::FQ; ++x) {
                     const int64_t r = w.q0 + (fq0 + x) / 4 * 64 + 4 * i + x % 4, row = r < a.Q ? r : a.Q - 1;
                     const uint32_t d = *reinterpret_cast<const uint32_t*>(a.q + e * a.strideq + row * a.ldq + b * 16 + g * 4);
-                    const uint32_t sv = a.qs[e * a.strideqs + b * a.ldqs + row];
+                    const uint32_t sv = a.qs[e * a.strideqs + row * a.ldqs + b];
                     const uint4 v = mx4_widen<DT>(d, 1.0f);
                     f32x4 f;
 #pragma unroll
