@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -45,6 +46,21 @@ int to_dt(int dt) { return dt == SSG_F16 ? ssg::DT_F16 : ssg::DT_BF16; }
 int to_out(int dt) { return dt == SSG_F32 ? ssg::OUT_F32 : dt == SSG_F16 ? ssg::OUT_F16 : ssg::OUT_BF16; }
 
 // ------------------------------------------------------------------ the choice of kernel
+//
+// Times in us of the launches that a plan would make, from what they measured
+// on this chip: a workgroup's time on its CU times the workgroups a CU gets,
+// but no less than the weights take from memory.  Every kernel handles every
+// product it can be chosen for, so a wrong estimate costs time only.
+
+constexpr double kBytesPerUs = 5.2e6, kTileMx4BytesPerUs = 3.2e6;   // the tiles' 64-byte rows of mx4 weights
+
+// Skinny: 16 rt weight rows x 16 nt tokens a workgroup of a 4096-long
+// contraction, by operand types (16-bit, mx4 x mx4, mx4 x 16-bit), nt and rt.
+// Measured at 4096 x 4096 with 16 and 32 tokens; 16-bit weights with 2 and 4 rt are
+// priced up to where many workgroups measured (11008 x 4096 x 16: 30, 33, 32 us).
+constexpr double kSkinnyUs[3][2][3] = {{{9.1, 19.0, 36.0}, {13.0, 16.0, 27.0}},
+                                       {{4.4, 4.7, 6.8}, {6.0, 6.5, 8.0}},
+                                       {{6.0, 7.8, 10.3}, {10.6, 11.9, 14.1}}};
 
 struct Plan {
     bool skinny;
@@ -72,31 +88,65 @@ int64_t q_mats(const MmArgs& a) { return a.pt ? 1 : std::max<int64_t>(a.E, 1); }
 Plan plan(const MmArgs& a) {
     Plan p{};
     p.splits = 1;
-    const int64_t busy = a.offs && !a.pt ? std::max<int64_t>(1, std::min(a.E, a.P)) : 1;
-    const int64_t avg = (a.P + busy - 1) / busy;         // rows of an expert that has some
-    if (!a.qt && !a.pt && avg <= 32) {
-        p.skinny = true;
-        p.nt = avg <= 16 ? 1 : 2;
-        const int64_t tiles = a.P / (16 * p.nt) + busy;
-        p.rt = (a.Q + 31) / 32 * tiles >= 2 * kCUs ? 2 : 1;
-        return p;
+    // experts that have rows, if rows choose them at random, and their rows
+    const double E = a.offs ? std::max<double>(1, (double)a.E) : 1;
+    const double busy = a.offs && !a.pt ? std::max(1.0, E * (1 - std::exp(-(double)a.P / E))) : 1;
+    const double avg = (double)a.P / busy;
+    auto row_tiles = [&](int t) {
+        if (a.pt) return (double)((a.P + t - 1) / t) * E;
+        if (!a.offs || E == 1) return (double)((a.P + t - 1) / t);
+        return busy * std::max(1.0, avg / t + 0.6);
+    };
+    auto ceil_div = [](int64_t n, int64_t d) { return (double)((n + d - 1) / d); };
+    const double bytes = a.pt ? 0 : busy * (double)a.Q * (double)a.C * (a.mode == ssg::MM_16 ? 2 : 0.53);
+    const double tile_floor = bytes / (a.mode == ssg::MM_16 ? kBytesPerUs : kTileMx4BytesPerUs);
+    double best = 1e30;
+    if (!a.qt && !a.pt && avg <= 64) {
+        for (int nt = 1; nt <= 2; ++nt)
+            for (int k = 0; k < 3; ++k) {
+                const int rt = 1 << k;
+                const double wgs = ceil_div(a.Q, 16 * rt) * row_tiles(16 * nt);
+                const double fill = std::min(1.0, avg / (16 * nt));   // tokens of a tile that exist
+                const double one = kSkinnyUs[a.mode][nt - 1][k] * (0.2 + 0.8 * (double)a.C / 4096) * (0.7 + 0.3 * fill);
+                const double us = 3.5 + std::max(std::max(1.0, std::ceil(wgs / kCUs)) * one, bytes / kBytesPerUs);
+                if (us < best) {
+                    best = us;
+                    p.skinny = true;
+                    p.nt = nt;
+                    p.rt = rt;
+                }
+            }
     }
-    // The tile: rounds of a full chip times what a round of that tile takes
-    double best = 0;
+    // Tiles: a stage takes as long as its products at the rate of a full chip,
+    // or its latency.  A split adds the pass over its partials.
+    const int64_t stages = (a.pt ? (int64_t)((double)a.C / E) : a.C) / (a.mode == ssg::MM_MX4 ? 128 : 32) + 1;
     for (int k = 0; k < 3; ++k) {
         const ssg::MmTileSize& t = ssg::kMmTileSizes[k];
-        const double np = a.pt ? (double)((a.P + t.p - 1) / t.p) * a.E
-                               : a.offs ? (double)a.P / t.p + 0.5 * busy : (double)((a.P + t.p - 1) / t.p);
-        const double n = np * (double)((a.Q + t.q - 1) / t.q), slots = (double)kCUs * t.per_cu;
-        const double rounds = n <= slots ? 1 : n / slots + (k == 0 ? 0.25 : 0.5);
-        const double cost = rounds * t.per_cu * t.q * t.p / t.rate;
-        if (k == 0 || cost < best) {
-            best = cost;
-            p.size = k;
-            const int64_t stages = (a.C + (a.mode == ssg::MM_MX4 ? 127 : 31)) / (a.mode == ssg::MM_MX4 ? 128 : 32);
-            p.splits = a.pt || k == 0 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({8, (int64_t)(slots / n), stages / 8}));
+        const double tiles = row_tiles(t.p) * ceil_div(a.Q, t.q);
+        const double stage = t.q * t.p * (a.mode == ssg::MM_MX4 ? 1.3 : 1.0) / t.rate / 78000;
+        for (int splits = 1; splits <= 8; splits *= 2) {
+            if (splits > 1 && (a.pt || k == 0 || stages / splits < 8)) break;
+            const double n = tiles * splits, whole = std::floor(n / kCUs), rest = n - whole * kCUs;
+            double us;
+            if (k == 0) {
+                const double cut = rest <= 0 ? 0 : rest <= kCUs / 4 ? 0.3 : rest <= kCUs / 2 ? 0.55 : 1;
+                us = (whole * stage + (cut > 0 ? std::max(t.latency, cut * stage) : 0)) * stages;
+            } else {
+                const double m = n <= kCUs ? 1 : n / kCUs + 0.25;
+                us = std::max(t.latency * std::ceil(m / t.per_cu), m * stage) * (double)(stages / splits);
+            }
+            us = 6.5 + std::max(us, tile_floor);
+            if (splits > 1) us += 4 + (double)splits * a.P * a.Q * 8 / 3e6;
+            if (a.mode == ssg::MM_MX4) us += 6;
+            if (us < best) {
+                best = us;
+                p.skinny = false;
+                p.size = k;
+                p.splits = splits;
+            }
         }
     }
+    if (p.skinny) return p;
     int64_t at = 0;
     auto take = [&](int64_t n) {
         const int64_t r = at;

@@ -43,13 +43,14 @@ struct MmArgs {
 // end in a partial one.
 int64_t mm_tile_bound(const MmArgs& a, int T);
 hipError_t launch_mm_skinny(const MmArgs& a, int rt, int nt, hipStream_t s);
-// Tile sizes of the tiled kernels, the workgroups a CU holds at once, and the
-// matrix rate of a chip full of them relative to the largest.
+// Tile sizes of the tiled kernels, the workgroups a CU holds at once, the
+// matrix rate of a chip full of them relative to the largest, and the time of
+// a stage (us) when a CU has one workgroup that waits for nothing else.
 struct MmTileSize {
     int q, p, per_cu;
-    double rate;
+    double rate, latency;
 };
-constexpr MmTileSize kMmTileSizes[3] = {{256, 256, 1, 1.0}, {128, 128, 2, 0.7}, {128, 64, 3, 0.5}};
+constexpr MmTileSize kMmTileSizes[3] = {{256, 256, 1, 1.0, 0.26}, {128, 128, 2, 0.65, 0.26}, {128, 64, 3, 0.48, 0.2}};
 // Scales [mats][rows][nb], ld bytes a row, to planes [mats][ceil(nb / 4)][4][plane]
 // for the tiled products of two mx4 operands (which take the planes' size as
 // ldqs / ldps).

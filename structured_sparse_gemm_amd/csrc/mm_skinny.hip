@@ -15,9 +15,10 @@
 // * mx4: lane (i, g) loads one 32-element block (16 bytes) of row i, block
 //   4 t + g, t < 4, and one dword of scales, blocks 4 g .. 4 g + 3 of the
 //   step, which the lanes of a row then exchange.  Against 16-bit activations
-//   dword j of the block meets elements 8 j .. 8 j + 7 of the same block of
-//   the token: the order of the contraction is free as long as both operands
-//   agree.
+//   the four lane groups also exchange the blocks' dwords (four lane-swap
+//   instructions), after which register j holds dword g of block 4 t + j and
+//   meets elements 8 g .. 8 g + 7 of that block of the token, 64 contiguous
+//   bytes a row and load.
 #include <algorithm>
 
 #include "mm_args.hpp"
@@ -46,185 +47,342 @@ __device__ __forceinline__ uint4 ld8(const uint8_t* row, int64_t k, int64_t n) {
     return v;
 }
 
-__device__ __forceinline__ uint4 ld16(const uint8_t* p) {
+// 16 bytes at a wave-uniform address plus a lane's 32-bit offset: the load
+// takes both as they are, without a 64-bit address a lane.
+__device__ __forceinline__ uint4 ld16(const uint8_t* base, uint32_t off, int imm) {
     uint4 v;
-    __builtin_memcpy(&v, p, 16);
+    __builtin_memcpy(&v, base + off + imm, 16);
     return v;
 }
 
-template <int MODE> constexpr int kStep = MODE == MM_16 ? 256 : 512;
+// Lane groups of 16 as rows, d[0 .. 3] as columns: the transpose.
+__device__ __forceinline__ void transpose4(uint32_t (&d)[4]) {
+    // swap the lower group of one pair of registers with the upper one of the
+    // other: first over two groups (32 lanes), then over one
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const auto r = __builtin_amdgcn_permlane32_swap(d[k], d[k + 2], false, false);
+        d[k] = r[0];
+        d[k + 2] = r[1];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+        const auto r = __builtin_amdgcn_permlane16_swap(d[k], d[k + 1], false, false);
+        d[k] = r[0];
+        d[k + 1] = r[1];
+    }
+}
+
+template <int MODE> constexpr int kStep = MODE == MM_MX4 ? 256 : 128;
+constexpr int kRound = 4096;           // mx4: elements whose scales a workgroup holds at once, at most
+constexpr int kScaleRow = kRound / kMxBlock + 16;  // LDS bytes of a row's scales; the pad spreads 16 rows over the banks
 
 template <int MODE, int DT, int RT, int NT>
 struct Skinny {
+    static constexpr bool MX = MODE == MM_MX4, W4 = MODE == MM_W4;
+    static constexpr int S = kStep<MODE>;
+    static constexpr int UW = MODE == MM_16 ? S / 32 : S / 128;      // 16-byte loads of a weight row
+    static constexpr int UX = MX ? S / 128 : S / 32;                 // and of a token row
+    // Scales read by the lanes that use them are four bytes a row and load, and
+    // as many memory requests as the elements: 44032 x 4096 with 16 tokens took
+    // 46 us (bf16) and 35 us (mx4).  Through LDS, 16 bytes a thread for 4096
+    // elements of every row, it takes 37 and 32; with fewer rows a workgroup
+    // the barriers cost more than the requests.
+    static constexpr bool SHARED = MODE != MM_16 && RT >= 4;
+
+    // One step's operands.
+    struct Ops {
+        uint4 w[RT][UW], x[NT][UX];
+        uint32_t ws[RT], xs[NT];       // scales, where the workgroup does not share them
+    };
+
     const MmArgs& a;
-    const uint8_t* qrow[RT];
-    const uint8_t* prow[NT];
-    const uint8_t* qsrow[RT];
-    const uint8_t* psrow[NT];
+    const uint8_t *q, *p, *qs, *ps;    // the tile's first rows (wave-uniform)
+    uint32_t qo[RT], po[NT], qso[RT], pso[NT];   // this lane's rows
+    int64_t qrows, prows, prow0;       // rows of W from q on; the tile's rows from p on, and the first of them
+    uint8_t* sc;                       // LDS: scales of 16 RT weight rows, then of 16 NT tokens (mx4 x mx4)
     int64_t nb;                        // scale bytes of a row
     int i, g;
+    bool odd;                          // met a scale that the 16-bit type cannot hold
     f32x4 acc[RT][NT];
 
-    // scales of blocks 4 g .. 4 g + 3 of the step whose first block is b0; 127 (1.0) past the end
+    // The scales of 128 blocks from `first` on, 16 bytes a thread: from memory,
+    // and into LDS.
+    static constexpr int SROWS = 16 * RT + (MX ? 16 * NT : 0);
+    static constexpr int SPT = (SROWS * 8 + kThreads - 1) / kThreads;
+    __device__ __forceinline__ void load_scales(int64_t first, uint4 (&v)[SPT]) const {
+#pragma unroll
+        for (int j = 0; j < SPT; ++j) {
+            const int t = j * kThreads + threadIdx.x, row = t >> 3;
+            const int64_t b = first + (t & 7) * 16;
+            const bool is_q = row < 16 * RT;
+            const int64_t r = is_q ? std::min<int64_t>(row, qrows - 1)
+                                   : std::max<int64_t>(prow0, std::min<int64_t>(row - 16 * RT, prows - 1));
+            const uint8_t* at = is_q ? qs + r * a.ldqs : ps + r * a.ldps;
+            v[j] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);   // 1.0 past the end
+            if (row >= SROWS) continue;
+            if (b + 16 <= nb) {
+                __builtin_memcpy(&v[j], at + b, 16);
+            } else if (b < nb) {
+                uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (b + e < nb) w[e >> 2] = (w[e >> 2] & ~(0xFFu << (8 * (e & 3)))) | ((uint32_t)at[b + e] << (8 * (e & 3)));
+                v[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+    __device__ __forceinline__ void store_scales(const uint4 (&v)[SPT]) const {
+#pragma unroll
+        for (int j = 0; j < SPT; ++j) {
+            const int t = j * kThreads + threadIdx.x, row = t >> 3;
+            if (row < SROWS) *reinterpret_cast<uint4*>(sc + row * kScaleRow + (t & 7) * 16) = v[j];
+        }
+    }
+
+    // scales of blocks b + 4 lg .. + 3; 1.0 past the end
     template <bool FULL>
-    __device__ __forceinline__ uint32_t ld_scales(const uint8_t* row, int64_t b0) const {
-        const int64_t b = b0 + 4 * g;
+    __device__ __forceinline__ uint32_t ld_scales(const uint8_t* base, uint32_t off, int64_t b, int lg) const {
         uint32_t v = 0x7F7F7F7Fu;
-        if (FULL || b + 4 <= nb) {
-            __builtin_memcpy(&v, row + b, 4);
+        if (FULL || b + 4 * lg + 4 <= nb) {
+            __builtin_memcpy(&v, base + b + (off + 4 * lg), 4);
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (b + e < nb) v = (v & ~(0xFFu << (8 * e))) | ((uint32_t)row[b + e] << (8 * e));
+                if (b + 4 * lg + e < nb) v = (v & ~(0xFFu << (8 * e))) | ((uint32_t)(base + b)[off + 4 * lg + e] << (8 * e));
         }
         return v;
     }
 
+    // block b + g, in a row of n blocks
     template <bool FULL>
-    __device__ __forceinline__ uint4 ld_block(const uint8_t* row, int64_t b) const {
-        if (FULL || b < nb) return ld16(row + b * 16);
+    __device__ __forceinline__ uint4 ld_block(const uint8_t* base, uint32_t off, int64_t b, int imm) const {
+        if (FULL || b + imm / 16 + g < nb) return ld16(base + b * 16, off + 16 * g, imm);
         return make_uint4(0, 0, 0, 0);
     }
 
+    // elements k + 8 g .. + 7 of a 16-bit row
     template <bool FULL>
-    __device__ __forceinline__ void step(int64_t k0) {
+    __device__ __forceinline__ uint4 ld_row(const uint8_t* base, uint32_t off, int64_t k, int imm) const {
+        if constexpr (FULL) return ld16(base + k * 2, off + 16 * g, imm);
+        else return ld8(base + off, k + imm / 2 + 8 * g, a.C);
+    }
+
+    template <bool FULL>
+    __device__ __forceinline__ void load(int64_t k0, Ops& o) const {
+        const int64_t b0 = k0 / kMxBlock;
         if constexpr (MODE == MM_16) {
-            uint4 w[RT][8], x[NT][8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int64_t k = k0 + 32 * u + 8 * g;
+            for (int u = 0; u < UW; ++u)
 #pragma unroll
-                for (int r = 0; r < RT; ++r) w[r][u] = FULL ? ld16(qrow[r] + k * 2) : ld8(qrow[r], k, a.C);
+                for (int r = 0; r < RT; ++r) o.w[r][u] = ld_row<FULL>(q, qo[r], k0, 64 * u);
+        } else {
 #pragma unroll
-                for (int t = 0; t < NT; ++t) x[t][u] = FULL ? ld16(prow[t] + k * 2) : ld8(prow[t], k, a.C);
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int u = 0; u < UW; ++u) o.w[r][u] = ld_block<FULL>(q, qo[r], b0, 64 * u);
+            if constexpr (!SHARED) {
+                // (mx4 x mx4: two groups of four blocks, from lane groups 0 and 1; the others repeat them)
+#pragma unroll
+                for (int r = 0; r < RT; ++r) o.ws[r] = ld_scales<FULL>(qs, qso[r], b0, MX ? g & 1 : 0);
             }
+        }
+        if constexpr (MX) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int r = 0; r < RT; ++r)
+                for (int u = 0; u < UX; ++u) o.x[t][u] = ld_block<FULL>(p, po[t], b0, 64 * u);
+            if constexpr (!SHARED) {
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) acc[r][t] = mfma16<DT>(w[r][u], x[t][u], acc[r][t]);
-        } else if constexpr (MODE == MM_MX4) {
-            const int64_t b0 = k0 / kMxBlock;
-            uint4 w[RT][4], x[NT][4];
-            uint32_t ws[RT], xs[NT];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-#pragma unroll
-                for (int r = 0; r < RT; ++r) w[r][u] = ld_block<FULL>(qrow[r], b0 + 4 * u + g);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) x[t][u] = ld_block<FULL>(prow[t], b0 + 4 * u + g);
-            }
-#pragma unroll
-            for (int r = 0; r < RT; ++r) ws[r] = ld_scales<FULL>(qsrow[r], b0);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) xs[t] = ld_scales<FULL>(psrow[t], b0);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                uint32_t sw[RT], sx[NT];
-#pragma unroll
-                for (int r = 0; r < RT; ++r) sw[r] = (uint32_t)__shfl((int)ws[r], 16 * u + i) >> (8 * g);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) sx[t] = (uint32_t)__shfl((int)xs[t], 16 * u + i) >> (8 * g);
-#pragma unroll
-                for (int r = 0; r < RT; ++r)
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) acc[r][t] = mfma_mx4<0, 0>(w[r][u], x[t][u], acc[r][t], sw[r], sx[t]);
+                for (int t = 0; t < NT; ++t) o.xs[t] = ld_scales<FULL>(ps, pso[t], b0, g & 1);
             }
         } else {
-            const int64_t b0 = k0 / kMxBlock;
-            uint4 w[RT][4];
-            uint32_t ws[RT];
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                ws[r] = ld_scales<FULL>(qsrow[r], b0);
+            for (int u = 0; u < UX; ++u)
 #pragma unroll
-                for (int u = 0; u < 4; ++u) w[r][u] = ld_block<FULL>(qrow[r], b0 + 4 * u + g);
-            }
+                for (int t = 0; t < NT; ++t) o.x[t][u] = ld_row<FULL>(p, po[t], k0, 64 * u);
+        }
+    }
+
+    // Scale dword (blocks 4 u .. 4 u + 3 of the step) of this lane's row: row
+    // tile r of the weights, or RT + t of the tokens; `at` is the LDS offset in
+    // a row's scales of the step's first block
+    __device__ __forceinline__ uint32_t scales(uint32_t own, int tile, int at, int u) const {
+        if constexpr (SHARED) return *reinterpret_cast<const uint32_t*>(sc + (16 * tile + i) * kScaleRow + at + 4 * u);
+        else return MX ? (uint32_t)__shfl((int)own, 16 * u + i) : own;
+    }
+
+    template <bool ODD>
+    __device__ __forceinline__ void products(const Ops& o, int at) {
+        if constexpr (MODE == MM_16) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                uint4 x[NT][4];
-                const int64_t k = k0 + 32 * (4 * u + g);
+            for (int u = 0; u < UW; ++u)
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int r = 0; r < RT; ++r)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        x[t][j] = FULL ? ld16(prow[t] + (k + 8 * j) * 2) : ld8(prow[t], k + 8 * j, a.C);
+                    for (int t = 0; t < NT; ++t) acc[r][t] = mfma16<DT>(o.w[r][u], o.x[t][u], acc[r][t]);
+        } else if constexpr (MX) {
+            uint32_t sx[NT][UW];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int u = 0; u < UW; ++u)
+                    sx[t][u] = scales(o.xs[t], RT + t, at, u) >> (8 * g);
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int u = 0; u < UW; ++u) {
+                    const uint32_t sw = scales(o.ws[r], r, at, u) >> (8 * g);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) acc[r][t] = mfma_mx4<0, 0>(o.w[r][u], o.x[t][u], acc[r][t], sw, sx[t][u]);
+                }
+        } else {
+#pragma unroll
+            for (int u = 0; u < UW; ++u)
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
-                    const uint32_t s = ((uint32_t)__shfl((int)ws[r], 16 * u + i) >> (8 * g)) & 0xFFu;
-                    const uint32_t d[4] = {w[r][u].x, w[r][u].y, w[r][u].z, w[r][u].w};
-                    if (__builtin_expect(!__any(s - kSafeLo<DT> > kSafeHi<DT> - kSafeLo<DT>), 1)) {
-                        const float f = __uint_as_float(s << 23);
+                    uint32_t d[4] = {o.w[r][u].x, o.w[r][u].y, o.w[r][u].z, o.w[r][u].w};
+                    transpose4(d);
+                    const uint32_t s4 = scales(o.ws[r], r, at, u);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint4 v = mx4_widen<DT>(d[j], f);
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t s = (s4 >> (8 * j)) & 0xFFu;
+                        if constexpr (!ODD) {
+                            odd |= s - kSafeLo<DT> > kSafeHi<DT> - kSafeLo<DT>;
+                            const uint4 v = mx4_widen<DT>(d[j], __uint_as_float(s << 23));
 #pragma unroll
-                            for (int t = 0; t < NT; ++t) acc[r][t] = mfma16<DT>(v, x[t][j], acc[r][t]);
-                        }
-                    } else {
-                        // one block of each row at a time, unscaled, its sum scaled in fp32
-                        for (int b = 0; b < 4; ++b) {
-                            f32x4 sum[NT];
+                            for (int t = 0; t < NT; ++t) acc[r][t] = mfma16<DT>(v, o.x[t][4 * u + j], acc[r][t]);
+                        } else {
+                            const uint4 v = mx4_widen<DT>(d[j], 1.0f);
+                            f32x4 f;
 #pragma unroll
-                            for (int t = 0; t < NT; ++t) sum[t] = f32x4{0, 0, 0, 0};
+                            for (int e = 0; e < 4; ++e) f[e] = e8m0_to_f32((uint32_t)__shfl((int)s, 4 * g + e));
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint4 z = make_uint4(0, 0, 0, 0);
-                                const uint4 v = g == b ? mx4_widen<DT>(d[j], 1.0f) : z;
-#pragma unroll
-                                for (int t = 0; t < NT; ++t) sum[t] = mfma16<DT>(v, g == b ? x[t][j] : z, sum[t]);
-                            }
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float f = e8m0_to_f32((uint32_t)__shfl((int)s, 16 * b + 4 * g + e));
-#pragma unroll
-                                for (int t = 0; t < NT; ++t) acc[r][t][e] += f * sum[t][e];
-                            }
+                            for (int t = 0; t < NT; ++t)
+                                acc[r][t] += f * mfma16<DT>(v, o.x[t][4 * u + j], f32x4{0, 0, 0, 0});
                         }
                     }
                 }
+        }
+    }
+
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[r][t] = f32x4{0, 0, 0, 0};
+    }
+
+    // This wave's part of the contraction: steps wave, wave + kWaves, ..  ODD
+    // (mx4 weights against 16-bit activations): the elements unscaled, their
+    // sums scaled in fp32.
+    template <bool ODD>
+    __device__ __forceinline__ void run_steps(int wave) {
+        // a block that K ends inside is whole in an mx4 operand, not in a 16-bit one
+        const int64_t whole = (MX ? nb * kMxBlock : a.C) / S, steps = (a.C + S - 1) / S;
+        int64_t n = wave;
+        Ops o;
+        for (; n < whole; n += kWaves) {
+            load<true>(n * S, o);
+            products<ODD>(o, 0);
+        }
+        if (n < steps) {
+            load<false>(n * S, o);
+            products<ODD>(o, 0);
+        }
+    }
+
+    // The same with shared scales: slice `wave` of every round.  Every wave
+    // takes part in the barriers.
+    template <bool ODD>
+    __device__ __forceinline__ void run_rounds(int wave) {
+        const int64_t whole = MX ? nb * kMxBlock : a.C;
+        // rounds of equal length, a wave's slices of them whole steps
+        const int64_t rounds = (a.C + kRound - 1) / kRound;
+        const int slice = (int)(((a.C + rounds * kWaves - 1) / (rounds * kWaves) + S - 1) / S * S);
+        for (int64_t n = 0; n < rounds; ++n) {
+            const int64_t k0 = (n * kWaves + wave) * slice;
+            uint4 v[SPT];
+            load_scales(n * kWaves * slice / kMxBlock, v);
+            Ops o;
+            if (k0 < a.C) {            // the first step's loads are under way while the scales arrive
+                if (k0 + S <= whole) load<true>(k0, o);
+                else load<false>(k0, o);
+            }
+            if (n > 0) lds_barrier();  // every wave has read the last round's scales
+            store_scales(v);
+            lds_barrier();
+#pragma unroll 1                           // unrolled, its registers cost half the waves
+            for (int h = 0; h < slice; h += S) {
+                const int64_t k = k0 + h;
+                if (k >= a.C) break;
+                if (h > 0) {
+                    if (k + S <= whole) load<true>(k, o);
+                    else load<false>(k, o);
+                }
+                products<ODD>(o, (wave * slice + h) / kMxBlock);
             }
         }
     }
 };
 
 template <int MODE, int DT, int RT, int NT>
-__global__ void __launch_bounds__(kThreads) k_mm_skinny(MmArgs a, uint32_t nq) {
-    __shared__ f32x4 red[kWaves][RT * NT * 64];
+// (two workgroups of 64 rows x 16 tokens on a CU: within 128 registers)
+__global__ void __launch_bounds__(kThreads, RT == 4 && NT == 1 ? 4 : 2) k_mm_skinny(MmArgs a, uint32_t nq) {
+    using K = Skinny<MODE, DT, RT, NT>;
+    constexpr int kRed = kWaves * RT * NT * 64 * 16, kSc = K::SHARED ? K::SROWS * kScaleRow : 0;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kRed > kSc ? kRed : kSc];   // the scales, then the waves' sums
+    f32x4(*const red)[RT * NT * 64] = reinterpret_cast<f32x4(*)[RT * NT * 64]>(lds);
     const uint32_t tt = blockIdx.x / nq, qt = blockIdx.x - tt * nq;
     MmTile tile;
     if (!mm_find_tile(a, 16 * NT, (int)tt, &tile)) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t q0 = (int64_t)qt * 16 * RT;
-    Skinny<MODE, DT, RT, NT> k{a};
+    K k{a};
+    k.sc = lds;
+    k.qrows = a.Q - q0;
+    k.prow0 = tile.v0 - tile.r0;
+    k.prows = tile.r1 - tile.r0;
     k.i = lane & 15;
     k.g = lane >> 4;
     k.nb = (a.C + kMxBlock - 1) / kMxBlock;
     const int64_t e = tile.e < 0 ? 0 : tile.e;
+    k.q = a.q + e * a.strideq + q0 * a.ldq;
+    k.p = a.p + tile.r0 * a.ldp;
+    k.qs = MODE != MM_16 ? a.qs + e * a.strideqs + q0 * a.ldqs : nullptr;
+    k.ps = MODE == MM_MX4 ? a.ps + tile.r0 * a.ldps : nullptr;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-        const int64_t row = std::min<int64_t>(q0 + 16 * r + k.i, a.Q - 1);
-        k.qrow[r] = a.q + e * a.strideq + row * a.ldq;
-        if constexpr (MODE != MM_16) k.qsrow[r] = a.qs + e * a.strideqs + row * a.ldqs;
+        const int64_t row = std::min<int64_t>(16 * r + k.i, a.Q - 1 - q0);
+        k.qo[r] = (uint32_t)(row * a.ldq);
+        k.qso[r] = (uint32_t)(row * a.ldqs);
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const int64_t row = std::max(tile.v0, std::min<int64_t>(tile.r0 + 16 * t + k.i, tile.r1 - 1));
-        k.prow[t] = a.p + row * a.ldp;
-        if constexpr (MODE == MM_MX4) k.psrow[t] = a.ps + row * a.ldps;
+        const int64_t row = std::max(tile.v0, std::min<int64_t>(tile.r0 + 16 * t + k.i, tile.r1 - 1)) - tile.r0;
+        k.po[t] = (uint32_t)(row * a.ldp);
+        k.pso[t] = (uint32_t)(row * a.ldps);
     }
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) k.acc[r][t] = f32x4{0, 0, 0, 0};
+    k.zero();
     if (tile.e >= 0) {
-        constexpr int S = kStep<MODE>;
-        // a block that K ends inside is whole in an mx4 operand, not in a 16-bit one
-        const int64_t whole = MODE == MM_MX4 ? k.nb * kMxBlock : a.C;
-        for (int64_t k0 = (int64_t)wave * S; k0 < a.C; k0 += kWaves * S) {
-            if (k0 + S <= whole) k.template step<true>(k0);
-            else k.template step<false>(k0);
+        k.odd = false;
+        if constexpr (K::SHARED) {
+            k.template run_rounds<false>(wave);
+            if constexpr (MODE == MM_W4) {
+                if (__syncthreads_or(k.odd)) {
+                    k.zero();
+                    k.template run_rounds<true>(wave);
+                }
+            }
+            __syncthreads();           // the scales give way to the sums
+        } else {
+            k.template run_steps<false>(wave);
+            if constexpr (MODE == MM_W4) {
+                if (__any(k.odd)) {
+                    k.zero();
+                    k.template run_steps<true>(wave);
+                }
+            }
         }
     }
 #pragma unroll
@@ -258,8 +416,9 @@ hipError_t go(const MmArgs& a, hipStream_t s) {
 
 template <int MODE, int DT>
 hipError_t pick(const MmArgs& a, int rt, int nt, hipStream_t s) {
-    if (nt == 1) return rt == 1 ? go<MODE, DT, 1, 1>(a, s) : go<MODE, DT, 2, 1>(a, s);
-    return rt == 1 ? go<MODE, DT, 1, 2>(a, s) : go<MODE, DT, 2, 2>(a, s);
+    if (rt == 1) return nt == 1 ? go<MODE, DT, 1, 1>(a, s) : go<MODE, DT, 1, 2>(a, s);
+    if (rt == 2) return nt == 1 ? go<MODE, DT, 2, 1>(a, s) : go<MODE, DT, 2, 2>(a, s);
+    return nt == 1 ? go<MODE, DT, 4, 1>(a, s) : go<MODE, DT, 4, 2>(a, s);
 }
 
 }  // namespace

@@ -8,7 +8,7 @@
 // out-of-range offsets read as zero, so ragged edges need no branch.  A wave
 // reads the 16-row fragments of stage i + 1 into registers while it multiplies
 // those of stage i, so stage i's slot is free as soon as the barrier that opens
-// stage i has passed: with a ring of kRing = 4 slots the loads run up to four
+// stage i has passed: with a ring of 4 slots the loads run up to four
 // stages ahead, which covers their latency (two whole stages of 128 bytes a
 // row, the same LDS, left it exposed: bf16 8 x 4096 x 4096 with 8192 tokens
 // took 345 us).
@@ -52,7 +52,6 @@ namespace ssg {
 
 constexpr int kMmGroupP = 8;           // row tiles walked together
 constexpr int kMmCUs = 256;
-constexpr int kRing = 4;
 
 __device__ __forceinline__ int mm_swz(int i) { return ((i ^ (i >> 1)) & 1) | ((i >> 1) & 2); }
 
@@ -190,16 +189,20 @@ struct MmWork {
 template <int MODE, int TQ, int TP, int WQ, int WP>
 struct MmLay {
     static constexpr int NW = WQ * WP;
+    // stages in the ring (eight of the small tile's gain nothing: 18.5 against
+    // 18.9 us at 4096 x 4096 with 32 tokens, bf16)
+    static constexpr int kRing = 4;
     static constexpr int FQ = TQ / WQ / 16, FP = TP / WP / 16;       // fragments per wave
     static constexpr bool W4 = MODE == MM_W4, MX = MODE == MM_MX4;
     static constexpr int Q_BYTES = TQ * 64, P_BYTES = TP * 64;
     static constexpr int QS_BYTES = MX || W4 ? 1024 : 0, PS_BYTES = MX ? 1024 : 0;
     // a ring slot holds a stage's P (and Q); mx4 weights against 16-bit
-    // activations have two slots of their own, each for four stages
+    // activations have slots of their own, each for four stages
     static constexpr int P_AT = W4 ? 0 : Q_BYTES, QS_AT = P_AT + P_BYTES, PS_AT = QS_AT + (W4 ? 0 : QS_BYTES);
     static constexpr int STAGE = PS_AT + PS_BYTES;
     static constexpr int W_AT = kRing * STAGE, W_SLOT = Q_BYTES + QS_BYTES;
-    static constexpr int LDS = kRing * STAGE + (W4 ? 2 * W_SLOT : 0);
+    static constexpr int WS = kRing / 4 + 1;                          // those slots
+    static constexpr int LDS = kRing * STAGE + (W4 ? WS * W_SLOT : 0);
     static constexpr int QL = Q_BYTES / 1024 / NW, PL = P_BYTES / 1024 / NW;
     static constexpr int VM = W4 ? PL : QL + PL + (MX ? 1 : 0);      // loads per wave and stage
     static constexpr int VMW = W4 ? QL + 1 : 0;                       // and per four stages of weights
@@ -273,7 +276,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
     __amdgpu_buffer_rsrc_t rq, rp;
     auto load = [&](auto uc, int it) {
         constexpr int U = decltype(uc)::value, NQ = W4 ? 0 : L::QL;
-        const uint32_t dst = lds32 + (it & (kRing - 1)) * L::STAGE;
+        const uint32_t dst = lds32 + (it & (L::kRing - 1)) * L::STAGE;
         if constexpr (U < NQ) {
             if constexpr (U == 0) rq = lq.open(it);
             lq.template load<U>(rq, it, dst, wave);
@@ -286,7 +289,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
     };
     auto issue = [&](int it) { mm_for<L::VM>([&](auto u) { load(u, it); }); };
     auto issue_w = [&](int grp) {
-        const uint32_t dst = lds32 + L::W_AT + (grp & 1) * L::W_SLOT;
+        const uint32_t dst = lds32 + L::W_AT + grp % L::WS * L::W_SLOT;
         rq = lq.open(grp);
         mm_for<L::QL>([&](auto u) { lq.template load<decltype(u)::value>(rq, grp, dst, wave); });
         lw.issue(grp, dst + L::Q_BYTES);
@@ -324,8 +327,8 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
     constexpr int NS = MX ? SQ + SP : 0, NRD = NS + L::FQ + L::FP;
     auto read = [&](auto uc, int it, Ops& o) {
         constexpr int U = decltype(uc)::value;
-        const uint8_t* st = lds + (it & (kRing - 1)) * L::STAGE;
-        const uint8_t* ws = lds + L::W_AT + ((it >> 2) & 1) * L::W_SLOT;   // W4 only
+        const uint8_t* st = lds + (it & (L::kRing - 1)) * L::STAGE;
+        const uint8_t* ws = lds + L::W_AT + (it >> 2) % L::WS * L::W_SLOT;   // W4 only
         const int b = it & 3;                                              // W4: block of the group
         if constexpr (U < NS) {
             if constexpr (U < SQ)
@@ -348,7 +351,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
         }
     };
     auto row_scales = [&](int it, int x) -> uint32_t {   // W4
-        return *reinterpret_cast<const uint32_t*>(lds + L::W_AT + ((it >> 2) & 1) * L::W_SLOT + L::Q_BYTES +
+        return *reinterpret_cast<const uint32_t*>(lds + L::W_AT + (it >> 2) % L::WS * L::W_SLOT + L::Q_BYTES +
                                                   (fq0 + x) * 64 + i * 4);
     };
     bool odd = false;                  // W4: this lane met a scale outside the safe range
@@ -376,11 +379,15 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
     };
 
     if (w.nst > 0) {
+        // (W4) the weights of group m follow the activations of stage 4 m - 1,
+        // here and in the loop
         if constexpr (W4) issue_w(0);
 #pragma unroll
-        for (int s = 0; s < kRing; ++s) issue(s);
-        if constexpr (W4) issue_w(1);
-        wait_vm<(kRing - 1) * L::VM + L::VMW>();
+        for (int s = 0; s < L::kRing; ++s) {
+            issue(s);
+            if (W4 && s % 4 == 3) issue_w(s / 4 + 1);
+        }
+        wait_vm<(L::kRing - 1) * L::VM + L::kRing / 4 * L::VMW>();
         lds_barrier();
         Ops o[2];
         mm_for<NRD>([&](auto u) { read(u, 0, o[0]); });
@@ -390,15 +397,15 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
         }
         // One stage: stage it + 1 has landed and every wave has read stage it.
         // Its products in FP groups, the first half of which also read the next
-        // stage's operands, and all of which share the loads of stage it + kRing:
+        // stage's operands, and all of which share the loads of stage it + ring:
         // issued in one burst after the barrier, the loads' scalar instructions
         // kept the matrix unit waiting in all waves at once.
-        constexpr int V = (kRing - 2) * L::VM;
+        constexpr int V = (L::kRing - 2) * L::VM;
         constexpr int RPG = (NRD + (NG + 1) / 2 - 1) / ((NG + 1) / 2), LPG = (L::VM + NG - 1) / NG;
         auto stage = [&](int it, Ops& cur, Ops& nxt, auto bc) {
             constexpr int B = decltype(bc)::value;   // W4: stage of the group
             constexpr bool last_of_4 = W4 && B == 3;
-            wait_vm<V + (B < 3 ? L::VMW : 0)>();
+            wait_vm<V + (L::kRing / 4 - (B < 3 ? 0 : 1)) * L::VMW>();
             lds_barrier();
             uint4 v = make_uint4(0, 0, 0, 0), vn = v;
             if constexpr (W4) v = widen(std::integral_constant<int, 0>{}, B, cur);
@@ -412,7 +419,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
                 });
                 mm_for<LPG>([&](auto k) {
                     constexpr int U = G * LPG + decltype(k)::value;
-                    if constexpr (U < L::VM) load(std::integral_constant<int, U>{}, it + kRing);
+                    if constexpr (U < L::VM) load(std::integral_constant<int, U>{}, it + L::kRing);
                 });
                 v = vn;
                 __builtin_amdgcn_sched_barrier(0);
@@ -422,12 +429,12 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
 #pragma unroll
                 for (int x = 0; x < L::FQ; ++x) wsc[x] = row_scales(it + 1, x);
             }
-            if constexpr (last_of_4) issue_w((it >> 2) + 2);
+            if constexpr (last_of_4) issue_w((it >> 2) + L::WS);
         };
         if constexpr (W4) {
-            // the weights of group gr + 1 are issued after the activations of
-            // stage 4 gr + 3, so they may be outstanding in the first three
-            // stages of group gr
+            // so the weights issued after the next stage's activations, one
+            // group for each four stages of the ring, may be outstanding with
+            // the activations; the last stage of a group needs the oldest of them
             for (int gr = 0; gr < groups; ++gr) {
                 stage(4 * gr, o[0], o[1], std::integral_constant<int, 0>{});
                 stage(4 * gr + 1, o[1], o[0], std::integral_constant<int, 1>{});
