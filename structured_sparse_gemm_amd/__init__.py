@@ -1023,9 +1023,31 @@ def ssg_grouped_mm_dw(dY, X, offs, dW, ws=None, stream=None) -> None:
     _run_with_workspace("ssg_grouped_mm_dw", ops, dW, _stack(dW, "dW"), ws, stream)
 
 
+class _Unbuilt:
+    """Stands for the compiled marshalling where it is not built: takes no call."""
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+_calls = None
+
+
+def _compiled():
+    """The compiled marshalling of these calls.  It returns None for a call that
+    it does not take; the binding then makes the call itself."""
+    global _calls
+    if _calls is None:
+        _calls = _abi.torch_calls() or _Unbuilt()
+    return _calls
+
+
 def mx4_quantize(A: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(elements, scales) of A [R, K] or a stack [E, R, K] in the mx4 format:
     uint8 [.., 16 * ceil(K / 32)] and uint8 [.., ceil(K / 32)]."""
+    if stream is None:
+        done = (_calls or _compiled()).mx4_quantize(A)
+        if done is not None:
+            return done
     if A.dim() == 3:
         e, s = mx4_quantize(A.reshape(-1, A.shape[2]), stream)
         return e.view(*A.shape[:2], -1), s.view(*A.shape[:2], -1)
@@ -1040,6 +1062,10 @@ def mx4_quantize(A: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tens
 def mx4_dequantize(elems: torch.Tensor, scales: torch.Tensor, K: int, dtype: torch.dtype = torch.float32,
                    stream=None) -> torch.Tensor:
     """The values of mx4 rows [R, K] (or of a stack [E, R, K]) in `dtype`."""
+    if stream is None:
+        done = (_calls or _compiled()).mx4_dequantize(elems, scales, K, dtype)
+        if done is not None:
+            return done
     if elems.dim() == 3:
         d = mx4_dequantize(elems.reshape(-1, elems.shape[2]), scales.reshape(-1, scales.shape[2]), K, dtype, stream)
         return d.view(*elems.shape[:2], K)
@@ -1052,6 +1078,10 @@ def mx4_dequantize(elems: torch.Tensor, scales: torch.Tensor, K: int, dtype: tor
 def mm_mx4(X, W, scales, xscales=None, out_dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
     """X W^T with mx4 weights W [M, K]: X [N, K] fp16 / bf16, or mx4 elements with
     their scales in xscales.  Returns [N, M]; fp32 sums, rounded to out_dtype."""
+    if stream is None:
+        Y = (_calls or _compiled()).mx4_product(X, xscales, W, scales, None, out_dtype)
+        if Y is not None:
+            return Y
     Y = _empty((X.shape[0], W.shape[0]), out_dtype, X, stream)
     ssg_mm_mx4(X, W, scales, Y, xscales=xscales, stream=stream)
     return Y
@@ -1061,6 +1091,10 @@ def grouped_mm_mx4(X, W, scales, offs, xscales=None, out_dtype: torch.dtype = to
                    stream=None) -> torch.Tensor:
     """Rows offs[e] .. offs[e + 1] - 1 of X times W[e]^T, mx4 weights W [E, M, K]
     (see mm_mx4); rows of no expert are zero."""
+    if stream is None:
+        Y = (_calls or _compiled()).mx4_product(X, xscales, W, scales, offs, out_dtype)
+        if Y is not None:
+            return Y
     _need(W.dim() == 3, "W must be 3-D", W)
     Y = _empty((X.shape[0], W.shape[1]), out_dtype, X, stream)
     ssg_grouped_mm_mx4(X, W, scales, offs, Y, xscales=xscales, stream=stream)
@@ -1071,6 +1105,10 @@ def grouped_mm(X, W, offs, out_dtype: Optional[torch.dtype] = None, stream=None)
     """Rows offs[e] .. offs[e + 1] - 1 of X [N, K] times W[e]^T, W [E, M, K]; both
     fp16 or both bf16.  Returns [N, M] in out_dtype (X's type or fp32; None:
     X's type); rows of no expert are zero."""
+    if stream is None:
+        Y = (_calls or _compiled()).grouped_product(0, X, W, offs, out_dtype or X.dtype)
+        if Y is not None:
+            return Y
     _need(W.dim() == 3, "W must be 3-D", W)
     Y = _empty((X.shape[0], W.shape[1]), out_dtype or X.dtype, X, stream)
     ssg_grouped_mm(X, W, offs, Y, stream=stream)
@@ -1079,6 +1117,10 @@ def grouped_mm(X, W, offs, out_dtype: Optional[torch.dtype] = None, stream=None)
 
 def grouped_mm_dx(dY, W, offs, out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
     """Gradient of grouped_mm with respect to X: rows of dY [N, M] times W[e]."""
+    if stream is None:
+        dX = (_calls or _compiled()).grouped_product(1, dY, W, offs, out_dtype or dY.dtype)
+        if dX is not None:
+            return dX
     _need(W.dim() == 3, "W must be 3-D", W)
     dX = _empty((dY.shape[0], W.shape[2]), out_dtype or dY.dtype, dY, stream)
     ssg_grouped_mm_dx(dY, W, offs, dX, stream=stream)
@@ -1088,6 +1130,10 @@ def grouped_mm_dx(dY, W, offs, out_dtype: Optional[torch.dtype] = None, stream=N
 def grouped_mm_dw(dY, X, offs, out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
     """Gradient of grouped_mm with respect to W: [E, M, K], for each expert the
     sum over its rows of dY[n] X[n]^T (zeros for an expert without rows)."""
+    if stream is None:
+        dW = (_calls or _compiled()).grouped_product(2, dY, X, offs, out_dtype or dY.dtype)
+        if dW is not None:
+            return dW
     _need(dY.dim() == 2 and X.dim() == 2 and offs.dim() == 1 and offs.shape[0] > 0, "shapes of dY, X, offs", dY, X, offs)
     dW = _empty((offs.shape[0] - 1, dY.shape[1], X.shape[1]), out_dtype or dY.dtype, dY, stream)
     ssg_grouped_mm_dw(dY, X, offs, dW, stream=stream)

@@ -127,3 +127,14 @@ def load(path: str = LIB_PATH):
                 raise RuntimeError("libssgemm ABI version %d, expected 1" % lib.ssg_abi_version())
             _lib = lib
     return _lib
+
+
+def torch_calls():
+    """The compiled marshalling of the mx4 and expert-grouped calls, or None
+    where it is not built (the calls are then marshalled in Python)."""
+    load()
+    try:
+        from . import _torch_calls
+    except ImportError:
+        return None
+    return _torch_calls

@@ -3,8 +3,9 @@
     python -m structured_sparse_gemm_amd.build
 
 compiles every source under csrc/ with hipcc and links
-structured_sparse_gemm_amd/libssgemm.so.  Objects go to _build/ at the
-repository root.
+structured_sparse_gemm_amd/libssgemm.so, then the torch marshalling of the
+mx4 and expert-grouped calls (csrc/binding) into _torch_calls.so beside it.
+Objects go to _build/ at the repository root.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build", "ssgemm")
 LIB = os.path.join(PKG, "libssgemm.so")
+CALLS = os.path.join(PKG, "_torch_calls.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -58,9 +61,29 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
     os.replace(tmp, LIB)
+    build_calls()
     if verbose:
         print("built", LIB)
     return LIB
+
+
+def build_calls() -> str:
+    """Compile the torch marshalling against the installed torch and this library."""
+    import torch
+    tdir = os.path.dirname(torch.__file__)
+    tmp = CALLS + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1",
+           "-DUSE_ROCM=1", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I", INCLUDE,
+           "-I", os.path.join(tdir, "include"), "-I", os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include"),
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "binding", "torch_calls.cpp"), "-o", tmp,
+           "-L", PKG, "-l:" + os.path.basename(LIB), "-L", os.path.join(tdir, "lib"), "-lc10", "-lc10_hip",
+           "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
+    os.replace(tmp, CALLS)
+    return CALLS
 
 
 if __name__ == "__main__":

@@ -196,3 +196,45 @@ def test_captured_step_replays():
         for a, b in zip(outs, step()):
             assert torch.equal(a, b)
         torch.cuda.synchronize()
+
+
+def test_compiled_and_python_marshalling_agree():
+    # the compiled path takes the call without a stream, the Python one the call
+    # with the current stream named: the same bits, also where a workspace is needed
+    cur = torch.cuda.current_stream()
+    for dt, sizes, M, K in [("bf16", [3, 0, 5], 72, 64), ("f16", [90, 40], 264, 1001), ("bf16", [30], 512, 2048)]:
+        X, W, dY, offs = case(dt, sizes, M, K, 3)
+        Xg, Wg, dYg, og = X.cuda(), W.cuda(), dY.cuda(), offs.cuda()
+        for f, a in [(ssg.grouped_mm, (Xg, Wg, og)), (ssg.grouped_mm_dx, (dYg, Wg, og)), (ssg.grouped_mm_dw, (dYg, Xg, og))]:
+            for out in (None, torch.float32):
+                assert torch.equal(f(*a, out_dtype=out), f(*a, out_dtype=out, stream=cur))
+        e, s = ssg.mx4_quantize(Wg)
+        e1, s1 = ssg.mx4_quantize(Xg)
+        e2, s2 = ssg.mx4_quantize(Xg, stream=cur)
+        assert torch.equal(e1, e2) and torch.equal(s1, s2)
+        assert torch.equal(ssg.mx4_dequantize(e1, s1, K), ssg.mx4_dequantize(e1, s1, K, stream=cur))
+        assert torch.equal(ssg.grouped_mm_mx4(Xg, e, s, og), ssg.grouped_mm_mx4(Xg, e, s, og, stream=cur))
+        assert torch.equal(ssg.mm_mx4(Xg, e[0], s[0]), ssg.mm_mx4(Xg, e[0], s[0], stream=cur))
+        if K % 32 == 0:
+            assert torch.equal(ssg.mm_mx4(e1, e[0], s[0], xscales=s1), ssg.mm_mx4(e1, e[0], s[0], xscales=s1, stream=cur))
+
+
+def test_refusals_on_the_device():
+    X, W, dY, offs = (t.cuda() for t in case("f16", [4, 4], 24, 32, 1))
+    e, s = ssg.mx4_quantize(W)
+
+    def status(f, *a, **k):
+        with pytest.raises(ssg.SsgError) as err:
+            f(*a, **k)
+        return err.value.status
+
+    assert status(ssg.grouped_mm, X, W, offs.long()) == 4
+    assert status(ssg.grouped_mm, X, W, offs[:2]) == 2
+    assert status(ssg.grouped_mm, X, W, offs, out_dtype=torch.bfloat16) == 4
+    assert status(ssg.grouped_mm, X, W.transpose(1, 2), offs) in (2, 3)
+    assert status(ssg.grouped_mm, X.t().contiguous().t(), W, offs) == 3
+    assert status(ssg.grouped_mm_dx, X, W, offs) == 2
+    assert status(ssg.grouped_mm_dw, dY, X[:4], offs) == 2
+    assert status(ssg.grouped_mm_mx4, X, e, s[:, :, :0], offs) == 2
+    assert status(ssg.mm_mx4, X, e[0], s[0], out_dtype=torch.bfloat16) == 4
+    assert status(ssg.mx4_quantize, X.double()) == 4

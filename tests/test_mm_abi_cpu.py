@@ -150,3 +150,20 @@ def test_python_refusals():
     assert status(ssg.grouped_mm, h, w[0], offs) == SHAPE
     assert status(ssg.grouped_mm_dx, h, w, offs) == SHAPE
     assert status(ssg.grouped_mm_dw, h, h[:3], offs) == SHAPE
+
+
+def test_compiled_calls_take_only_device_tensors():
+    # built beside the library; anything it does not take is left to the
+    # Python binding, which says what is wrong
+    calls = _abi.torch_calls()
+    assert calls is not None
+    h, u, s = torch.zeros(4, 64, dtype=torch.float16), torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(8, 2, dtype=torch.uint8)
+    w, offs = torch.zeros(2, 8, 64, dtype=torch.float16), torch.zeros(3, dtype=torch.int32)
+    assert calls.mx4_quantize(h) is None and calls.mx4_quantize(None) is None and calls.mx4_quantize(h, h) is None
+    assert calls.mx4_dequantize(u, s, 64, torch.float16) is None
+    assert calls.mx4_dequantize(u, s, "64", torch.float16) is None and calls.mx4_dequantize(u, s, 64, 1) is None
+    assert calls.mx4_product(h, None, u, s, None, torch.float32) is None
+    assert calls.mx4_product(h, None, u, s, offs, 3) is None and calls.mx4_product(1, 2, 3) is None
+    for kind in (0, 1, 2):
+        assert calls.grouped_product(kind, h, w, offs, torch.float16) is None
+        assert calls.grouped_product(kind, "x", w, offs, torch.float16) is None
