@@ -211,25 +211,24 @@ struct MmLay {
     static_assert(LDS <= 160 * 1024, "LDS");
 };
 
-// Sixteen (n) consecutive outputs.
-__device__ __forceinline__ void mm_store16(void* y, int out, int64_t at, int n, bool vec, const f32x4 (&v)[4]) {
-    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-    if (out != OUT_F32 && vec && n >= 16) {
-        union { f16x4 h[4]; bf16x4 b[4]; uint4 u[2]; } w;
+// 16 bytes of outputs (n of the elements that they hold exist) to any address.
+template <int ES>
+__device__ __forceinline__ void mm_store_chunk(uint8_t* at, int64_t n, uint4 v) {
+    if (n * ES >= 16) {
+        __builtin_memcpy(at, &v, 16);
+    } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (out == OUT_F16) w.h[k] = __builtin_convertvector(v[k], f16x4);
-            else w.b[k] = __builtin_convertvector(v[k], bf16x4);
+        for (int k = 0; k < 16 / ES; ++k) {
+            if (k < n) {
+                if constexpr (ES == 4) __builtin_memcpy(at + 4 * k, &w[k], 4);
+                else {
+                    const uint16_t h = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
+                    __builtin_memcpy(at + 2 * k, &h, 2);
+                }
+            }
         }
-        uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(y) + at);
-        d[0] = w.u[0];
-        d[1] = w.u[1];
-        return;
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (n > 4 * k) mm_store4(y, out, at + 4 * k, n - 4 * k, vec, v[k]);
 }
 
 template <int MODE, int DT, bool QT, bool PT, int TQ, int TP, int WQ, int WP>
@@ -489,38 +488,84 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
         }
     }
 
-    // lane (i, g), register r of fragments (x, y): row 16 y + i of the wave's rows
-    // (PT) or 4 i + y % 4 of 64, column 16 x + 4 g + r (QT) or 16 g + 4 r + x % 4 of 64
-    const bool vec = a.part ? a.Q % 4 == 0 : a.ldy % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0 &&
-                                                 a.stridey % 8 == 0;
+    // Lane (i, g), register r of fragments (x, y) is row 16 y + i of the wave's
+    // rows (PT) or 4 i + y % 4 of 64, column 16 x + 4 g + r (QT) or
+    // 16 g + 4 r + x % 4 of 64.  A wave turns its outputs in 8 KiB of LDS, 64
+    // columns of 64 (16-bit) or 32 (fp32) rows at a time, into 16-byte pieces of
+    // rows, so that a store covers whole cache lines: written from the registers
+    // as they are (8 bytes a lane, 16 rows a store), the weight gradient of 8 x
+    // 4096 x 4096 with few rows took 88 us.  16-byte chunk c of row r sits at
+    // chunk c ^ (r % chunks).  (fp32 columns of QT are whole 16 bytes a lane and 64
+    // a row already: 65 us as they are, 89 through LDS at 40 x 1000 x 1416.)
+    lds_barrier();                     // every wave has read its last stage
     void* const out = a.part ? (void*)(a.part + (int64_t)w.split * a.P * a.Q) : a.y;
     const int64_t ldo = a.part ? a.Q : a.ldy, oat = PT && !a.part ? e * a.stridey : 0;
-    const int kind = a.part ? (int)OUT_F32 : a.out;
+    uint8_t* const turn = lds + wave * 8192;
+    auto write_out = [&](auto es, auto half) {
+        constexpr int ES = decltype(es)::value, NY = ES == 2 ? 4 : 2;       // fragments of rows a time
+        constexpr int CH = 64 * ES / 16, YN = NY < L::FP ? NY : L::FP;      // chunks a row
+        constexpr bool HALF = decltype(half)::value;
+        if constexpr (QT && ES == 4) {
+            const bool vec = ldo % 4 == 0 && (oat % 4 == 0) && reinterpret_cast<uintptr_t>(out) % 16 == 0;
 #pragma unroll
-    for (int y = 0; y < L::FP; ++y) {
-        const int fy = fp0 + y;
-        const int64_t p = w.r0 + (PT ? fy * 16 + i : fy / 4 * 64 + 4 * i + fy % 4);
-        if (p < w.v0 || p >= w.r1) continue;
+            for (int y = 0; y < L::FP; ++y) {
+                const int fy = fp0 + y;
+                const int64_t p = w.r0 + (PT ? fy * 16 + i : fy / 4 * 64 + 4 * i + fy % 4);
+                if (p < w.v0 || p >= w.r1) continue;
 #pragma unroll
-        for (int x = 0; x < L::FQ; x += 4) {
-            if constexpr (QT) {
-#pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    const int64_t q = w.q0 + (fq0 + x + f) * 16 + 4 * g;
-                    if (q < a.Q) mm_store4(out, kind, oat + p * ldo + q, a.Q - q < 4 ? (int)(a.Q - q) : 4, vec, acc[x + f][y]);
+                for (int x = 0; x < L::FQ; ++x) {
+                    const int64_t q = w.q0 + (fq0 + x) * 16 + 4 * g;
+                    if (q < a.Q) mm_store4(out, OUT_F32, oat + p * ldo + q, a.Q - q < 4 ? (int)(a.Q - q) : 4, vec, acc[x][y]);
                 }
-            } else {
-                const int64_t q = w.q0 + (fq0 + x) * 16 + 16 * g;
-                if (q < a.Q) {
-                    f32x4 v[4];
+            }
+            return;
+        }
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        v[r] = f32x4{acc[x][y][r], acc[x + 1][y][r], acc[x + 2][y][r], acc[x + 3][y][r]};
-                    mm_store16(out, kind, oat + p * ldo + q, a.Q - q < 16 ? (int)(a.Q - q) : 16, vec, v);
+        for (int xg = 0; xg < L::FQ; xg += 4) {
+#pragma unroll
+            for (int yg = 0; yg < L::FP; yg += YN) {
+#pragma unroll
+                for (int yy = 0; yy < YN; ++yy) {
+                    // LDS row of this lane's outputs
+                    const int row = PT ? yy * 16 + i : YN == 4 ? 4 * i + yy : YN * i + yy;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const f32x4 v = QT ? acc[xg + k][yg + yy]
+                                           : f32x4{acc[xg][yg + yy][k], acc[xg + 1][yg + yy][k], acc[xg + 2][yg + yy][k],
+                                                   acc[xg + 3][yg + yy][k]};
+                        const int col = QT ? 16 * k + 4 * g : 16 * g + 4 * k;
+                        const int at = col * ES, ch = (at >> 4) ^ (row & (CH - 1));
+                        uint8_t* const d = turn + row * (64 * ES) + (ch << 4) + (at & 15);
+                        if constexpr (ES == 4) {
+                            *reinterpret_cast<f32x4*>(d) = v;
+                        } else {
+                            typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+                            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+                            // one rounding to nearest even after the fp32 sums
+                            if constexpr (HALF) *reinterpret_cast<f16x4*>(d) = __builtin_convertvector(v, f16x4);
+                            else *reinterpret_cast<bf16x4*>(d) = __builtin_convertvector(v, bf16x4);
+                        }
+                    }
+                }
+                constexpr int RPI = 64 / CH;                                // rows a store
+#pragma unroll
+                for (int n = 0; n < YN * 16 / RPI; ++n) {
+                    const int row = n * RPI + lane / CH, c = lane % CH;
+                    const uint4 v = *reinterpret_cast<const uint4*>(turn + row * (64 * ES) + ((c ^ (row & (CH - 1))) << 4));
+                    // row of the tile: the wave's rows are 16 FP from 16 fp0 on (PT), or
+                    // every (4 / YN)th of the 64-row groups its fragments belong to
+                    const int f = fp0 + yg;
+                    const int64_t p = w.r0 + (PT ? f * 16 + row : f / 4 * 64 + (YN == 4 ? row : row / YN * 4 + row % YN + f % 4));
+                    const int64_t q = w.q0 + (fq0 + xg) * 16 + c * (16 / ES);
+                    if (p >= w.v0 && p < w.r1 && q < a.Q)
+                        mm_store_chunk<ES>(reinterpret_cast<uint8_t*>(out) + (oat + p * ldo + q) * ES, a.Q - q, v);
                 }
             }
         }
-    }
+    };
+    if (a.part || a.out == OUT_F32) write_out(std::integral_constant<int, 4>{}, std::false_type{});
+    else if (a.out == OUT_F16) write_out(std::integral_constant<int, 2>{}, std::true_type{});
+    else write_out(std::integral_constant<int, 2>{}, std::false_type{});
 }
 
 // Tile (pt, qt) of T.p x T.q tiles, walked kMmGroupP row tiles at a time.
@@ -531,6 +576,27 @@ __device__ __forceinline__ void mm_walk(uint32_t id, uint32_t np, uint32_t nq, u
     *pt = grp * kMmGroupP + in - *qt * gsz;
 }
 
+// The expert with the n-th most rows (ties by number).  A tile of the weight
+// gradient takes as long as its expert has rows, so the large ones go first:
+// begun last, one alone would keep the launch going.
+__device__ __forceinline__ uint32_t mm_by_size(const MmArgs& a, uint32_t n) {
+    if (!a.offs || a.E > 64) return n;
+    const int lane = threadIdx.x & 63;
+    int64_t lo = 0, hi = 0;
+    if (lane < a.E) {
+        lo = a.offs[lane];
+        hi = a.offs[lane + 1];
+    }
+    const int rows = lane < a.E ? (int)(hi > lo ? hi - lo : 0) : -1;
+    uint32_t rank = 0;
+    for (int k = 0; k < (int)a.E; ++k) {
+        const int r = __builtin_amdgcn_readlane(rows, k);
+        rank += r > rows || (r == rows && k < lane);
+    }
+    const uint64_t hit = __ballot(lane < a.E && rank == n);
+    return hit ? (uint32_t)__builtin_ctzll(hit) : n;
+}
+
 // The work of tile `id` of TQ x TP tiles; false if it is none.
 template <bool GC, int TQ, int TP>
 __device__ __forceinline__ bool mm_work(const MmArgs& a, uint32_t id, uint32_t np, uint32_t nq, int split, int ce,
@@ -539,8 +605,9 @@ __device__ __forceinline__ bool mm_work(const MmArgs& a, uint32_t id, uint32_t n
     w->c_at = 0;
     w->c_len = a.C;
     if constexpr (GC) {
-        const uint32_t e = id / (np * nq);
+        uint32_t e = id / (np * nq);
         mm_walk(id - e * np * nq, np, nq, &pt, &qt);
+        e = mm_by_size(a, e);
         int64_t lo = 0, hi = a.C;
         if (a.offs) {
             const int64_t v0 = a.offs[e], v1 = a.offs[e + 1];
@@ -579,6 +646,16 @@ __device__ __forceinline__ bool mm_xcd(uint32_t b, uint32_t n, uint32_t* id) {
     return (b >> 3) < chunk && *id < n;
 }
 
+// The same for the weight gradient, whose experts differ in time: every XCD has
+// a range of every expert's `per` tiles, the experts one after the other.  (A
+// range of all tiles is whole experts: 272 us instead of 150 for 8 x 4096 x 2048
+// with 8192 tokens.)
+__device__ __forceinline__ bool mm_xcd_experts(uint32_t b, uint32_t per, uint32_t E, uint32_t* id) {
+    const uint32_t chunk = (per + 7) / 8, slot = b >> 3, e = slot / chunk, in = (b & 7) * chunk + slot % chunk;
+    *id = e * per + in;
+    return e < E && in < per;
+}
+
 // Large products: 256 x 256 tiles, the last round's cut where they fit.
 template <int MODE, int DT, bool QT, bool PT>
 __global__ void __launch_bounds__(512, 2) k_mm_large(MmArgs a, uint32_t nq, uint32_t np) {
@@ -593,7 +670,9 @@ __global__ void __launch_bounds__(512, 2) k_mm_large(MmArgs a, uint32_t nq, uint
     const uint32_t full = total / kMmCUs * kMmCUs, rem = total - full;
     const uint32_t cut = rem <= kMmCUs / 4 ? 4 : rem <= kMmCUs / 2 ? 2 : 1;
     uint32_t id, part = 0, parts = 1;
-    if (blockIdx.x < full) {
+    if (GC && full > 0) {
+        if (!mm_xcd_experts(blockIdx.x, rows * nq, (uint32_t)a.E, &id)) return;
+    } else if (blockIdx.x < full) {
         if (!mm_xcd(blockIdx.x, full, &id)) return;
     } else {
         if (!mm_xcd(blockIdx.x - full, rem * cut, &id)) return;
@@ -630,7 +709,9 @@ __global__ void __launch_bounds__(WQ* WP * 64, 2) k_mm_tiles(MmArgs a, uint32_t 
     const uint32_t rows = GC || !a.offs ? np : (uint32_t)mm_count_tiles(a, TP);
     const uint32_t per = rows * nq * (GC ? (uint32_t)a.E : 1u);
     uint32_t id;
-    if (!mm_xcd(blockIdx.x, per * (uint32_t)a.splits, &id)) return;
+    if (GC ? !mm_xcd_experts(blockIdx.x, rows * nq, (uint32_t)a.E, &id)
+           : !mm_xcd(blockIdx.x, per * (uint32_t)a.splits, &id))
+        return;
     const int split = (int)(id / per);
     MmWork w;
     if (!mm_work<GC, TQ, TP>(a, id - split * per, rows, nq, split, CE, &w)) return;
@@ -641,9 +722,10 @@ template <int MODE, int DT, bool QT, bool PT>
 hipError_t mm_tiles_size(const MmArgs& a, int size, hipStream_t s) {
     const MmTileSize t = kMmTileSizes[size];
     const int64_t nq = (a.Q + t.q - 1) / t.q, np = (a.P + t.p - 1) / t.p;
-    const int64_t tiles = PT ? np * a.E : mm_tile_bound(a, t.p);
+    // (the weight gradient deals every expert's tiles to 8 XCDs)
+    const int64_t tiles = PT ? (np * nq + 7) / 8 * 8 * a.E : mm_tile_bound(a, t.p) * nq;
     // cutting the last round adds at most 3 workgroups for each of 64 tiles
-    const int64_t total = tiles * nq * a.splits + (size == 0 ? 3 * kMmCUs / 4 : 0);
+    const int64_t total = tiles * a.splits + (size == 0 ? 3 * kMmCUs / 4 : 0);
     if (total >= (int64_t)1 << 31) return hipErrorInvalidValue;
     const dim3 grid((unsigned)((total + 7) / 8 * 8));
     const uint32_t q = (uint32_t)nq, p = (uint32_t)np;
