@@ -54,13 +54,15 @@ int to_out(int dt) { return dt == SSG_F32 ? ssg::OUT_F32 : dt == SSG_F16 ? ssg::
 
 constexpr double kBytesPerUs = 5.2e6, kTileMx4BytesPerUs = 3.2e6;   // the tiles' 64-byte rows of mx4 weights
 
-// Skinny: 16 rt weight rows x 16 nt tokens a workgroup of a 4096-long
-// contraction, by operand types (16-bit, mx4 x mx4, mx4 x 16-bit), nt and rt.
-// Measured at 4096 x 4096 with 16 and 32 tokens; 16-bit weights with 2 and 4 rt are
-// priced up to where many workgroups measured (11008 x 4096 x 16: 30, 33, 32 us).
-constexpr double kSkinnyUs[3][2][3] = {{{9.1, 19.0, 36.0}, {13.0, 16.0, 27.0}},
-                                       {{4.4, 4.7, 6.8}, {6.0, 6.5, 8.0}},
-                                       {{6.0, 7.8, 10.3}, {10.6, 11.9, 14.1}}};
+// Skinny: 16 rt weight rows (rt = 1 .. 4) x 16 nt tokens a workgroup of a
+// 4096-long contraction, by operand types (16-bit, mx4 x mx4, mx4 x 16-bit) and
+// nt; 0: not built.  Measured at 4096 and 11008 x 4096 with 16 and 32 tokens
+// (fp16 x mx4 at 11008 x 4096 x 16: 21, 19, 13, 15 us for rt = 1 .. 4; at 4096 x
+// 4096: 10, 12, 13, 14); 16-bit weights with rt > 1 are priced up to where many
+// workgroups measured (11008 x 4096 x 16: 30, 33, -, 32 us).
+constexpr double kSkinnyUs[3][2][4] = {{{9.1, 19.0, 0, 36.0}, {13.0, 16.0, 0, 27.0}},
+                                       {{4.4, 4.7, 6.0, 6.8}, {6.0, 6.5, 0, 8.0}},
+                                       {{6.0, 7.8, 9.2, 10.3}, {10.6, 11.9, 0, 14.1}}};
 
 struct Plan {
     bool skinny;
@@ -102,13 +104,16 @@ Plan plan(const MmArgs& a) {
     const double tile_floor = bytes / (a.mode == ssg::MM_16 ? kBytesPerUs : kTileMx4BytesPerUs);
     double best = 1e30;
     if (!a.qt && !a.pt && avg <= 64) {
-        for (int nt = 1; nt <= 2; ++nt)
-            for (int k = 0; k < 3; ++k) {
-                const int rt = 1 << k;
+        for (int nt = 1; nt <= (avg > 16 ? 2 : 1); ++nt)
+            for (int rt = 1; rt <= 4; ++rt) {
+                const double full = kSkinnyUs[a.mode][nt - 1][rt - 1];
+                if (full == 0) continue;
                 const double wgs = ceil_div(a.Q, 16 * rt) * row_tiles(16 * nt);
                 const double fill = std::min(1.0, avg / (16 * nt));   // tokens of a tile that exist
-                const double one = kSkinnyUs[a.mode][nt - 1][k] * (0.2 + 0.8 * (double)a.C / 4096) * (0.7 + 0.3 * fill);
-                const double us = 3.5 + std::max(std::max(1.0, std::ceil(wgs / kCUs)) * one, bytes / kBytesPerUs);
+                const double one = full * (0.2 + 0.8 * (double)a.C / 4096) * (0.7 + 0.3 * fill);
+                // (16-bit workgroups are small enough to run side by side)
+                const double more = std::max(0.0, std::ceil(wgs / kCUs) - 1) * (a.mode == ssg::MM_16 ? 0.85 : 1);
+                const double us = 3.5 + std::max((1 + more) * one, bytes / kBytesPerUs);
                 if (us < best) {
                     best = us;
                     p.skinny = true;

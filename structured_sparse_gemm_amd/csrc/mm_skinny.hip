@@ -86,9 +86,9 @@ struct Skinny {
     // Scales read by the lanes that use them are four bytes a row and load, and
     // as many memory requests as the elements: 44032 x 4096 with 16 tokens took
     // 46 us (bf16) and 35 us (mx4).  Through LDS, 16 bytes a thread for 4096
-    // elements of every row, it takes 37 and 32; with fewer rows a workgroup
-    // the barriers cost more than the requests.
-    static constexpr bool SHARED = MODE != MM_16 && RT >= 4;
+    // elements of every row, it takes 37 and 31; with fewer than 48 rows a
+    // workgroup the barriers cost more than the requests.
+    static constexpr bool SHARED = MODE != MM_16 && RT >= 3;
 
     // One step's operands.
     struct Ops {
@@ -418,6 +418,7 @@ template <int MODE, int DT>
 hipError_t pick(const MmArgs& a, int rt, int nt, hipStream_t s) {
     if (rt == 1) return nt == 1 ? go<MODE, DT, 1, 1>(a, s) : go<MODE, DT, 1, 2>(a, s);
     if (rt == 2) return nt == 1 ? go<MODE, DT, 2, 1>(a, s) : go<MODE, DT, 2, 2>(a, s);
+    if (rt == 3) return go<MODE, DT, 3, 1>(a, s);   // one token tile only (mm_abi.cpp)
     return nt == 1 ? go<MODE, DT, 4, 1>(a, s) : go<MODE, DT, 4, 2>(a, s);
 }
 
