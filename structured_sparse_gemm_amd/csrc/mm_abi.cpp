@@ -119,6 +119,20 @@ Plan plan(const MmArgs& a) {
                     p.skinny = true;
                     p.nt = nt;
                     p.rt = rt;
+                    p.splits = 1;
+                }
+                // few rows of long weights: several workgroups a row, each with
+                // at least one step a wave (shared scales: one round)
+                const int64_t unit = rt >= 3 && a.mode != ssg::MM_16 ? 4096 : 8 * (a.mode == ssg::MM_MX4 ? 256 : 128);
+                for (int splits = 2; splits <= 8 && unit * splits <= a.C && wgs * splits <= kCUs; splits *= 2) {
+                    const double us2 = 3.5 + std::max(one / splits, bytes / kBytesPerUs) + 4 +
+                                       (double)splits * a.P * a.Q * 8 / 3e6;
+                    if (us2 >= best) continue;
+                    best = us2;
+                    p.skinny = true;
+                    p.nt = nt;
+                    p.rt = rt;
+                    p.splits = splits;
                 }
             }
     }
@@ -151,7 +165,10 @@ Plan plan(const MmArgs& a) {
             }
         }
     }
-    if (p.skinny) return p;
+    if (p.skinny) {
+        if (p.splits > 1) p.bytes = (size_t)((int64_t)p.splits * a.P * a.Q * 4);
+        return p;
+    }
     int64_t at = 0;
     auto take = [&](int64_t n) {
         const int64_t r = at;
@@ -159,12 +176,16 @@ Plan plan(const MmArgs& a) {
         return r;
     };
     const int64_t qb = q_bytes(a), pb = p_bytes(a), nb = blocks(a.C);
-    if (qb % 16 || !al(a.q, 16) || a.ldq % 16 || a.strideq % 16) {
+    // Rows are loaded 16 bytes at a time.  16-bit operands may begin at any dword
+    // (an odd contraction length ends inside one); others at 16 bytes.
+    const int64_t q_al = a.mode != ssg::MM_16 ? 16 : a.qt || a.C % 2 == 0 ? 4 : 0;
+    const int64_t p_al = a.mode != ssg::MM_16 ? 16 : a.pt || a.C % 2 == 0 ? 4 : 0;
+    if (q_al == 0 || (q_al == 16 && qb % 16) || !al(a.q, q_al) || a.ldq % q_al || a.strideq % q_al) {
         p.copy_q = true;
         p.ldq = up(qb, 16);
         p.at_q = take(q_mats(a) * q_rows(a) * p.ldq);
     }
-    if (pb % 16 || !al(a.p, 16) || a.ldp % 16) {
+    if (p_al == 0 || (p_al == 16 && pb % 16) || !al(a.p, p_al) || a.ldp % p_al) {
         p.copy_p = true;
         p.ldp = up(pb, 16);
         p.at_p = take(p_rows(a) * p.ldp);
@@ -187,16 +208,6 @@ Plan plan(const MmArgs& a) {
     return p;
 }
 
-hipError_t repack(const uint8_t* src, int64_t mats, int64_t stride, int64_t rows, int64_t n, int64_t ld, uint8_t* dst,
-                  int64_t ldd, int fill, hipStream_t s) {
-    if (stride == rows * ld || mats == 1) return ssg::launch_mm_repack(src, mats * rows, n, ld, dst, ldd, fill, s);
-    for (int64_t e = 0; e < mats; ++e) {
-        const hipError_t r = ssg::launch_mm_repack(src + e * stride, rows, n, ld, dst + e * rows * ldd, ldd, fill, s);
-        if (r != hipSuccess) return r;
-    }
-    return hipSuccess;
-}
-
 int run(MmArgs a, void* ws, size_t ws_bytes, hipStream_t s) {
     if (a.P == 0 || a.Q == 0 || (a.pt && a.E == 0)) return SSG_OK;
     const Plan p = plan(a);
@@ -205,23 +216,30 @@ int run(MmArgs a, void* ws, size_t ws_bytes, hipStream_t s) {
             return fail(SSG_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws ? ws_bytes : (size_t)0, p.bytes);
         if (!al(ws, 16)) return fail(SSG_ERR_WORKSPACE, "workspace must be 16-byte aligned");
     }
-    if (p.skinny) return hip_status(ssg::launch_mm_skinny(a, p.rt, p.nt, s), "kernel launch");
     uint8_t* const w = (uint8_t*)ws;
     hipError_t e = hipSuccess;
+    a.splits = p.splits;
+    if (p.skinny) {
+        if (p.splits > 1) a.part = (float*)w;
+        e = ssg::launch_mm_skinny(a, p.rt, p.nt, s);
+        if (e == hipSuccess && p.splits > 1) e = ssg::launch_mm_reduce(a, s);
+        return hip_status(e, "kernel launch");
+    }
     if (p.copy_q) {
-        e = repack(a.q, q_mats(a), a.strideq, q_rows(a), q_bytes(a), a.ldq, w + p.at_q, p.ldq, 0, s);
+        e = ssg::launch_mm_repack(a.q, q_mats(a), a.strideq, q_rows(a), q_bytes(a), a.ldq, w + p.at_q, p.ldq, 0,
+                                  a.pt ? nullptr : a.offs, s);
         a.q = w + p.at_q;
         a.ldq = p.ldq;
         a.strideq = q_rows(a) * p.ldq;
     }
     if (p.copy_p && e == hipSuccess) {
-        e = repack(a.p, 1, 0, p_rows(a), p_bytes(a), a.ldp, w + p.at_p, p.ldp, 0, s);
+        e = ssg::launch_mm_repack(a.p, 1, 0, p_rows(a), p_bytes(a), a.ldp, w + p.at_p, p.ldp, 0, nullptr, s);
         a.p = w + p.at_p;
         a.ldp = p.ldp;
     }
     if (p.copy_s && e == hipSuccess) {
         // past the row's blocks: 1.0, for elements that are zero
-        e = repack(a.qs, a.E, a.strideqs, a.Q, blocks(a.C), a.ldqs, w + p.at_qs, p.lds, 127, s);
+        e = ssg::launch_mm_repack(a.qs, a.E, a.strideqs, a.Q, blocks(a.C), a.ldqs, w + p.at_qs, p.lds, 127, a.offs, s);
         a.qs = w + p.at_qs;
         a.ldqs = p.lds;
         a.strideqs = a.Q * p.lds;
@@ -236,7 +254,6 @@ int run(MmArgs a, void* ws, size_t ws_bytes, hipStream_t s) {
         a.ps = w + p.at_ps;
         a.ldps = p.plane_p;
     }
-    a.splits = p.splits;
     if (p.splits > 1) a.part = (float*)(w + p.at_part);
     if (e == hipSuccess) e = ssg::launch_mm_tiles(a, p.size, s);
     if (e == hipSuccess && p.splits > 1) e = ssg::launch_mm_reduce(a, s);

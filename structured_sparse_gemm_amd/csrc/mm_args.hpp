@@ -64,9 +64,10 @@ hipError_t launch_mm_planes(const MmPlanes& q, const MmPlanes& p, hipStream_t s)
 hipError_t launch_mm_tiles(const MmArgs& a, int size, hipStream_t s);
 // Y = the sum of the partials in split order, in the output type.
 hipError_t launch_mm_reduce(const MmArgs& a, hipStream_t s);
-// Rows of n bytes to rows of ldd bytes (a multiple of 16), `fill` past n.
-hipError_t launch_mm_repack(const void* src, int64_t rows, int64_t n, int64_t lds, void* dst, int64_t ldd, int fill,
-                            hipStream_t s);
+// Matrices of `rows` rows of n bytes to rows of ldd bytes (a multiple of 16),
+// `fill` past n; matrix e is left out if offs is given and offs[e + 1] <= offs[e].
+hipError_t launch_mm_repack(const void* src, int64_t mats, int64_t stride, int64_t rows, int64_t n, int64_t lds,
+                            void* dst, int64_t ldd, int fill, const int32_t* offs, hipStream_t s);
 hipError_t launch_mx4_quantize(int src, int64_t R, int64_t K, const void* A, int64_t lda, void* elems, int64_t lde,
                                void* scales, int64_t lds, hipStream_t s);
 hipError_t launch_mx4_dequantize(int dst, int64_t R, int64_t K, const void* elems, int64_t lde, const void* scales,
@@ -222,13 +223,13 @@ __device__ __forceinline__ f32x4 mfma_mx4(uint4 a, uint4 b, f32x4 c, uint32_t qs
 
 // Four consecutive outputs of row p from column q on, rounded to nearest even
 // for 16-bit outputs (half a step of the type, the only rounding after the
-// fp32 sums).
-__device__ __forceinline__ void mm_store4(void* y, int out, int64_t at, int n, bool vec, f32x4 v) {
+// fp32 sums); any alignment.
+__device__ __forceinline__ void mm_store4(void* y, int out, int64_t at, int n, f32x4 v) {
     typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
     typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
     if (out == OUT_F32) {
         float* d = reinterpret_cast<float*>(y) + at;
-        if (vec && n >= 4) *reinterpret_cast<f32x4*>(d) = v;
+        if (n >= 4) __builtin_memcpy(d, &v, 16);
         else
             for (int r = 0; r < 4; ++r)
                 if (r < n) d[r] = v[r];
@@ -238,7 +239,7 @@ __device__ __forceinline__ void mm_store4(void* y, int out, int64_t at, int n, b
     if (out == OUT_F16) w.h = __builtin_convertvector(v, f16x4);
     else w.b = __builtin_convertvector(v, bf16x4);
     uint16_t* d = reinterpret_cast<uint16_t*>(y) + at;
-    if (vec && n >= 4) *reinterpret_cast<uint2*>(d) = w.u;
+    if (n >= 4) __builtin_memcpy(d, &w.u, 8);
     else
         for (int r = 0; r < 4; ++r)
             if (r < n) d[r] = w.s[r];

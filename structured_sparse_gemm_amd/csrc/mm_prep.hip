@@ -17,7 +17,6 @@ constexpr int kThreads = 256;
 __global__ void __launch_bounds__(kThreads) k_mm_reduce(MmArgs a) {
     const int64_t cpr = (a.Q + 3) / 4, n = a.P * cpr;
     const bool vin = a.Q % 4 == 0;
-    const bool vec = a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
     for (int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x; t < n; t += (int64_t)gridDim.x * kThreads) {
         const int64_t p = t / cpr, q = (t - p * cpr) * 4;
         const int m = a.Q - q < 4 ? (int)(a.Q - q) : 4;
@@ -29,17 +28,19 @@ __global__ void __launch_bounds__(kThreads) k_mm_reduce(MmArgs a) {
                 for (int r = 0; r < 4; ++r)
                     if (r < m) v[r] += src[r];
         }
-        mm_store4(a.y, a.out, p * a.ldy + q, m, vec, v);
+        mm_store4(a.y, a.out, p * a.ldy + q, m, v);
     }
 }
 
 // One 16-byte chunk a thread.
-__global__ void __launch_bounds__(kThreads) k_mm_repack(const uint8_t* src, int64_t rows, int64_t n, int64_t lds,
-                                                        uint8_t* dst, int64_t ldd, int fill) {
-    const int64_t cpr = ldd / 16, total = rows * cpr;
+__global__ void __launch_bounds__(kThreads) k_mm_repack(const uint8_t* src, int64_t stride, int64_t rows, int64_t n,
+                                                        int64_t lds, uint8_t* dst, int64_t ldd, int fill,
+                                                        const int32_t* offs, int64_t total) {
+    const int64_t cpr = ldd / 16, per = rows * cpr;
     for (int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x; t < total; t += (int64_t)gridDim.x * kThreads) {
-        const int64_t r = t / cpr, b = (t - r * cpr) * 16;
-        const uint8_t* at = src + r * lds + b;
+        const int64_t e = t / per, u = t - e * per, r = u / cpr, b = (u - r * cpr) * 16;
+        if (offs && offs[e + 1] <= offs[e]) continue;      // an expert that no product reads
+        const uint8_t* at = src + e * stride + r * lds + b;
         uint8_t v[16];
         if (b + 16 <= n) {
             __builtin_memcpy(v, at, 16);
@@ -47,7 +48,7 @@ __global__ void __launch_bounds__(kThreads) k_mm_repack(const uint8_t* src, int6
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = b + j < n ? at[j] : (uint8_t)fill;
         }
-        *reinterpret_cast<uint4*>(dst + r * ldd + b) = *reinterpret_cast<uint4*>(v);
+        *reinterpret_cast<uint4*>(dst + t * 16) = *reinterpret_cast<uint4*>(v);
     }
 }
 
@@ -108,11 +109,12 @@ hipError_t launch_mm_reduce(const MmArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_mm_repack(const void* src, int64_t rows, int64_t n, int64_t lds, void* dst, int64_t ldd, int fill,
-                            hipStream_t s) {
-    if (rows * ldd == 0) return hipSuccess;
-    hipLaunchKernelGGL(k_mm_repack, dim3(grid_of(rows * (ldd / 16))), dim3(kThreads), 0, s, (const uint8_t*)src, rows,
-                       n, lds, (uint8_t*)dst, ldd, fill);
+hipError_t launch_mm_repack(const void* src, int64_t mats, int64_t stride, int64_t rows, int64_t n, int64_t lds,
+                            void* dst, int64_t ldd, int fill, const int32_t* offs, hipStream_t s) {
+    const int64_t total = mats * rows * (ldd / 16);
+    if (total == 0) return hipSuccess;
+    hipLaunchKernelGGL(k_mm_repack, dim3(grid_of(total)), dim3(kThreads), 0, s, (const uint8_t*)src, stride, rows, n,
+                       lds, (uint8_t*)dst, ldd, fill, offs, total);
     return hipGetLastError();
 }
 

@@ -273,16 +273,15 @@ struct Skinny {
             for (int t = 0; t < NT; ++t) acc[r][t] = f32x4{0, 0, 0, 0};
     }
 
-    // This wave's part of the contraction: steps wave, wave + kWaves, ..  ODD
+    // This wave's part of the contraction: steps n, n + by, ..  ODD
     // (mx4 weights against 16-bit activations): the elements unscaled, their
     // sums scaled in fp32.
     template <bool ODD>
-    __device__ __forceinline__ void run_steps(int wave) {
+    __device__ __forceinline__ void run_steps(int64_t n, int64_t by) {
         // a block that K ends inside is whole in an mx4 operand, not in a 16-bit one
         const int64_t whole = (MX ? nb * kMxBlock : a.C) / S, steps = (a.C + S - 1) / S;
-        int64_t n = wave;
         Ops o;
-        for (; n < whole; n += kWaves) {
+        for (; n < whole; n += by) {
             load<true>(n * S, o);
             products<ODD>(o, 0);
         }
@@ -292,15 +291,15 @@ struct Skinny {
         }
     }
 
-    // The same with shared scales: slice `wave` of every round.  Every wave
+    // The same with shared scales: slice `wave` of every round of this split.  Every wave
     // takes part in the barriers.
     template <bool ODD>
-    __device__ __forceinline__ void run_rounds(int wave) {
+    __device__ __forceinline__ void run_rounds(int wave, int split) {
         const int64_t whole = MX ? nb * kMxBlock : a.C;
         // rounds of equal length, a wave's slices of them whole steps
         const int64_t rounds = (a.C + kRound - 1) / kRound;
         const int slice = (int)(((a.C + rounds * kWaves - 1) / (rounds * kWaves) + S - 1) / S * S);
-        for (int64_t n = 0; n < rounds; ++n) {
+        for (int64_t n = split; n < rounds; n += a.splits) {
             const int64_t k0 = (n * kWaves + wave) * slice;
             uint4 v[SPT];
             load_scales(n * kWaves * slice / kMxBlock, v);
@@ -309,7 +308,7 @@ struct Skinny {
                 if (k0 + S <= whole) load<true>(k0, o);
                 else load<false>(k0, o);
             }
-            if (n > 0) lds_barrier();  // every wave has read the last round's scales
+            if (n > split) lds_barrier();  // every wave has read the last round's scales
             store_scales(v);
             lds_barrier();
 #pragma unroll 1                           // unrolled, its registers cost half the waves
@@ -333,7 +332,8 @@ __global__ void __launch_bounds__(kThreads, RT == 4 && NT == 1 ? 4 : 2) k_mm_ski
     constexpr int kRed = kWaves * RT * NT * 64 * 16, kSc = K::SHARED ? K::SROWS * kScaleRow : 0;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kRed > kSc ? kRed : kSc];   // the scales, then the waves' sums
     f32x4(*const red)[RT * NT * 64] = reinterpret_cast<f32x4(*)[RT * NT * 64]>(lds);
-    const uint32_t tt = blockIdx.x / nq, qt = blockIdx.x - tt * nq;
+    const uint32_t per = gridDim.x / (uint32_t)a.splits, split = blockIdx.x / per, id = blockIdx.x - split * per;
+    const uint32_t tt = id / nq, qt = id - tt * nq;
     MmTile tile;
     if (!mm_find_tile(a, 16 * NT, (int)tt, &tile)) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -367,20 +367,22 @@ __global__ void __launch_bounds__(kThreads, RT == 4 && NT == 1 ? 4 : 2) k_mm_ski
     if (tile.e >= 0) {
         k.odd = false;
         if constexpr (K::SHARED) {
-            k.template run_rounds<false>(wave);
+            k.template run_rounds<false>(wave, (int)split);
             if constexpr (MODE == MM_W4) {
                 if (__syncthreads_or(k.odd)) {
                     k.zero();
-                    k.template run_rounds<true>(wave);
+                    k.template run_rounds<true>(wave, (int)split);
                 }
             }
             __syncthreads();           // the scales give way to the sums
         } else {
-            k.template run_steps<false>(wave);
+            // splits take the steps in turn
+            const int64_t first = (int64_t)split * kWaves + wave, by = (int64_t)a.splits * kWaves;
+            k.template run_steps<false>(first, by);
             if constexpr (MODE == MM_W4) {
                 if (__any(k.odd)) {
                     k.zero();
-                    k.template run_steps<true>(wave);
+                    k.template run_steps<true>(first, by);
                 }
             }
         }
@@ -398,8 +400,9 @@ __global__ void __launch_bounds__(kThreads, RT == 4 && NT == 1 ? 4 : 2) k_mm_ski
         const int64_t p = tile.r0 + 16 * t + (l & 15), q = q0 + 16 * r + 4 * (l >> 4);
         if (p >= tile.v0 && p < tile.r1 && q < a.Q) {
             const int64_t left = a.Q - q;
-            const bool vec = a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
-            mm_store4(a.y, a.out, p * a.ldy + q, left < 4 ? (int)left : 4, vec, v);
+            const int n = left < 4 ? (int)left : 4;
+            if (a.part) mm_store4(a.part, OUT_F32, ((int64_t)split * a.P + p) * a.Q + q, n, v);
+            else mm_store4(a.y, a.out, p * a.ldy + q, n, v);
         }
     }
 }
@@ -408,8 +411,8 @@ template <int MODE, int DT, int RT, int NT>
 hipError_t go(const MmArgs& a, hipStream_t s) {
     const int64_t nq = (a.Q + 16 * RT - 1) / (16 * RT);
     const int64_t tiles = mm_tile_bound(a, 16 * NT);
-    if (nq * tiles >= (int64_t)1 << 31) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_mm_skinny<MODE, DT, RT, NT>), dim3((unsigned)(nq * tiles)), dim3(kThreads), 0, s, a,
+    if (nq * tiles * a.splits >= (int64_t)1 << 31) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_mm_skinny<MODE, DT, RT, NT>), dim3((unsigned)(nq * tiles * a.splits)), dim3(kThreads), 0, s, a,
                        (uint32_t)nq);
     return hipGetLastError();
 }

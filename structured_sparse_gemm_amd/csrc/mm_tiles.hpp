@@ -70,7 +70,7 @@ __device__ __forceinline__ const uint8_t* mm_uniform(const uint8_t* p) {
 // the one to come.
 template <bool TR, int T, int L>
 struct MmLoad {
-    const uint8_t* next;
+    const uint8_t *next, *end;         // .. and the end of the operand: its dwords past that read as zero
     int64_t step;                      // bytes from a stage to the next
     int last, ragged, tail;            // stages; the one that ends inside its 64 bytes (TR: 32 rows), and where
     int at;                            // this lane's place in a stage (TR: of load 0)
@@ -82,10 +82,13 @@ struct MmLoad {
 
     // first .. rows - 1: the tile's rows that exist (TR: bytes of a row that
     // do); left: bytes of a row (TR: rows) of the contraction from the first
-    // stage on; nst: stages of this workgroup
-    __device__ __forceinline__ void init(const uint8_t* base, int64_t ld, int64_t left, int nst, int wave, int lane,
-                                         int64_t first, int64_t rows) {
+    // stage on; nst: stages of this workgroup.  Rows need 4-byte alignment: a
+    // chunk that a row ends inside brings the next row's first elements, which
+    // clear() takes out (contraction) or nobody stores (TR).
+    __device__ __forceinline__ void init(const uint8_t* base, const uint8_t* stop, int64_t ld, int64_t left, int nst,
+                                         int wave, int lane, int64_t first, int64_t rows) {
         next = mm_uniform(base);
+        end = mm_uniform(stop);
         step = TR ? 32 * ld : 64;
         last = nst;
         constexpr int U = TR ? 32 : 64;
@@ -111,7 +114,7 @@ struct MmLoad {
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t open(int it) {
         const uint8_t* p = next;
         next += step;
-        return rsrc(p, it < last ? 0x7fffffff : 0);
+        return rsrc(p, it < last ? end - p : 0);
     }
     // Load J of stage `it` to LDS address dst (the stage's).  No branch: it
     // would cut the block that the products are scheduled in.
@@ -119,6 +122,19 @@ struct MmLoad {
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int it, uint32_t dst, int wave) const {
         const int lim = (it == ragged ? tail : 64) - (TR ? J * (64 / (T / 8)) : 0);
         dma<16>(r, dst + (wave * L + J) * 1024, at < lim ? off[J] : kOob);
+    }
+    // The ragged stage's contraction may end inside a chunk: clear this wave's
+    // own chunks (which have landed) from there on.
+    __device__ __forceinline__ void clear(uint8_t* st, int wave, int lane) const {
+        const int n = tail - at;           // bytes of the lane's chunk that belong to the row
+        if (n <= 0 || n >= 16) return;
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            uint32_t* const d = reinterpret_cast<uint32_t*>(st + (wave * L + j) * 1024 + lane * 16);
+#pragma unroll
+            for (int k = 1; k < 4; ++k)
+                if (4 * k >= n) d[k] = 0;
+        }
     }
 };
 
@@ -245,20 +261,27 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
     MmLoad<QT, TQ, L::QL> lq;
     MmLoad<PT, TP, L::PL> lp;
     const int groups = (w.nst + 3) / 4;              // W4: a load of weights covers four stages
+    // a dword that the operand ends inside is read whole: it lies in the same 4-byte aligned memory
+    auto end_of = [](const uint8_t* base, int64_t rows, int64_t ld, int64_t bytes) {
+        return base + (rows - 1) * ld + (bytes + 3) / 4 * 4;
+    };
+    const int64_t qrow = MX || W4 ? nb * 16 : QT ? a.Q * ES : a.C * ES, prow = MX ? nb * 16 : PT ? a.P * ES : a.C * ES;
+    const uint8_t* const qend = end_of(a.q + (PT || a.E < 1 ? 0 : (a.E - 1) * a.strideq), QT ? a.C : a.Q, a.ldq, qrow);
+    const uint8_t* const pend = end_of(a.p, PT ? a.C : a.P, a.ldp, prow);
     if constexpr (QT) {
-        lq.init(a.q + (PT ? w.c_at * a.ldq : e * a.strideq) + w.st0 * 32 * a.ldq + w.q0 * ES, a.ldq,
+        lq.init(a.q + (PT ? w.c_at * a.ldq : e * a.strideq) + w.st0 * 32 * a.ldq + w.q0 * ES, qend, a.ldq,
                 w.c_len - w.st0 * 32, w.nst, wave, lane, 0, (a.Q - w.q0) * ES);
     } else {
         const int64_t at = W4 ? w.st0 / 4 * 64 : w.st0 * 64;         // W4: splits begin at whole groups of four stages
-        lq.init(a.q + e * a.strideq + w.q0 * a.ldq + at, a.ldq, (MX || W4 ? nb * 16 : a.C * ES) - at,
-                W4 ? groups : w.nst, wave, lane, 0, a.Q - w.q0);
+        lq.init(a.q + e * a.strideq + w.q0 * a.ldq + at, qend, a.ldq, qrow - at, W4 ? groups : w.nst, wave, lane, 0,
+                a.Q - w.q0);
     }
-    const int64_t prow = MX ? nb * 16 : a.C * ES;
     if constexpr (PT)
-        lp.init(a.p + (w.c_at + w.st0 * 32) * a.ldp + w.r0 * ES, a.ldp, w.c_len - w.st0 * 32, w.nst, wave, lane, 0,
-                (a.P - w.r0) * ES);
+        lp.init(a.p + (w.c_at + w.st0 * 32) * a.ldp + w.r0 * ES, pend, a.ldp, w.c_len - w.st0 * 32, w.nst, wave, lane,
+                0, (a.P - w.r0) * ES);
     else
-        lp.init(a.p + w.r0 * a.ldp + w.st0 * 64, a.ldp, prow - w.st0 * 64, w.nst, wave, lane, w.v0 - w.r0, w.r1 - w.r0);
+        lp.init(a.p + w.r0 * a.ldp + w.st0 * 64, pend, a.ldp, prow - w.st0 * 64, w.nst, wave, lane, w.v0 - w.r0,
+                w.r1 - w.r0);
     // one scale load a wave: mx4 x mx4, those of Q from even waves and of P from odd ones
     MmScales ls;
     MmRowScales<TQ> lw;
@@ -377,6 +400,13 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
         }
     };
 
+    // the stage that the contraction ends inside a chunk of, or -1
+    const int part = MODE == MM_16 && !PT && a.C % 8 != 0 && (w.st0 + w.nst) * 32 >= a.C ? w.nst - 1 : -1;
+    auto clear_part = [&]() {
+        uint8_t* const st = lds + (part & (L::kRing - 1)) * L::STAGE;
+        if constexpr (!QT) lq.clear(st, wave, lane);
+        if constexpr (!PT) lp.clear(st + L::P_AT, wave, lane);
+    };
     if (w.nst > 0) {
         // (W4) the weights of group m follow the activations of stage 4 m - 1,
         // here and in the loop
@@ -387,6 +417,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
             if (W4 && s % 4 == 3) issue_w(s / 4 + 1);
         }
         wait_vm<(L::kRing - 1) * L::VM + L::kRing / 4 * L::VMW>();
+        if (MODE == MM_16 && part == 0) clear_part();
         lds_barrier();
         Ops o[2];
         mm_for<NRD>([&](auto u) { read(u, 0, o[0]); });
@@ -405,6 +436,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
             constexpr int B = decltype(bc)::value;   // W4: stage of the group
             constexpr bool last_of_4 = W4 && B == 3;
             wait_vm<V + (L::kRing / 4 - (B < 3 ? 0 : 1)) * L::VMW>();
+            if (MODE == MM_16 && !PT && it + 1 == part) clear_part();
             lds_barrier();
             uint4 v = make_uint4(0, 0, 0, 0), vn = v;
             if constexpr (W4) v = widen(std::integral_constant<int, 0>{}, B, cur);
@@ -446,9 +478,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
                 stage(it, o[0], o[1], std::integral_constant<int, 0>{});
                 stage(it + 1, o[1], o[0], std::integral_constant<int, 0>{});
             }
-            if (it < w.nst) {
-                mm_for<NG>([&](auto gc) { mmas(gc, o[0], make_uint4(0, 0, 0, 0)); });
-            }
+            if (it < w.nst) mm_for<NG>([&](auto gc) { mmas(gc, o[0], make_uint4(0, 0, 0, 0)); });
         }
         wait_vm<0>();                  // no load of this workgroup may land after it ends
     }
@@ -506,7 +536,6 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
         constexpr int CH = 64 * ES / 16, YN = NY < L::FP ? NY : L::FP;      // chunks a row
         constexpr bool HALF = decltype(half)::value;
         if constexpr (QT && ES == 4) {
-            const bool vec = ldo % 4 == 0 && (oat % 4 == 0) && reinterpret_cast<uintptr_t>(out) % 16 == 0;
 #pragma unroll
             for (int y = 0; y < L::FP; ++y) {
                 const int fy = fp0 + y;
@@ -515,7 +544,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
 #pragma unroll
                 for (int x = 0; x < L::FQ; ++x) {
                     const int64_t q = w.q0 + (fq0 + x) * 16 + 4 * g;
-                    if (q < a.Q) mm_store4(out, OUT_F32, oat + p * ldo + q, a.Q - q < 4 ? (int)(a.Q - q) : 4, vec, acc[x][y]);
+                    if (q < a.Q) mm_store4(out, OUT_F32, oat + p * ldo + q, a.Q - q < 4 ? (int)(a.Q - q) : 4, acc[x][y]);
                 }
             }
             return;

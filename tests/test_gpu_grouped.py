@@ -27,7 +27,8 @@ def case(dt, sizes, M, K, seed, first=0, extra=0):
 # (sizes, M, K): single tokens; empty experts; around the kernels' borders; odd lengths; many experts; one expert
 CASES = [([1], 16, 32), ([0, 1, 0], 8, 8), ([2, 0, 1], 100, 72), ([16, 17], 40, 1000), ([33, 0, 64, 31], 264, 136),
          ([65, 63, 128, 129], 136, 264), ([300, 0, 2], 520, 400), ([7] * 40, 33, 35), ([50, 1, 90], 77, 101),
-         ([257], 300, 513), ([0, 0], 24, 40), ([40, 60], 1, 1), ([500, 24, 0, 300], 129, 1023)]
+         ([257], 300, 513), ([0, 0], 24, 40), ([40, 60], 1, 1), ([500, 24, 0, 300], 129, 1023),
+         ([70, 45], 70, 1002), ([3, 2], 262, 34), ([130, 0, 260], 390, 86), ([1, 0, 3], 20, 5000)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
@@ -238,3 +239,57 @@ def test_refusals_on_the_device():
     assert status(ssg.grouped_mm_mx4, X, e, s[:, :, :0], offs) == 2
     assert status(ssg.mm_mx4, X, e[0], s[0], out_dtype=torch.bfloat16) == 4
     assert status(ssg.mx4_quantize, X.double()) == 4
+
+
+@pytest.mark.parametrize("M,K", [(70, 70), (72, 1002), (300, 262), (66, 65)])
+@pytest.mark.parametrize("rows", [3, 60, 300])
+def test_a_row_of_nan_stays_in_its_row(M, K, rows):
+    # lengths that end inside a 16-byte piece of a row: what the piece brings of
+    # the next row must not reach this one's sums
+    sizes = [rows, rows + 7]
+    X, W, dY, offs = case("bf16", sizes, M, K, 9)
+    N = 2 * rows + 7
+    X[1] = float("nan")
+    W[0, 5] = float("nan")
+    dY[2] = float("nan")
+    W2 = W.clone()
+    W2[0, 5] = 1.0
+    og = offs.cuda()
+    Y = ssg.grouped_mm(X.cuda(), W.cuda(), og).float().cpu()
+    want = torch.zeros(N, M, dtype=torch.bool)
+    want[1] = True
+    want[:rows, 5] = True
+    assert torch.equal(torch.isnan(Y), want)
+    dX = ssg.grouped_mm_dx(dY.cuda(), W2.cuda(), og).float().cpu()
+    want = torch.zeros(N, K, dtype=torch.bool)
+    want[2] = True
+    assert torch.equal(torch.isnan(dX), want)
+    X[1] = 0
+    X[rows:, K - 1] = float("inf")
+    dY[2] = 0
+    dY[rows:] = dY[rows:].abs() + 1
+    dW = ssg.grouped_mm_dw(dY.cuda(), X.cuda(), og).float().cpu()
+    assert torch.isfinite(dW[0]).all() and torch.isfinite(dW[1, :, :K - 1]).all()
+    assert (dW[1, :, K - 1] == float("inf")).all()
+
+
+# tiles of the largest size, its halves and quarters, in whole and partly filled rounds
+@pytest.mark.parametrize("sizes,M,K", [([900, 0, 1500, 333], 2304, 1058), ([2100], 4096, 512), ([257, 255, 256], 1024, 520),
+                                       ([3000, 100, 700], 2560, 264)])
+def test_large_products(sizes, M, K):
+    X, W, dY, offs = case("bf16", sizes, M, K, 17)
+    Xg, Wg, dYg, og = X.cuda(), W.cuda(), dY.cuda(), offs.cuda()
+    x, w, d = Xg.double(), Wg.double(), dYg.double()
+    e, s = ssg.mx4_quantize(Wg)
+    xe, xs = ssg.mx4_quantize(Xg)
+    wq, xq = ssg.mx4_dequantize(e, s, K).double(), ssg.mx4_dequantize(xe, xs, K).double()
+    got = {"Y": ssg.grouped_mm(Xg, Wg, og), "dX": ssg.grouped_mm_dx(dYg, Wg, og, out_dtype=torch.float32),
+           "dW": ssg.grouped_mm_dw(dYg, Xg, og), "w4": ssg.grouped_mm_mx4(Xg, e, s, og),
+           "mx": ssg.grouped_mm_mx4(xe, e, s, og, xscales=xs, out_dtype=torch.bfloat16)}
+    for i, a, b in D.segments(offs, X.shape[0]):
+        parts = {"Y": (x[a:b], w[i].t(), K), "dX": (d[a:b], w[i], M), "dW": (d[a:b].t(), x[a:b], b - a),
+                 "w4": (x[a:b], wq[i].t(), K), "mx": (xq[a:b], wq[i].t(), K)}
+        for name, (l, r, n) in parts.items():
+            l, r = l.contiguous(), r.contiguous()
+            out = got[name][i] if name == "dW" else got[name][a:b]
+            D.check(out, (l @ r).cpu().numpy(), (l.abs() @ r.abs()).cpu().numpy(), n, "%s of expert %d" % (name, i))
