@@ -103,7 +103,7 @@ Plan plan(const MmArgs& a) {
     const double bytes = a.pt ? 0 : busy * (double)a.Q * (double)a.C * (a.mode == ssg::MM_16 ? 2 : 0.53);
     const double tile_floor = bytes / (a.mode == ssg::MM_16 ? kBytesPerUs : kTileMx4BytesPerUs);
     double best = 1e30;
-    if (!a.qt && !a.pt && avg <= 64) {
+    if (!a.qt && !a.pt && avg <= 128) {
         for (int nt = 1; nt <= (avg > 16 ? 2 : 1); ++nt)
             for (int rt = 1; rt <= 4; ++rt) {
                 const double full = kSkinnyUs[a.mode][nt - 1][rt - 1];
@@ -177,15 +177,19 @@ Plan plan(const MmArgs& a) {
     };
     const int64_t qb = q_bytes(a), pb = p_bytes(a), nb = blocks(a.C);
     // Rows are loaded 16 bytes at a time.  16-bit operands may begin at any dword
-    // (an odd contraction length ends inside one); others at 16 bytes.
+    // (an odd contraction length ends inside one); others at 16 bytes.  The
+    // kernel finds the end of transposed rows of part chunks with 31 bits.
     const int64_t q_al = a.mode != ssg::MM_16 ? 16 : a.qt || a.C % 2 == 0 ? 4 : 0;
     const int64_t p_al = a.mode != ssg::MM_16 ? 16 : a.pt || a.C % 2 == 0 ? 4 : 0;
-    if (q_al == 0 || (q_al == 16 && qb % 16) || !al(a.q, q_al) || a.ldq % q_al || a.strideq % q_al) {
+    auto far = [](int64_t rows, int64_t ld) { return rows * ld >= (int64_t)1 << 31; };
+    if (q_al == 0 || (qb % 16 && (q_al == 16 || (a.qt && far(q_rows(a), a.ldq)))) || !al(a.q, q_al) || a.ldq % q_al ||
+        a.strideq % q_al) {
         p.copy_q = true;
         p.ldq = up(qb, 16);
         p.at_q = take(q_mats(a) * q_rows(a) * p.ldq);
     }
-    if (p_al == 0 || (p_al == 16 && pb % 16) || !al(a.p, p_al) || a.ldp % p_al) {
+    if (p_al == 0 || (pb % 16 && (p_al == 16 || (a.pt && far(p_rows(a), a.ldp)))) || !al(a.p, p_al) ||
+        a.ldp % p_al) {
         p.copy_p = true;
         p.ldp = up(pb, 16);
         p.at_p = take(p_rows(a) * p.ldp);

@@ -52,9 +52,15 @@ __global__ void __launch_bounds__(kThreads) k_mm_repack(const uint8_t* src, int6
     }
 }
 
+__host__ __device__ inline int64_t mm_plane_threads(int64_t nb, int64_t plane) {
+    return plane / 4 * ((nb + 63) / 64 * 4);
+}
+
 // Scales [rows][nb] to planes [blocks / 4][4][plane]: a thread takes 4 rows by
-// 16 blocks, transposes them in registers, and writes 16 dwords of 4 rows each,
-// consecutive threads consecutive rows.  Rows and blocks past the end get 127
+// 16 blocks, transposes them in registers, and writes 16 dwords of 4 rows each.
+// Four consecutive threads read 64 bytes of the same rows, every fourth writes
+// consecutive rows (with the rows consecutive alone, 28672 x 256 scales took 7.7 us
+// instead of 6.2).  Rows and blocks past the end get 127
 // (1.0): their elements are zeros.
 __global__ void __launch_bounds__(kThreads) k_mm_planes(MmPlanes jq, MmPlanes jp, int64_t nq, int64_t total) {
     for (int64_t n = (int64_t)blockIdx.x * kThreads + threadIdx.x; n < total; n += (int64_t)gridDim.x * kThreads) {
@@ -62,8 +68,10 @@ __global__ void __launch_bounds__(kThreads) k_mm_planes(MmPlanes jq, MmPlanes jp
         const uint8_t* const src = j.src;
         uint8_t* const dst = j.dst;
         const int64_t t = n < nq ? n : n - nq, nb = j.nb, ld = j.ld, rows = j.rows, stride = j.stride, plane = j.plane;
-        const int64_t r4 = plane / 4, planes = (nb + 3) / 4 * 4, per_mat = r4 * ((planes + 15) / 16);
-        const int64_t e = t / per_mat, u = t - e * per_mat, c = u / r4, r = (u - c * r4) * 4, b = c * 16;
+        const int64_t r4 = plane / 4, planes = (nb + 3) / 4 * 4, per_mat = mm_plane_threads(nb, plane);
+        const int64_t e = t / per_mat, u = t - e * per_mat, cb = u / (4 * r4), v0 = u - cb * 4 * r4;
+        const int64_t r = v0 / 4 * 4, b = (cb * 4 + v0 % 4) * 16;
+        if (b >= planes) continue;
         uint32_t v[4][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -119,7 +127,7 @@ hipError_t launch_mm_repack(const void* src, int64_t mats, int64_t stride, int64
 }
 
 hipError_t launch_mm_planes(const MmPlanes& q, const MmPlanes& p, hipStream_t s) {
-    auto threads = [](const MmPlanes& j) { return j.mats * (j.plane / 4) * (((j.nb + 3) / 4 * 4 + 15) / 16); };
+    auto threads = [](const MmPlanes& j) { return j.mats * mm_plane_threads(j.nb, j.plane); };
     const int64_t nq = threads(q), total = nq + threads(p);
     if (total == 0) return hipSuccess;
     hipLaunchKernelGGL(k_mm_planes, dim3(grid_of(total)), dim3(kThreads), 0, s, q, p, nq, total);

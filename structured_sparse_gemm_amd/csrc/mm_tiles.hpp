@@ -65,32 +65,61 @@ __device__ __forceinline__ const uint8_t* mm_uniform(const uint8_t* p) {
     return reinterpret_cast<const uint8_t*>(((uint64_t)hi << 32) | lo);
 }
 
+// A 16-byte direct-to-LDS load: lane l's bytes from offset voff of the buffer
+// (base, hi, bytes, flags) land at LDS address dst + IMM + 16 l; dwords past
+// the buffer's bytes read as zero.  The kernel counts these loads itself
+// (wait_vm); GFX9 needs one wait state between the write of M0 and the load.
+template <int IMM>
+__device__ __forceinline__ void mm_dma(i32x4 buf, uint32_t dst, uint32_t voff) {
+    asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds" ::"s"(dst), "n"(IMM),
+                 "v"(voff), "s"(buf)
+                 : "memory", "m0", "scc");
+}
+
 // A tile of T rows by 64 bytes (TR: 32 contraction rows by T columns) as
-// 1 KiB loads, L a wave.  Stages are issued in order; `next` is the origin of
-// the one to come.
-template <bool TR, int T, int L>
+// 1 KiB loads, L a wave.  Stages are opened in order.  Scalar instructions
+// between the products are not free (a dozen more a stage cost 8% of the
+// rate), so each kind has the cheapest ends that are exact for it:
+//   MASK: rows of mx4 elements and of a TR operand.  Lanes past the tile's rows
+//     or columns, past the contraction in the ragged stage, and whole stages
+//     past the last read zeros.
+//   else: rows of 16-bit elements along the contraction.  Rows past the tile's
+//     are past the buffer and read as zero; what the last stage brings of the
+//     next row is cleared in LDS (clear()); stages past the last bring what
+//     nobody reads.
+template <bool TR, int T, int L, bool MASK>
 struct MmLoad {
-    const uint8_t *next, *end;         // .. and the end of the operand: its dwords past that read as zero
+    static_assert(MASK || !TR, "a TR operand's ends are masked");
+    uint32_t lo, hi;                   // origin of the next stage
+    int lim, dec;                      // bytes from there that may be read, and how many fewer a stage later
     int64_t step;                      // bytes from a stage to the next
     int last, ragged, tail;            // stages; the one that ends inside its 64 bytes (TR: 32 rows), and where
-    int at;                            // this lane's place in a stage (TR: of load 0)
+    int at;                            // MASK: this lane's place in a stage (TR: of load 0)
     uint32_t off[L];
 
     // tile row of an LDS fragment row
     __device__ __forceinline__ static int row_of(int slot) { return (slot & ~63) + 4 * (slot & 15) + ((slot >> 4) & 3); }
     __device__ __forceinline__ static int swz_c(int c) { return ((c & 3) | ((c >> 1) & 4)) & (T / 16 - 1); }
 
-    // first .. rows - 1: the tile's rows that exist (TR: bytes of a row that
-    // do); left: bytes of a row (TR: rows) of the contraction from the first
-    // stage on; nst: stages of this workgroup.  Rows need 4-byte alignment: a
-    // chunk that a row ends inside brings the next row's first elements, which
-    // clear() takes out (contraction) or nobody stores (TR).
-    __device__ __forceinline__ void init(const uint8_t* base, const uint8_t* stop, int64_t ld, int64_t left, int nst,
-                                         int wave, int lane, int64_t first, int64_t rows) {
-        next = mm_uniform(base);
-        end = mm_uniform(stop);
+    // rows: the tile's rows from `base` on (TR: contraction rows from the first
+    // stage on); bytes: what a row holds from `base` on; nst: stages of this
+    // workgroup.  Rows of 16-bit elements need 4-byte alignment; a dword that
+    // the last one ends inside is read whole (it lies in the same aligned
+    // memory), and where rows may end inside a chunk (TR: bytes % 16) the
+    // buffer ends with the last of them (those of 2^31 bytes and more come
+    // here as copies with whole chunks).
+    __device__ __forceinline__ void init(const uint8_t* base, int64_t ld, int64_t rows, int64_t bytes, int nst,
+                                         int wave, int lane) {
+        const uint64_t p = reinterpret_cast<uint64_t>(base);
+        lo = __builtin_amdgcn_readfirstlane((uint32_t)p);
+        hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
         step = TR ? 32 * ld : 64;
         last = nst;
+        const int64_t n = TR ? rows : (rows < T ? rows : T), end = n > 0 ? (n - 1) * ld + (bytes + 3) / 4 * 4 : 0;
+        const bool exact = !MASK || (TR && bytes % 16 != 0 && end <= 0x7fffffff);
+        lim = exact ? (int)end : 0x7fffffff;
+        dec = exact ? (int)step : 0;
+        const int64_t left = TR ? rows : bytes;
         constexpr int U = TR ? 32 : 64;
         ragged = left < (int64_t)nst * U ? nst - 1 : -1;
         tail = (int)(left - (int64_t)(nst - 1) * U < U ? left - (int64_t)(nst - 1) * U : U);
@@ -102,37 +131,44 @@ struct MmLoad {
                 constexpr int CPR = T / 8;
                 const int c = unit / CPR, pos = unit % CPR;
                 const int chunk = (((pos >> 1) ^ swz_c(c)) << 1) | (pos & 1);
-                off[j] = 16 * chunk < rows ? (uint32_t)(c * ld + 16 * chunk) : kOob;
+                off[j] = 16 * chunk < bytes ? (uint32_t)(c * ld + 16 * chunk) : kOob;
             } else {
-                const int slot = unit >> 2, r = row_of(slot), chunk = (unit & 3) ^ mm_swz(slot & 15);
-                off[j] = r >= first && r < rows ? (uint32_t)(r * ld + 16 * chunk) : kOob;
+                const int slot = unit >> 2, r = row_of(slot);
+                off[j] = !MASK || r < rows ? (uint32_t)(r * ld + 16 * ((unit & 3) ^ mm_swz(slot & 15))) : kOob;
             }
         }
     }
 
-    // Buffer of stage `it`, empty past the last.
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t open(int it) {
-        const uint8_t* p = next;
-        next += step;
-        return rsrc(p, it < last ? end - p : 0);
+    // Buffer of stage `it`, the next.
+    __device__ __forceinline__ i32x4 open(int it) {
+        const i32x4 r = {(int)lo, (int)hi, MASK ? (it < last ? lim : 0) : (lim > 0 ? lim : 0), 0x00020000};
+        const uint64_t p = (((uint64_t)hi << 32) | lo) + step;
+        lo = (uint32_t)p;
+        hi = (uint32_t)(p >> 32);
+        if constexpr (TR || !MASK) lim -= dec;
+        return r;
     }
-    // Load J of stage `it` to LDS address dst (the stage's).  No branch: it
-    // would cut the block that the products are scheduled in.
-    template <int J>
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int it, uint32_t dst, int wave) const {
-        const int lim = (it == ragged ? tail : 64) - (TR ? J * (64 / (T / 8)) : 0);
-        dma<16>(r, dst + (wave * L + J) * 1024, at < lim ? off[J] : kOob);
+    // Load J of stage `it` to LDS address dst + AT + (this wave's part).  No
+    // branch: it would cut the block that the products are scheduled in.
+    template <int J, int AT>
+    __device__ __forceinline__ void load(i32x4 r, int it, uint32_t dst) const {
+        if constexpr (MASK) {
+            const int end = (it == ragged ? tail : 64) - (TR ? J * (64 / (T / 8)) : 0);
+            mm_dma<AT + J * 1024>(r, dst, at < end ? off[J] : kOob);
+        } else {
+            mm_dma<AT + J * 1024>(r, dst, off[J]);
+        }
     }
-    // The ragged stage's contraction may end inside a chunk: clear this wave's
-    // own chunks (which have landed) from there on.
+    // The contraction may end inside the last stage: this wave's own chunks
+    // (which have landed) from there on become zeros.
     __device__ __forceinline__ void clear(uint8_t* st, int wave, int lane) const {
-        const int n = tail - at;           // bytes of the lane's chunk that belong to the row
-        if (n <= 0 || n >= 16) return;
+        const int n = tail - 16 * ((lane & 3) ^ mm_swz(lane >> 2));   // bytes of the lane's chunk that stay
+        if (n >= 16) return;
 #pragma unroll
         for (int j = 0; j < L; ++j) {
             uint32_t* const d = reinterpret_cast<uint32_t*>(st + (wave * L + j) * 1024 + lane * 16);
 #pragma unroll
-            for (int k = 1; k < 4; ++k)
+            for (int k = 0; k < 4; ++k)
                 if (4 * k >= n) d[k] = 0;
         }
     }
@@ -153,7 +189,7 @@ struct MmScales {
         const int pl = lane / (T / 16), at = lane % (T / 16);
         off = pl < 4 ? (uint32_t)(pl * plane + 16 * at) : kOob;
     }
-    // past the last stage: zeros, for elements that are zeros
+    // (past the last stage: zeros that nobody reads)
     __device__ __forceinline__ void issue(int it, uint32_t dst) {
         const uint8_t* p = next;
         next += step;
@@ -258,30 +294,22 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
     const int64_t nb = (a.C + kMxBlock - 1) / kMxBlock;
     constexpr int ES = 2;
 
-    MmLoad<QT, TQ, L::QL> lq;
-    MmLoad<PT, TP, L::PL> lp;
+    MmLoad<QT, TQ, L::QL, MODE != MM_16 || QT> lq;
+    MmLoad<PT, TP, L::PL, MODE != MM_16 || PT> lp;
     const int groups = (w.nst + 3) / 4;              // W4: a load of weights covers four stages
-    // a dword that the operand ends inside is read whole: it lies in the same 4-byte aligned memory
-    auto end_of = [](const uint8_t* base, int64_t rows, int64_t ld, int64_t bytes) {
-        return base + (rows - 1) * ld + (bytes + 3) / 4 * 4;
-    };
     const int64_t qrow = MX || W4 ? nb * 16 : QT ? a.Q * ES : a.C * ES, prow = MX ? nb * 16 : PT ? a.P * ES : a.C * ES;
-    const uint8_t* const qend = end_of(a.q + (PT || a.E < 1 ? 0 : (a.E - 1) * a.strideq), QT ? a.C : a.Q, a.ldq, qrow);
-    const uint8_t* const pend = end_of(a.p, PT ? a.C : a.P, a.ldp, prow);
     if constexpr (QT) {
-        lq.init(a.q + (PT ? w.c_at * a.ldq : e * a.strideq) + w.st0 * 32 * a.ldq + w.q0 * ES, qend, a.ldq,
-                w.c_len - w.st0 * 32, w.nst, wave, lane, 0, (a.Q - w.q0) * ES);
+        lq.init(a.q + (PT ? w.c_at * a.ldq : e * a.strideq) + w.st0 * 32 * a.ldq + w.q0 * ES, a.ldq,
+                w.c_len - w.st0 * 32, qrow - w.q0 * ES, w.nst, wave, lane);
     } else {
         const int64_t at = W4 ? w.st0 / 4 * 64 : w.st0 * 64;         // W4: splits begin at whole groups of four stages
-        lq.init(a.q + e * a.strideq + w.q0 * a.ldq + at, qend, a.ldq, qrow - at, W4 ? groups : w.nst, wave, lane, 0,
-                a.Q - w.q0);
+        lq.init(a.q + e * a.strideq + w.q0 * a.ldq + at, a.ldq, a.Q - w.q0, qrow - at, W4 ? groups : w.nst, wave, lane);
     }
     if constexpr (PT)
-        lp.init(a.p + (w.c_at + w.st0 * 32) * a.ldp + w.r0 * ES, pend, a.ldp, w.c_len - w.st0 * 32, w.nst, wave, lane,
-                0, (a.P - w.r0) * ES);
+        lp.init(a.p + (w.c_at + w.st0 * 32) * a.ldp + w.r0 * ES, a.ldp, w.c_len - w.st0 * 32, prow - w.r0 * ES, w.nst,
+                wave, lane);
     else
-        lp.init(a.p + w.r0 * a.ldp + w.st0 * 64, pend, a.ldp, prow - w.st0 * 64, w.nst, wave, lane, w.v0 - w.r0,
-                w.r1 - w.r0);
+        lp.init(a.p + w.r0 * a.ldp + w.st0 * 64, a.ldp, w.r1 - w.r0, prow - w.st0 * 64, w.nst, wave, lane);
     // one scale load a wave: mx4 x mx4, those of Q from even waves and of P from odd ones
     MmScales ls;
     MmRowScales<TQ> lw;
@@ -294,27 +322,28 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
     if constexpr (W4)
         lw.init(a.qs + e * a.strideqs + w.q0 * a.ldqs + w.st0, a.ldqs, groups, wave, lane, a.Q - w.q0);
     const int sdst = odd_wave ? L::PS_AT : L::QS_AT;
-    // load U of stage `it` into its ring slot; stages past the last write zeros that nobody reads
-    __amdgpu_buffer_rsrc_t rq, rp;
+    // load U of stage `it` into its ring slot; past the last stage: zeros, or what nobody reads
+    i32x4 rq, rp;
+    const uint32_t wave_q = lds32 + wave * L::QL * 1024, wave_p = lds32 + wave * L::PL * 1024;
     auto load = [&](auto uc, int it) {
         constexpr int U = decltype(uc)::value, NQ = W4 ? 0 : L::QL;
-        const uint32_t dst = lds32 + (it & (L::kRing - 1)) * L::STAGE;
+        const uint32_t slot = (it & (L::kRing - 1)) * L::STAGE;
         if constexpr (U < NQ) {
             if constexpr (U == 0) rq = lq.open(it);
-            lq.template load<U>(rq, it, dst, wave);
+            lq.template load<U, 0>(rq, it, slot + wave_q);
         } else if constexpr (U < NQ + L::PL) {
             if constexpr (U == NQ) rp = lp.open(it);
-            lp.template load<U - NQ>(rp, it, dst + L::P_AT, wave);
+            lp.template load<U - NQ, L::P_AT>(rp, it, slot + wave_p);
         } else if constexpr (MX) {
-            ls.issue(it, dst + sdst);
+            ls.issue(it, lds32 + slot + sdst);
         }
     };
     auto issue = [&](int it) { mm_for<L::VM>([&](auto u) { load(u, it); }); };
     auto issue_w = [&](int grp) {
-        const uint32_t dst = lds32 + L::W_AT + grp % L::WS * L::W_SLOT;
+        const uint32_t slot = grp % L::WS * L::W_SLOT;
         rq = lq.open(grp);
-        mm_for<L::QL>([&](auto u) { lq.template load<decltype(u)::value>(rq, grp, dst, wave); });
-        lw.issue(grp, dst + L::Q_BYTES);
+        mm_for<L::QL>([&](auto u) { lq.template load<decltype(u)::value, L::W_AT>(rq, grp, slot + wave_q); });
+        lw.issue(grp, lds32 + L::W_AT + slot + L::Q_BYTES);
     };
 
     const int wq = wave % WQ, wp = wave / WQ;
@@ -400,8 +429,8 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
         }
     };
 
-    // the stage that the contraction ends inside a chunk of, or -1
-    const int part = MODE == MM_16 && !PT && a.C % 8 != 0 && (w.st0 + w.nst) * 32 >= a.C ? w.nst - 1 : -1;
+    // the stage that the contraction of 16-bit rows ends inside of, or -1
+    const int part = MODE == MM_16 && !PT && a.C % 32 != 0 && (w.st0 + w.nst) * 32 >= a.C ? w.nst - 1 : -1;
     auto clear_part = [&]() {
         uint8_t* const st = lds + (part & (L::kRing - 1)) * L::STAGE;
         if constexpr (!QT) lq.clear(st, wave, lane);
@@ -417,7 +446,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
             if (W4 && s % 4 == 3) issue_w(s / 4 + 1);
         }
         wait_vm<(L::kRing - 1) * L::VM + L::kRing / 4 * L::VMW>();
-        if (MODE == MM_16 && part == 0) clear_part();
+        if (MODE == MM_16 && !PT && part == 0) clear_part();
         lds_barrier();
         Ops o[2];
         mm_for<NRD>([&](auto u) { read(u, 0, o[0]); });
