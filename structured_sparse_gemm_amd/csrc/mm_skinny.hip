@@ -429,8 +429,12 @@ hipError_t pick(const MmArgs& a, int rt, int nt, hipStream_t s) {
 
 int64_t mm_tile_bound(const MmArgs& a, int T) {
     if (!a.offs) return (a.P + T - 1) / T;
-    // a segment's partial tile, and the rows an mx4 tile begins before it
-    return (a.P + (a.mode == MM_MX4 ? 15 * (a.E + 2) : 0)) / T + a.E + 2;
+    // n rows need (n - 1) / T + 1 tiles, rounded down; an mx4 tile begins up to 15
+    // rows before them.  No more segments than rows have any: idle workgroups
+    // are not free (2 tokens, 28 experts: 2 of 30 tiles had rows, and 6496
+    // workgroups took 15 us)
+    const int64_t some = std::min(a.P, a.E + 2);
+    return (a.P + (a.mode == MM_MX4 ? 14 : -1) * some) / T + some;
 }
 
 hipError_t launch_mm_skinny(const MmArgs& a, int rt, int nt, hipStream_t s) {
