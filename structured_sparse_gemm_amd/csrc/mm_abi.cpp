@@ -50,9 +50,12 @@ int to_out(int dt) { return dt == SSG_F32 ? ssg::OUT_F32 : dt == SSG_F16 ? ssg::
 // Times in us of the launches that a plan would make, from what they measured
 // on this chip: a workgroup's time on its CU times the workgroups a CU gets,
 // but no less than the weights take from memory.  Every kernel handles every
-// product it can be chosen for, so a wrong estimate costs time only.
+// product it can be chosen for, so a wrong estimate costs time only.  Over 250
+// random products of each kind (1 .. 64 experts, 64 .. 16384 rows, contractions
+// of 64 .. 12288, 1 .. 8192 tokens), all kernels timed, the choice is 2 to 3%
+// (gradients of the rows: 1%) slower than the best one in the geometric mean.
 
-constexpr double kBytesPerUs = 5.2e6, kTileMx4BytesPerUs = 3.2e6;   // the tiles' 64-byte rows of mx4 weights
+constexpr double kBytesPerUs = 5.2e6;
 
 // Skinny: 16 rt weight rows (rt = 1 .. 4) x 16 nt tokens a workgroup of a
 // 4096-long contraction, by operand types (16-bit, mx4 x mx4, mx4 x 16-bit) and
@@ -63,6 +66,14 @@ constexpr double kBytesPerUs = 5.2e6, kTileMx4BytesPerUs = 3.2e6;   // the tiles
 constexpr double kSkinnyUs[3][2][4] = {{{9.1, 19.0, 0, 36.0}, {13.0, 16.0, 0, 27.0}},
                                        {{4.4, 4.7, 6.0, 6.8}, {6.0, 6.5, 0, 8.0}},
                                        {{6.0, 7.8, 9.2, 10.3}, {10.6, 11.9, 0, 14.1}}};
+
+// The same for other lengths, in parts of it: the start, and the rest by
+// length / 4096.  Workgroups that share their scales (rt >= 3) start once for
+// every 4096 elements.
+struct SkinnyShape {
+    double start, length, shared_start, shared_length;
+};
+constexpr SkinnyShape kSkinnyShape[3] = {{0.2, 0.7, 0, 0}, {0.3, 0.9, 0.9, 0.45}, {0.1, 0.7, 0.7, 0.2}};
 
 struct Plan {
     bool skinny;
@@ -101,19 +112,25 @@ Plan plan(const MmArgs& a) {
     };
     auto ceil_div = [](int64_t n, int64_t d) { return (double)((n + d - 1) / d); };
     const double bytes = a.pt ? 0 : busy * (double)a.Q * (double)a.C * (a.mode == ssg::MM_16 ? 2 : 0.53);
-    const double tile_floor = bytes / (a.mode == ssg::MM_16 ? kBytesPerUs : kTileMx4BytesPerUs);
+    const double floor_us = bytes / kBytesPerUs;
     double best = 1e30;
-    if (!a.qt && !a.pt && avg <= 128) {
+    if (!a.qt && !a.pt && avg <= 160) {
         for (int nt = 1; nt <= (avg > 16 ? 2 : 1); ++nt)
             for (int rt = 1; rt <= 4; ++rt) {
                 const double full = kSkinnyUs[a.mode][nt - 1][rt - 1];
                 if (full == 0) continue;
                 const double wgs = ceil_div(a.Q, 16 * rt) * row_tiles(16 * nt);
                 const double fill = std::min(1.0, avg / (16 * nt));   // tokens of a tile that exist
-                const double one = full * (0.2 + 0.8 * (double)a.C / 4096) * (0.7 + 0.3 * fill);
-                // (16-bit workgroups are small enough to run side by side)
-                const double more = std::max(0.0, std::ceil(wgs / kCUs) - 1) * (a.mode == ssg::MM_16 ? 0.85 : 1);
-                const double us = 3.5 + std::max((1 + more) * one, bytes / kBytesPerUs);
+                const bool shared = rt >= 3 && a.mode != ssg::MM_16;  // scales through LDS, 4096 elements a round
+                const SkinnyShape& h = kSkinnyShape[a.mode];
+                auto one = [&](int64_t C) {
+                    const double len = (double)C / 4096;
+                    const double parts = shared ? h.shared_start * std::ceil(len) + h.shared_length * len
+                                                : h.start + h.length * len;
+                    return full * parts * (0.7 + 0.3 * fill);
+                };
+                const double more = std::max(0.0, std::ceil(wgs / kCUs) - 1) * 0.8;
+                const double us = 3.5 + std::max((1 + more) * one(a.C), floor_us);
                 if (us < best) {
                     best = us;
                     p.skinny = true;
@@ -123,9 +140,10 @@ Plan plan(const MmArgs& a) {
                 }
                 // few rows of long weights: several workgroups a row, each with
                 // at least one step a wave (shared scales: one round)
-                const int64_t unit = rt >= 3 && a.mode != ssg::MM_16 ? 4096 : 8 * (a.mode == ssg::MM_MX4 ? 256 : 128);
+                const int64_t unit = shared ? 4096 : 8 * (a.mode == ssg::MM_MX4 ? 256 : 128);
                 for (int splits = 2; splits <= 8 && unit * splits <= a.C && wgs * splits <= kCUs; splits *= 2) {
-                    const double us2 = 3.5 + std::max(one / splits, bytes / kBytesPerUs) + 4 +
+                    const int64_t rounds = (a.C + unit - 1) / unit;
+                    const double us2 = 3.5 + std::max(one((rounds + splits - 1) / splits * unit), floor_us) + 8 +
                                        (double)splits * a.P * a.Q * 8 / 3e6;
                     if (us2 >= best) continue;
                     best = us2;
@@ -136,27 +154,31 @@ Plan plan(const MmArgs& a) {
                 }
             }
     }
-    // Tiles: a stage takes as long as its products at the rate of a full chip,
-    // or its latency.  A split adds the pass over its partials.
+    // Tiles: a stage takes as long as its products at the rate of a full chip
+    // (smaller tiles for a last round of at most half, and less for one that
+    // leaves CUs idle), or its latency.  A split adds the pass over its partials.
     const int64_t stages = (a.pt ? (int64_t)((double)a.C / E) : a.C) / (a.mode == ssg::MM_MX4 ? 128 : 32) + 1;
     for (int k = 0; k < 3; ++k) {
         const ssg::MmTileSize& t = ssg::kMmTileSizes[k];
         const double tiles = row_tiles(t.p) * ceil_div(a.Q, t.q);
-        const double stage = t.q * t.p * (a.mode == ssg::MM_MX4 ? 1.3 : 1.0) / t.rate / 78000;
+        const double stage = t.q * t.p * (a.mode == ssg::MM_MX4 ? 1.3 : 1.1) / t.rate / 78000;
         for (int splits = 1; splits <= 8; splits *= 2) {
             if (splits > 1 && (a.pt || k == 0 || stages / splits < 8)) break;
             const double n = tiles * splits, whole = std::floor(n / kCUs), rest = n - whole * kCUs;
             double us;
             if (k == 0) {
-                const double cut = rest <= 0 ? 0 : rest <= kCUs / 4 ? 0.3 : rest <= kCUs / 2 ? 0.55 : 1;
+                const double cut = rest <= 0           ? 0
+                                   : rest <= kCUs / 4 ? 0.3
+                                   : rest <= kCUs / 2 ? 0.55
+                                                      : 0.35 + 0.65 * rest / kCUs;
                 us = (whole * stage + (cut > 0 ? std::max(t.latency, cut * stage) : 0)) * stages;
             } else {
                 const double m = n <= kCUs ? 1 : n / kCUs + 0.25;
                 us = std::max(t.latency * std::ceil(m / t.per_cu), m * stage) * (double)(stages / splits);
             }
-            us = 6.5 + std::max(us, tile_floor);
+            us = 6.5 + std::max(us, floor_us);
             if (splits > 1) us += 4 + (double)splits * a.P * a.Q * 8 / 3e6;
-            if (a.mode == ssg::MM_MX4) us += 6;
+            if (a.mode == ssg::MM_MX4) us += 5;   // the scale planes
             if (us < best) {
                 best = us;
                 p.skinny = false;
