@@ -612,9 +612,10 @@ int ssg_mx4_dequantize(int dtype, int64_t R, int64_t K, const uint8_t* elems, in
  * W, scales and xscales: bytes.
  *
  * The *_workspace_bytes call with the same operands gives the workspace a
- * product needs (0 for few rows and for most aligned operands): partial sums
- * where the contraction is split, copies of operands whose rows are not
- * aligned to 16 bytes.  ws may be NULL where it is 0.
+ * product needs (0 for few rows and most 16-bit operands): partial sums where
+ * the contraction is split, the scales of two mx4 operands rearranged, and
+ * copies of operands whose rows do not begin at 16 bytes (mx4) or at 4 (16-bit;
+ * also those contracted along an odd length).  ws may be NULL where it is 0.
  */
 size_t ssg_mm_mx4_workspace_bytes(int x, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
                                   const uint8_t* xscales, int64_t ldxs, const uint8_t* W, int64_t ldw,
