@@ -3,12 +3,19 @@
 //
 // Bound by reading the weights once.  A workgroup owns 16 * RT weight rows and
 // 16 * NT tokens of one expert; its 8 waves split the contraction, each wave
-// loads both operands from memory straight into MFMA operand registers (no
-// LDS, no barrier in the loop: with at most 32 tokens nothing is worth
-// sharing between waves), and the waves' fp32 sums meet once in LDS, added in
+// loads both operands from memory straight into MFMA operand registers (not
+// through LDS: with at most 32 tokens no element is worth sharing between
+// waves), and the waves' fp32 sums meet once in LDS, added in
 // wave order.  Any length, stride and alignment is taken: rows and tokens past
 // the end repeat the last one (their results are not stored), and the last
 // steps of a row load under guards.
+//
+// Measured (copy of 1 GiB: 5.2 TB/s): mx4 4096 x 4096, one bf16 token 5.9 us
+// (8.9 MB; 3 to 4 us of it pass before the first weight arrives); mx4 11008 x
+// 4096, 16 fp16 tokens 12.3 us; 36 of 64 mx4 experts of 2048 x 4096 43.8 us (159
+// MB, 3.6 TB/s: 64 bytes a row and wave leave 128-byte lines to be read twice
+// where two workgroups a CU fill the L2 - 199 MB come from memory); two fp16
+// experts of 4096 x 4096 16.2 us (67 MB, 4.1 TB/s).
 //
 // A wave's step is kStep contraction elements:
 // * 16-bit: lane (i, g) loads 16 bytes of row i, elements 32 u + 8 g, u < 8.

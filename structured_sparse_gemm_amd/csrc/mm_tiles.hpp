@@ -35,6 +35,12 @@
 //   elements) every fourth stage and stay 4-bit in LDS; a wave widens its
 //   fragment (4 conversions) on the way into the MFMA.
 //
+// Measured: 16-bit 4096^3 114 us, 1.2 PFLOP/s (the vendor's product 97 us), its
+// input gradient 122 to 127 us, weight gradient 119 to 127; mx4 x mx4 45 us, 3.05
+// PFLOP/s; mx4 x 16-bit 109 us.  8192^3: 1.34 to 1.39 PFLOP/s (vendor: 1.3 to 1.6 on
+// the same cards), mx4 x mx4 4.3.  The matrix units are busy 39 to 49% of the
+// cycles of the cases of a layer's size.
+//
 // Workgroups are dealt round-robin to the 8 XCDs; tile numbers are dealt so
 // that each XCD gets a contiguous range, walked 8 row tiles at a time, which
 // keeps the operand panels of the tiles in flight in its L2.  The number of
