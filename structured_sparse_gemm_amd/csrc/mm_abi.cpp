@@ -63,7 +63,7 @@ constexpr double kBytesPerUs = 5.2e6;
 // (fp16 x mx4 at 11008 x 4096 x 16: 21, 19, 13, 15 us for rt = 1 .. 4; at 4096 x
 // 4096: 10, 12, 13, 14); 16-bit weights with rt > 1 are priced up to where many
 // workgroups measured (11008 x 4096 x 16: 30, 33, -, 32 us).
-constexpr double kSkinnyUs[3][2][4] = {{{9.1, 19.0, 0, 36.0}, {13.0, 16.0, 0, 27.0}},
+constexpr double kSkinnyUs[3][2][4] = {{{8.4, 19.0, 0, 36.0}, {13.0, 16.0, 0, 27.0}},
                                        {{4.4, 4.7, 6.0, 6.8}, {6.0, 6.5, 0, 8.0}},
                                        {{6.0, 7.8, 9.2, 10.3}, {10.6, 11.9, 0, 14.1}}};
 

@@ -15,7 +15,7 @@
 // 4096, 16 fp16 tokens 12.3 us; 36 of 64 mx4 experts of 2048 x 4096 43.8 us (159
 // MB, 3.6 TB/s: 64 bytes a row and wave leave 128-byte lines to be read twice
 // where two workgroups a CU fill the L2 - 199 MB come from memory); two fp16
-// experts of 4096 x 4096 16.2 us (67 MB, 4.1 TB/s).
+// experts of 4096 x 4096 14.1 us (67 MB, 4.8 TB/s).
 //
 // A wave's step is kStep contraction elements:
 // * 16-bit: lane (i, g) loads 16 bytes of row i, elements 32 u + 8 g, u < 8.
@@ -96,6 +96,10 @@ struct Skinny {
     // elements of every row, it takes 37 and 31; with fewer than 48 rows a
     // workgroup the barriers cost more than the requests.
     static constexpr bool SHARED = MODE != MM_16 && RT >= 3;
+    // Steps whose loads go out together: small 16-bit workgroups leave a wave
+    // with little in flight (fp16 4096 x 4096, one token: 9.6 us instead of 11.5;
+    // 11008 x 4096: 21.6 instead of 23.4).  mx4 workgroups gain nothing.
+    static constexpr int AHEAD = MODE != MM_16 ? 1 : RT * NT == 1 ? 4 : RT * NT == 2 ? 2 : 1;
 
     // One step's operands.
     struct Ops {
@@ -288,6 +292,15 @@ struct Skinny {
         // a block that K ends inside is whole in an mx4 operand, not in a 16-bit one
         const int64_t whole = (MX ? nb * kMxBlock : a.C) / S, steps = (a.C + S - 1) / S;
         Ops o;
+        if constexpr (!ODD && AHEAD > 1) {
+            for (; n + (AHEAD - 1) * by < whole; n += AHEAD * by) {
+                Ops b[AHEAD];
+#pragma unroll
+                for (int d = 0; d < AHEAD; ++d) load<true>((n + d * by) * S, b[d]);
+#pragma unroll
+                for (int d = 0; d < AHEAD; ++d) products<ODD>(b[d], 0);
+            }
+        }
         for (; n < whole; n += by) {
             load<true>(n * S, o);
             products<ODD>(o, 0);
