@@ -13,8 +13,7 @@
 // Measured (copy of 1 GiB: 5.2 TB/s): mx4 4096 x 4096, one bf16 token 5.9 us
 // (8.9 MB; 3 to 4 us of it pass before the first weight arrives); mx4 11008 x
 // 4096, 16 fp16 tokens 12.3 us; 36 of 64 mx4 experts of 2048 x 4096 43.8 us (159
-// MB, 3.6 TB/s: 64 bytes a row and wave leave 128-byte lines to be read twice
-// where two workgroups a CU fill the L2 - 199 MB come from memory); two fp16
+// MB needed, 199 read from memory by the counters: 4.5 TB/s); two fp16
 // experts of 4096 x 4096 14.1 us (67 MB, 4.8 TB/s).
 //
 // A wave's step is kStep contraction elements:
