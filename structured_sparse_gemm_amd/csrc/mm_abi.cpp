@@ -55,7 +55,7 @@ int to_out(int dt) { return dt == SSG_F32 ? ssg::OUT_F32 : dt == SSG_F16 ? ssg::
 // of 64 .. 12288, 1 .. 8192 tokens), all kernels timed, the choice is 2 to 3%
 // (gradients of the rows: 1%) slower than the best one in the geometric mean.
 
-constexpr double kBytesPerUs = 5.2e6;
+constexpr double kBytesPerUs = 5.2e6, kCopyBytesPerUs = 4.5e6;
 
 // Skinny: 16 rt weight rows (rt = 1 .. 4) x 16 nt tokens a workgroup of a
 // 4096-long contraction, by operand types (16-bit, mx4 x mx4, mx4 x 16-bit) and
@@ -113,6 +113,19 @@ Plan plan(const MmArgs& a) {
     auto ceil_div = [](int64_t n, int64_t d) { return (double)((n + d - 1) / d); };
     const double bytes = a.pt ? 0 : busy * (double)a.Q * (double)a.C * (a.mode == ssg::MM_16 ? 2 : 0.53);
     const double floor_us = bytes / kBytesPerUs;
+    const int64_t qb = q_bytes(a), pb = p_bytes(a), nb = blocks(a.C);
+    // Tiles load rows 16 bytes at a time.  16-bit operands may begin at any dword
+    // (an odd contraction length ends inside one); others at 16 bytes.  The
+    // kernel finds the end of transposed rows of part chunks with 31 bits.
+    const int64_t q_al = a.mode != ssg::MM_16 ? 16 : a.qt || a.C % 2 == 0 ? 4 : 0;
+    const int64_t p_al = a.mode != ssg::MM_16 ? 16 : a.pt || a.C % 2 == 0 ? 4 : 0;
+    auto far = [](int64_t rows, int64_t ld) { return rows * ld >= (int64_t)1 << 31; };
+    p.copy_q = q_al == 0 || (qb % 16 && (q_al == 16 || (a.qt && far(q_rows(a), a.ldq)))) || !al(a.q, q_al) ||
+               a.ldq % q_al || a.strideq % q_al;
+    p.copy_p = p_al == 0 || (pb % 16 && (p_al == 16 || (a.pt && far(p_rows(a), a.ldp)))) || !al(a.p, p_al) ||
+               a.ldp % p_al;
+    const double copies = (p.copy_q ? 4 + 2 * bytes / kCopyBytesPerUs : 0) +
+                          (p.copy_p ? 4 + 2 * (double)p_rows(a) * (double)pb / kCopyBytesPerUs : 0);
     double best = 1e30;
     if (!a.qt && !a.pt && avg <= 160) {
         for (int nt = 1; nt <= (avg > 16 ? 2 : 1); ++nt)
@@ -176,7 +189,7 @@ Plan plan(const MmArgs& a) {
                 const double m = n <= kCUs ? 1 : n / kCUs + 0.25;
                 us = std::max(t.latency * std::ceil(m / t.per_cu), m * stage) * (double)(stages / splits);
             }
-            us = 6.5 + std::max(us, floor_us);
+            us = 6.5 + std::max(us, floor_us) + copies;
             if (splits > 1) us += 4 + (double)splits * a.P * a.Q * 8 / 3e6;
             if (a.mode == ssg::MM_MX4) us += 5;   // the scale planes
             if (us < best) {
@@ -197,22 +210,11 @@ Plan plan(const MmArgs& a) {
         at += up(n, 256);
         return r;
     };
-    const int64_t qb = q_bytes(a), pb = p_bytes(a), nb = blocks(a.C);
-    // Rows are loaded 16 bytes at a time.  16-bit operands may begin at any dword
-    // (an odd contraction length ends inside one); others at 16 bytes.  The
-    // kernel finds the end of transposed rows of part chunks with 31 bits.
-    const int64_t q_al = a.mode != ssg::MM_16 ? 16 : a.qt || a.C % 2 == 0 ? 4 : 0;
-    const int64_t p_al = a.mode != ssg::MM_16 ? 16 : a.pt || a.C % 2 == 0 ? 4 : 0;
-    auto far = [](int64_t rows, int64_t ld) { return rows * ld >= (int64_t)1 << 31; };
-    if (q_al == 0 || (qb % 16 && (q_al == 16 || (a.qt && far(q_rows(a), a.ldq)))) || !al(a.q, q_al) || a.ldq % q_al ||
-        a.strideq % q_al) {
-        p.copy_q = true;
+    if (p.copy_q) {
         p.ldq = up(qb, 16);
         p.at_q = take(q_mats(a) * q_rows(a) * p.ldq);
     }
-    if (p_al == 0 || (pb % 16 && (p_al == 16 || (a.pt && far(p_rows(a), a.ldp)))) || !al(a.p, p_al) ||
-        a.ldp % p_al) {
-        p.copy_p = true;
+    if (p.copy_p) {
         p.ldp = up(pb, 16);
         p.at_p = take(p_rows(a) * p.ldp);
     }

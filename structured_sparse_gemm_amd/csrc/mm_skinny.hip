@@ -171,21 +171,34 @@ struct Skinny {
         return make_uint4(0, 0, 0, 0);
     }
 
-    // elements k + 8 g .. + 7 of a 16-bit row
-    template <bool FULL>
+    // elements k + 8 g .. + 7 of a 16-bit row.  HALF: rows may begin inside a
+    // dword, where a 16-byte load is cut into many (3 fp16 experts of 4928 x
+    // 2605, 37 rows: 59 us): the dwords that hold the elements, moved together.
+    template <bool FULL, bool HALF>
     __device__ __forceinline__ uint4 ld_row(const uint8_t* base, uint32_t off, int64_t k, int imm) const {
-        if constexpr (FULL) return ld16(base + k * 2, off + 16 * g, imm);
-        else return ld8(base + off, k + imm / 2 + 8 * g, a.C);
+        if constexpr (FULL && HALF) {
+            const uint32_t b = (uint32_t)reinterpret_cast<uintptr_t>(base) & 2, m = (b + off) & 2;
+            const uint32_t at = off + b - m + 16 * g;
+            const uint4 v = ld16(base - b + k * 2, at, imm);
+            uint32_t last;
+            __builtin_memcpy(&last, base - b + k * 2 + at + imm + (m ? 16 : 12), 4);
+            return make_uint4(__builtin_amdgcn_alignbit(v.y, v.x, 8 * m), __builtin_amdgcn_alignbit(v.z, v.y, 8 * m),
+                              __builtin_amdgcn_alignbit(v.w, v.z, 8 * m), __builtin_amdgcn_alignbit(last, v.w, 8 * m));
+        } else if constexpr (FULL) {
+            return ld16(base + k * 2, off + 16 * g, imm);
+        } else {
+            return ld8(base + off, k + imm / 2 + 8 * g, a.C);
+        }
     }
 
-    template <bool FULL>
+    template <bool FULL, bool HALF = false>
     __device__ __forceinline__ void load(int64_t k0, Ops& o) const {
         const int64_t b0 = k0 / kMxBlock;
         if constexpr (MODE == MM_16) {
 #pragma unroll
             for (int u = 0; u < UW; ++u)
 #pragma unroll
-                for (int r = 0; r < RT; ++r) o.w[r][u] = ld_row<FULL>(q, qo[r], k0, 64 * u);
+                for (int r = 0; r < RT; ++r) o.w[r][u] = ld_row<FULL, HALF>(q, qo[r], k0, 64 * u);
         } else {
 #pragma unroll
             for (int r = 0; r < RT; ++r)
@@ -210,7 +223,7 @@ struct Skinny {
 #pragma unroll
             for (int u = 0; u < UX; ++u)
 #pragma unroll
-                for (int t = 0; t < NT; ++t) o.x[t][u] = ld_row<FULL>(p, po[t], k0, 64 * u);
+                for (int t = 0; t < NT; ++t) o.x[t][u] = ld_row<FULL, HALF>(p, po[t], k0, 64 * u);
         }
     }
 
@@ -285,13 +298,13 @@ struct Skinny {
 
     // This wave's part of the contraction: steps n, n + by, ..  ODD
     // (mx4 weights against 16-bit activations): the elements unscaled, their
-    // sums scaled in fp32.
-    template <bool ODD>
+    // sums scaled in fp32.  HALF: see ld_row.
+    template <bool ODD, bool HALF = false>
     __device__ __forceinline__ void run_steps(int64_t n, int64_t by) {
         // a block that K ends inside is whole in an mx4 operand, not in a 16-bit one
         const int64_t whole = (MX ? nb * kMxBlock : a.C) / S, steps = (a.C + S - 1) / S;
         Ops o;
-        if constexpr (!ODD && AHEAD > 1) {
+        if constexpr (!ODD && !HALF && AHEAD > 1) {
             for (; n + (AHEAD - 1) * by < whole; n += AHEAD * by) {
                 Ops b[AHEAD];
 #pragma unroll
@@ -301,7 +314,7 @@ struct Skinny {
             }
         }
         for (; n < whole; n += by) {
-            load<true>(n * S, o);
+            load<true, HALF>(n * S, o);
             products<ODD>(o, 0);
         }
         if (n < steps) {
@@ -397,7 +410,10 @@ __global__ void __launch_bounds__(kThreads, RT == 4 && NT == 1 ? 4 : 2) k_mm_ski
         } else {
             // splits take the steps in turn
             const int64_t first = (int64_t)split * kWaves + wave, by = (int64_t)a.splits * kWaves;
-            k.template run_steps<false>(first, by);
+            if (MODE == MM_16 && ((reinterpret_cast<uintptr_t>(k.q) | reinterpret_cast<uintptr_t>(k.p) | a.ldq | a.ldp) & 2))
+                k.template run_steps<false, MODE == MM_16>(first, by);
+            else
+                k.template run_steps<false>(first, by);
             if constexpr (MODE == MM_W4) {
                 if (__any(k.odd)) {
                     k.zero();
