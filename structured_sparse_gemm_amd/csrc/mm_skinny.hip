@@ -325,7 +325,7 @@ struct Skinny {
 
     // The same with shared scales: slice `wave` of every round of this split.  Every wave
     // takes part in the barriers.
-    template <bool ODD>
+    template <bool ODD, bool HALF = false>
     __device__ __forceinline__ void run_rounds(int wave, int split) {
         const int64_t whole = MX ? nb * kMxBlock : a.C;
         // rounds of equal length, a wave's slices of them whole steps
@@ -337,7 +337,7 @@ struct Skinny {
             load_scales(n * kWaves * slice / kMxBlock, v);
             Ops o;
             if (k0 < a.C) {            // the first step's loads are under way while the scales arrive
-                if (k0 + S <= whole) load<true>(k0, o);
+                if (k0 + S <= whole) load<true, HALF>(k0, o);
                 else load<false>(k0, o);
             }
             if (n > split) lds_barrier();  // every wave has read the last round's scales
@@ -348,7 +348,7 @@ struct Skinny {
                 const int64_t k = k0 + h;
                 if (k >= a.C) break;
                 if (h > 0) {
-                    if (k + S <= whole) load<true>(k, o);
+                    if (k + S <= whole) load<true, HALF>(k, o);
                     else load<false>(k, o);
                 }
                 products<ODD>(o, (wave * slice + h) / kMxBlock);
@@ -396,10 +396,14 @@ __global__ void __launch_bounds__(kThreads, RT == 4 && NT == 1 ? 4 : 2) k_mm_ski
         k.pso[t] = (uint32_t)(row * a.ldps);
     }
     k.zero();
+    // 16-bit rows that may begin inside a dword
+    const bool half = (MODE != MM_MX4 && (reinterpret_cast<uintptr_t>(k.p) | a.ldp) & 2) ||
+                      (MODE == MM_16 && (reinterpret_cast<uintptr_t>(k.q) | a.ldq) & 2);
     if (tile.e >= 0) {
         k.odd = false;
         if constexpr (K::SHARED) {
-            k.template run_rounds<false>(wave, (int)split);
+            if (half) k.template run_rounds<false, MODE != MM_MX4>(wave, (int)split);
+            else k.template run_rounds<false>(wave, (int)split);
             if constexpr (MODE == MM_W4) {
                 if (__syncthreads_or(k.odd)) {
                     k.zero();
@@ -410,10 +414,8 @@ __global__ void __launch_bounds__(kThreads, RT == 4 && NT == 1 ? 4 : 2) k_mm_ski
         } else {
             // splits take the steps in turn
             const int64_t first = (int64_t)split * kWaves + wave, by = (int64_t)a.splits * kWaves;
-            if (MODE == MM_16 && ((reinterpret_cast<uintptr_t>(k.q) | reinterpret_cast<uintptr_t>(k.p) | a.ldq | a.ldp) & 2))
-                k.template run_steps<false, MODE == MM_16>(first, by);
-            else
-                k.template run_steps<false>(first, by);
+            if (half) k.template run_steps<false, MODE != MM_MX4>(first, by);
+            else k.template run_steps<false>(first, by);
             if constexpr (MODE == MM_W4) {
                 if (__any(k.odd)) {
                     k.zero();

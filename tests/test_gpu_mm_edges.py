@@ -101,3 +101,17 @@ def test_long_contractions_of_few_rows(x, M, K, N):
         xv = X.double().numpy()
         Y = ssg.mm_mx4(X.cuda(), dev(e), dev(s))
     D.check(Y, xv @ wv.T, np.abs(xv) @ np.abs(wv).T, K, "mm_mx4")
+
+
+@pytest.mark.parametrize("before,after", [(0, 0), (1, 0), (1, 1), (2, 1), (3, 4)])
+@pytest.mark.parametrize("M,K,sizes", [(100, 257, [3, 0, 20]), (33, 1001, [1]), (520, 4097, [16, 17, 1]), (264, 640, [40])])
+def test_few_rows_that_begin_anywhere(before, after, M, K, sizes):
+    """16-bit rows at odd elements, with NaN around the operands."""
+    offs, nan = D.offsets(sizes), float("nan")
+    X, W = D.randn((sum(sizes), K), "f16", 51), D.randn((len(sizes), M, K), "f16", 52, 0.1)
+    e, s = D.random_mx4((len(sizes), M, K), 53)
+    Xv, x = inside(X, before, after, nan), X.double().numpy()
+    D.check(ssg.grouped_mm(Xv, inside(W, before, after, nan), offs.cuda(), out_dtype=torch.float32),
+            *D.grouped(x, W.double().numpy(), offs), K, "16-bit weights")
+    D.check(ssg.grouped_mm_mx4(Xv, dev(e), dev(s), offs.cuda()), *D.grouped(x, D.mx4_values(e, s, K), offs), K,
+            "mx4 weights")
