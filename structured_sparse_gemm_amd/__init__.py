@@ -806,15 +806,25 @@ def _on_device(t: torch.Tensor, name: str) -> Optional[int]:
     return t.data_ptr() or None
 
 
+def _row_stride(R: int, C: int, ld: int, unit: int, name: str) -> int:
+    """Row stride of R rows of C columns; that of a single row, or of rows
+    without columns, means nothing.  Rows that repeat or overlap (expanded or
+    unfolded tensors) are refused."""
+    if unit != 1 and C > 1:
+        raise SsgError(_abi.SSG_ERR_STRIDE, "%s must have unit column stride" % name)
+    if R <= 1 or C == 0:
+        return C
+    if ld < C:
+        raise SsgError(_abi.SSG_ERR_STRIDE, "rows of %s overlap: row stride %d < %d" % (name, ld, C))
+    return ld
+
+
 def _mat(t: torch.Tensor, name: str) -> Tuple[Optional[int], int]:
     """(address, row stride) of a matrix with unit column stride."""
     if t.dim() != 2:
         raise SsgError(_abi.SSG_ERR_SHAPE, "%s must be 2-D, got shape %s" % (name, tuple(t.shape)))
-    R, C = t.shape
-    ld, unit = t.stride()
-    if unit != 1 and C > 1:
-        raise SsgError(_abi.SSG_ERR_STRIDE, "%s must have unit column stride" % name)
-    return _on_device(t, name), (ld if R > 1 and ld > C else C)
+    ld = _row_stride(*t.shape, *t.stride(), name)
+    return _on_device(t, name), ld
 
 
 def _stack(t: torch.Tensor, name: str) -> Tuple[Optional[int], int, int]:
@@ -822,10 +832,8 @@ def _stack(t: torch.Tensor, name: str) -> Tuple[Optional[int], int, int]:
     if t.dim() != 3:
         raise SsgError(_abi.SSG_ERR_SHAPE, "%s must be 3-D, got shape %s" % (name, tuple(t.shape)))
     E, R, C = t.shape
-    stride, ld, unit = t.stride()
-    if unit != 1 and C > 1:
-        raise SsgError(_abi.SSG_ERR_STRIDE, "%s must have unit column stride" % name)
-    ld = ld if R > 1 and ld > C else C
+    stride, *rows = t.stride()
+    ld = _row_stride(R, C, *rows, name)
     return _on_device(t, name), ld, (stride if E > 1 else R * ld)
 
 

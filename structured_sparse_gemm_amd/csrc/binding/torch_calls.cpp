@@ -46,12 +46,20 @@ const at::Tensor* tensor(PyObject* o, int device) {
     return t.is_cuda() && t.get_device() == device ? &t : nullptr;
 }
 
+// Row stride of rows x cols; that of a single row, or of rows without columns,
+// means nothing.  False for rows that repeat or overlap, and for columns apart.
+bool row_stride(int64_t rows, int64_t cols, int64_t ld, int64_t unit, int64_t* out) {
+    if (cols > 1 && unit != 1) return false;
+    const bool any = rows <= 1 || cols == 0;
+    *out = any ? cols : ld;
+    return any || ld >= cols;
+}
+
 bool mat(const at::Tensor& t, Mat* m) {
     if (t.dim() != 2) return false;
     m->rows = t.size(0);
     m->cols = t.size(1);
-    if (m->cols > 1 && t.stride(1) != 1) return false;
-    m->ld = m->rows > 1 && t.stride(0) > m->cols ? t.stride(0) : m->cols;
+    if (!row_stride(m->rows, m->cols, t.stride(0), t.stride(1), &m->ld)) return false;
     m->p = t.data_ptr();
     return true;
 }
@@ -61,8 +69,7 @@ bool stack(const at::Tensor& t, Stack* s) {
     s->mats = t.size(0);
     s->rows = t.size(1);
     s->cols = t.size(2);
-    if (s->cols > 1 && t.stride(2) != 1) return false;
-    s->ld = s->rows > 1 && t.stride(1) > s->cols ? t.stride(1) : s->cols;
+    if (!row_stride(s->rows, s->cols, t.stride(1), t.stride(2), &s->ld)) return false;
     s->stride = s->mats > 1 ? t.stride(0) : s->rows * s->ld;
     s->p = t.data_ptr();
     return true;

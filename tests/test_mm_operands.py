@@ -1,0 +1,123 @@
+"""Operands that the mx4 and expert-grouped calls have to refuse, or take, by
+their strides and extents.  Refusals come before anything is enqueued."""
+import pytest
+import torch
+
+import structured_sparse_gemm_amd as ssg
+from structured_sparse_gemm_amd import _abi
+from tests import _mm as D
+
+NULL, SHAPE, STRIDE = _abi.SSG_ERR_NULL, _abi.SSG_ERR_SHAPE, _abi.SSG_ERR_STRIDE
+
+
+def status(f, *a, **k):
+    with pytest.raises(ssg.SsgError) as e:
+        f(*a, **k)
+    return e.value.status
+
+
+def repeated(t):
+    """t's shape, every row the first one: row stride 0."""
+    return t[..., :1, :].expand(t.shape)
+
+
+def overlapping(t):
+    """t's shape, every row one element after the one before."""
+    strides = list(t.stride())
+    strides[-2] = 1
+    return t.as_strided(t.shape, strides)
+
+
+def operands(device):
+    X, dY = (torch.ones(6, c, dtype=torch.float16, device=device) for c in (64, 8))
+    W = torch.ones(2, 8, 64, dtype=torch.float16, device=device)
+    e, s = (torch.zeros(2, 8, c, dtype=torch.uint8, device=device) for c in (32, 2))
+    xe, xs = (torch.zeros(6, c, dtype=torch.uint8, device=device) for c in (32, 2))
+    return X, dY, W, e, s, xe, xs, torch.tensor([0, 2, 6], dtype=torch.int32, device=device)
+
+
+def calls_with(bad, device):
+    """Every call with one operand in the layout `bad`; each is a function to
+    call, and what it would call in the compiled marshalling (None: no such call)."""
+    X, dY, W, e, s, xe, xs, offs = operands(device)
+    f16, f32 = torch.float16, torch.float32
+    Y, dX, dW = (torch.empty(n, device=device) for n in ((6, 8), (6, 64), (2, 8, 64)))
+    prod, grp = "mx4_product", "grouped_product"
+    return [
+        (ssg.mx4_quantize, (bad(X),), ("mx4_quantize", bad(X))),
+        (ssg.mx4_dequantize, (bad(xe), xs, 64), ("mx4_dequantize", bad(xe), xs, 64, f32)),
+        (ssg.mx4_dequantize, (xe, bad(xs), 64), ("mx4_dequantize", xe, bad(xs), 64, f32)),
+        (ssg.mm_mx4, (bad(X), e[0], s[0]), (prod, bad(X), None, e[0], s[0], None, f32)),
+        (ssg.mm_mx4, (X, bad(e[0]), s[0]), (prod, X, None, bad(e[0]), s[0], None, f32)),
+        (ssg.mm_mx4, (X, e[0], bad(s[0])), (prod, X, None, e[0], bad(s[0]), None, f32)),
+        (ssg.mm_mx4, (bad(xe), e[0], s[0], xs), (prod, bad(xe), xs, e[0], s[0], None, f32)),
+        (ssg.mm_mx4, (xe, e[0], s[0], bad(xs)), (prod, xe, bad(xs), e[0], s[0], None, f32)),
+        (ssg.grouped_mm_mx4, (bad(X), e, s, offs), (prod, bad(X), None, e, s, offs, f32)),
+        (ssg.grouped_mm_mx4, (X, bad(e), s, offs), (prod, X, None, bad(e), s, offs, f32)),
+        (ssg.grouped_mm_mx4, (X, e, bad(s), offs), (prod, X, None, e, bad(s), offs, f32)),
+        (ssg.grouped_mm, (bad(X), W, offs), (grp, 0, bad(X), W, offs, f16)),
+        (ssg.grouped_mm, (X, bad(W), offs), (grp, 0, X, bad(W), offs, f16)),
+        (ssg.grouped_mm_dx, (bad(dY), W, offs), (grp, 1, bad(dY), W, offs, f16)),
+        (ssg.grouped_mm_dx, (dY, bad(W), offs), (grp, 1, dY, bad(W), offs, f16)),
+        (ssg.grouped_mm_dw, (bad(dY), X, offs), (grp, 2, bad(dY), X, offs, f16)),
+        (ssg.grouped_mm_dw, (dY, bad(X), offs), (grp, 2, dY, bad(X), offs, f16)),
+        # outputs
+        (ssg.ssg_mx4_quantize, (X, bad(xe), xs), None),
+        (ssg.ssg_mx4_quantize, (X, xe, bad(xs)), None),
+        (ssg.ssg_mx4_dequantize, (xe, xs, bad(dX)), None),
+        (ssg.ssg_mm_mx4, (X, e[0], s[0], bad(Y)), None),
+        (ssg.ssg_grouped_mm_mx4, (X, e, s, offs, bad(Y)), None),
+        (ssg.ssg_grouped_mm, (X, W, offs, bad(Y)), None),
+        (ssg.ssg_grouped_mm_dx, (dY, W, offs, bad(dX)), None),
+        (ssg.ssg_grouped_mm_dw, (dY, X, offs, bad(dW)), None),
+    ]
+
+
+class NoLibrary:
+    """Takes every call and does nothing."""
+    def __getattr__(self, name):
+        return lambda *args: 0
+
+
+@pytest.fixture
+def host_tensors(monkeypatch):
+    """Host tensors get as far as the library, and no call leaves the binding."""
+    monkeypatch.setattr(ssg, "_lib", NoLibrary)
+    monkeypatch.setattr(ssg, "_on_device", lambda t, name: t.data_ptr())
+    monkeypatch.setattr(ssg, "_raw_stream", lambda t, stream: None)
+
+
+@pytest.mark.parametrize("bad", [repeated, overlapping])
+def test_rows_that_repeat_or_overlap_are_refused(bad, host_tensors):
+    for f, args, _ in calls_with(lambda t: t, "cpu"):
+        f(*args)
+    for i, (f, args, _) in enumerate(calls_with(bad, "cpu")):
+        assert status(f, *args) == STRIDE, (i, f.__name__)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [repeated, overlapping])
+def test_rows_that_repeat_or_overlap_are_refused_on_the_device(bad):
+    compiled = _abi.torch_calls()
+    for i, (f, args, call) in enumerate(calls_with(bad, "cuda")):
+        if call is not None:
+            assert getattr(compiled, call[0])(*call[1:]) is None, (i, call[0])
+        assert status(f, *args) == STRIDE, (i, f.__name__)
+
+
+@pytest.mark.gpu
+def test_strides_without_a_meaning():
+    # a single row, and rows of one column, whatever their strides; one weight
+    # for every expert
+    gen = torch.Generator().manual_seed(5)
+    x, w = torch.randn(1, 64, generator=gen).half(), torch.randn(1, 8, 64, generator=gen).half()
+    offs = torch.tensor([0, 0, 1], dtype=torch.int32).cuda()
+    X, W = x.cuda().as_strided((1, 64), (0, 1)), w.cuda().expand(2, 8, 64)
+    D.check(ssg.grouped_mm(X, W, offs), (x.double() @ w[0].double().t()).numpy(),
+            (x.double().abs() @ w[0].double().abs().t()).numpy(), 64, "one row")
+    dY = torch.randn(5, 3, generator=gen).half().cuda()
+    one = torch.ones(2, 1, 3, dtype=torch.float16).cuda().transpose(1, 2)       # [2, 3, 1], strides (3, 1, 3)
+    offs = torch.tensor([0, 2, 5], dtype=torch.int32).cuda()
+    got = ssg.grouped_mm_dx(dY, one, offs, out_dtype=torch.float32)
+    ref = dY.double().cpu()
+    D.check(got, ref.sum(1, keepdim=True).numpy(), ref.abs().sum(1, keepdim=True).numpy(), 3, "one column")
