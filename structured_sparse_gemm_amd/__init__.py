@@ -101,12 +101,23 @@ def _ptr(t: Optional[torch.Tensor], name: str):
     return t.data_ptr() if t.numel() > 0 else None
 
 
+def _row_stride(R: int, C: int, ld: int, unit: int, name: str) -> int:
+    """Row stride of R rows of C columns; that of a single row, or of rows
+    without columns, means nothing.  Rows that repeat or overlap (expanded or
+    unfolded tensors) are refused."""
+    if unit != 1 and C > 1:
+        raise SsgError(_abi.SSG_ERR_STRIDE, "%s must have unit column stride" % name)
+    if R <= 1 or C == 0:
+        return C
+    if ld < C:
+        raise SsgError(_abi.SSG_ERR_STRIDE, "rows of %s overlap: row stride %d < %d" % (name, ld, C))
+    return ld
+
+
 def _ld(t: torch.Tensor, name: str) -> int:
     if t.dim() != 2:
         raise SsgError(_abi.SSG_ERR_SHAPE, "%s must be 2-D, got shape %s" % (name, tuple(t.shape)))
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise SsgError(_abi.SSG_ERR_STRIDE, "%s must have unit column stride" % name)
-    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+    return _row_stride(*t.shape, *t.stride(), name)
 
 
 def _stream(t: torch.Tensor, stream) -> Optional[int]:
@@ -804,19 +815,6 @@ def _on_device(t: torch.Tensor, name: str) -> Optional[int]:
     if not t.is_cuda:
         raise SsgError(_abi.SSG_ERR_NULL, "%s must be a ROCm device tensor (got %s)" % (name, t.device))
     return t.data_ptr() or None
-
-
-def _row_stride(R: int, C: int, ld: int, unit: int, name: str) -> int:
-    """Row stride of R rows of C columns; that of a single row, or of rows
-    without columns, means nothing.  Rows that repeat or overlap (expanded or
-    unfolded tensors) are refused."""
-    if unit != 1 and C > 1:
-        raise SsgError(_abi.SSG_ERR_STRIDE, "%s must have unit column stride" % name)
-    if R <= 1 or C == 0:
-        return C
-    if ld < C:
-        raise SsgError(_abi.SSG_ERR_STRIDE, "rows of %s overlap: row stride %d < %d" % (name, ld, C))
-    return ld
 
 
 def _mat(t: torch.Tensor, name: str) -> Tuple[Optional[int], int]:

@@ -83,8 +83,10 @@ class NoLibrary:
 def host_tensors(monkeypatch):
     """Host tensors get as far as the library, and no call leaves the binding."""
     monkeypatch.setattr(ssg, "_lib", NoLibrary)
-    monkeypatch.setattr(ssg, "_on_device", lambda t, name: t.data_ptr())
-    monkeypatch.setattr(ssg, "_raw_stream", lambda t, stream: None)
+    for name in ("_on_device", "_ptr"):
+        monkeypatch.setattr(ssg, name, lambda t, name: None if t is None else t.data_ptr())
+    for name in ("_raw_stream", "_stream"):
+        monkeypatch.setattr(ssg, name, lambda t, stream: None)
 
 
 @pytest.mark.parametrize("bad", [repeated, overlapping])
@@ -121,3 +123,19 @@ def test_strides_without_a_meaning():
     got = ssg.grouped_mm_dx(dY, one, offs, out_dtype=torch.float32)
     ref = dY.double().cpu()
     D.check(got, ref.sum(1, keepdim=True).numpy(), ref.abs().sum(1, keepdim=True).numpy(), 3, "one column")
+
+
+@pytest.mark.parametrize("bad", [repeated, overlapping])
+def test_rows_of_sparse_operands_that_repeat_or_overlap_are_refused(bad, host_tensors):
+    A, B, C = torch.ones(8, 64, dtype=torch.float16), torch.ones(64, 4, dtype=torch.float16), torch.empty(8, 4)
+    v, m = torch.ones(8, 32, dtype=torch.float16), torch.full((8, 8), 0x44, dtype=torch.uint8)
+    calls = [(ssg.ssg_prune_2to4, 0, A, A.clone()), (ssg.ssg_prune_2to4, 1, A, A.clone()),
+             (ssg.ssg_compress_2to4, 0, A, v, m), (ssg.ssg_compress_2to4, 1, A, v, m), (ssg.ssg_compress_2to4, 2, A, v, m),
+             (ssg.ssg_decompress_2to4, 2, v, m, A), (ssg.ssg_compress_2to4_prefill, 0, A, v, m),
+             (ssg.ssg_spmm_2to4_packed, 3, v, m, 8, B, C), (ssg.ssg_spmm_2to4_packed, 4, v, m, 8, B, C),
+             (ssg.ssg_spmm_2to4_packed_bt, 3, v, m, 8, A, C), (ssg.ssg_spmm_2to4_prefill, 3, v, m, 8, B, C),
+             (ssg.ssg_spmm_2to4_prefill_bt, 3, v, m, 8, A, C)]
+    for i, (f, at, *args) in enumerate(calls):
+        f(*args)
+        args[at] = bad(args[at])
+        assert status(f, *args) == STRIDE, (i, f.__name__)
