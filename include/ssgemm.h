@@ -636,7 +636,8 @@ int ssg_mm_mx4(int x, int y, int64_t M, int64_t N, int64_t K, const void* X, int
  *   ssg_grouped_mm_dw    dW_e[m, k] = sum_{n of e} dY[n, m] X[n, k] (zeros for
  *                        an expert without rows)
  * Outputs are fp32 or the inputs' type; sums are fp32.  16-bit strides count
- * elements, those of mx4 operands and scales bytes.
+ * elements, those of mx4 operands and scales bytes.  Matrices of dW that share
+ * elements are refused (SSG_ERR_STRIDE).
  */
 size_t ssg_grouped_mm_mx4_workspace_bytes(int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* X,
                                           int64_t ldx, const uint8_t* xscales, int64_t ldxs,

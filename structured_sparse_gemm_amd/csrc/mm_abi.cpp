@@ -318,6 +318,22 @@ int check_y(const char* name, const void* y, int64_t rows, int64_t cols, int64_t
     return SSG_OK;
 }
 
+// The matrices of an output stack may lie one after the other or between each
+// other's rows, but must not share elements.  d matrices on, a row is moved by
+// d * stride: the rows nearest to it are the two around that many.
+int check_apart(const char* name, int64_t E, int64_t rows, int64_t cols, int64_t ld, int64_t stride) {
+    if (rows == 0 || cols == 0) return SSG_OK;
+    const int64_t s = stride < 0 ? -stride : stride;
+    if (s >= (rows - 1) * ld + cols) return SSG_OK;
+    for (int64_t d = 1; d < E; ++d) {
+        const int64_t m = d * s / ld, r = d * s - m * ld;
+        if (m >= rows) break;
+        if (r < cols || (m + 1 < rows && ld - r < cols))
+            return fail(SSG_ERR_STRIDE, "matrices of %s overlap: stride %lld", name, (ll)stride);
+    }
+    return SSG_OK;
+}
+
 // X [N, K] (16-bit or mx4) against mx4 weights [E][M, K].
 int mx4_args(int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const uint8_t* xs,
              int64_t ldxs, const uint8_t* W, int64_t ldw, int64_t stridew, const uint8_t* S, int64_t lds,
@@ -503,7 +519,9 @@ int ssg_grouped_mm_dw(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, 
                       void* ws, size_t ws_bytes, void* stream) {
     MmArgs a{};
     int rc = grouped_args(DW, x, E, M, N, K, dY, lddy, X, ldx, 0, offs, &a);
-    if (rc || (rc = check_out(x, y)) || (rc = check_y("dW", dW, E * M, K, lddw))) return rc;
+    if (rc || (rc = check_out(x, y)) || (rc = check_y("dW", dW, E * M, K, lddw)) ||
+        (rc = check_apart("dW", E, M, K, lddw, stridedw)))
+        return rc;
     a.out = to_out(y);
     a.y = dW;
     a.ldy = lddw;

@@ -1,5 +1,7 @@
 """Operands that the mx4 and expert-grouped calls have to refuse, or take, by
 their strides and extents.  Refusals come before anything is enqueued."""
+import ctypes
+
 import pytest
 import torch
 
@@ -7,7 +9,7 @@ import structured_sparse_gemm_amd as ssg
 from structured_sparse_gemm_amd import _abi
 from tests import _mm as D
 
-NULL, SHAPE, STRIDE = _abi.SSG_ERR_NULL, _abi.SSG_ERR_SHAPE, _abi.SSG_ERR_STRIDE
+SHAPE, STRIDE, WORKSPACE = _abi.SSG_ERR_SHAPE, _abi.SSG_ERR_STRIDE, _abi.SSG_ERR_WORKSPACE
 
 
 def status(f, *a, **k):
@@ -139,3 +141,42 @@ def test_rows_of_sparse_operands_that_repeat_or_overlap_are_refused(bad, host_te
         f(*args)
         args[at] = bad(args[at])
         assert status(f, *args) == STRIDE, (i, f.__name__)
+
+
+def test_weight_gradients_that_share_elements_are_refused():
+    lib, at = _abi.load(), ctypes.c_void_p(0x1000)     # never dereferenced: no rows, or refused
+
+    def dw(E, M, K, ld, stride):
+        # rows of odd length need a workspace: without one, nothing is enqueued
+        assert K % 2 == 1
+        return lib.ssg_grouped_mm_dw(0, 3, E, M, 300, K, at, M + 1, at, K, at, at, ld, stride, None, 0, None)
+
+    def apart(E, M, K, ld, stride):
+        starts = [e * stride + m * ld for e in range(E) for m in range(M)]
+        cells = [a + k for a in starts for k in range(K)]
+        return len(set(cells)) == len(cells)
+
+    seen = set()
+    for E, M, K in [(2, 3, 5), (3, 2, 5), (4, 4, 3), (2, 1, 5), (5, 3, 1)]:
+        for ld in (K, K + 1, 2 * K, 3 * K + 1, 5 * K):
+            for stride in [*range(-2, 5 * K), M * ld - ld, M * ld - ld + K - 1, M * ld - ld + K, M * ld, -M * ld]:
+                ok = apart(E, M, K, ld, stride)
+                seen.add(ok)
+                assert dw(E, M, K, ld, stride) == (WORKSPACE if ok else STRIDE), (E, M, K, ld, stride)
+    assert seen == {False, True}
+    assert dw(1, 3, 5, 5, 0) == WORKSPACE                  # one matrix: the stride means nothing
+
+
+@pytest.mark.gpu
+def test_weight_gradients_in_any_layout_that_keeps_them_apart():
+    gen = torch.Generator().manual_seed(6)
+    dY, X = (torch.randn(70, c, generator=gen).half() for c in (12, 24))
+    offs = D.offsets([30, 0, 40])
+    ref = D.grouped_dw(dY.double().numpy(), X.double().numpy(), offs)
+    between = torch.empty(12, 3, 24).cuda().transpose(0, 1)      # every matrix's row m side by side
+    apart = torch.empty(3, 15, 30).cuda()[:, :12, :24]
+    for dW in (between, apart):
+        ssg.ssg_grouped_mm_dw(dY.cuda(), X.cuda(), offs.cuda(), dW)
+        D.check(dW, *ref, 40, "dW")
+    for dW in (torch.empty(1, 12, 24).cuda().expand(3, 12, 24), torch.empty(500).cuda().as_strided((3, 12, 24), (24, 24, 1))):
+        assert status(ssg.ssg_grouped_mm_dw, dY.cuda(), X.cuda(), offs.cuda(), dW) == STRIDE
