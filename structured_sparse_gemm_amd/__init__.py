@@ -927,7 +927,8 @@ def _mm_mx4_operands(X, W, scales, xscales):
     _need(X.dim() == 2 and W.dim() == 2 and scales.dim() == 2, "X, W and scales must be 2-D", X, W, scales)
     K = X.shape[1] if xscales is None else 2 * X.shape[1]
     M, nb = W.shape[0], (K + 31) // 32
-    _need(W.shape[1] == 16 * nb and scales.shape == (M, nb), "shapes of X, W, scales", X, W, scales)
+    _need(W.shape[1] == 16 * nb and scales.shape == (M, nb) and (xscales is None or X.shape[1] == W.shape[1]),
+          "shapes of X, W, scales", X, W, scales)
     x, xa = _mx4_activations(X, xscales, nb)
     _same_device(X, W, scales, xscales)
     return (x, M, X.shape[0], K, *xa, *_mat(W, "W"), *_mat(scales, "scales"))
@@ -939,7 +940,8 @@ def _grouped_mm_mx4_operands(X, W, scales, offs, xscales):
     _need(X.dim() == 2 and W.dim() == 3 and scales.dim() == 3, "X must be 2-D, W and scales 3-D", X, W, scales)
     K = X.shape[1] if xscales is None else 2 * X.shape[1]
     E, M, nb = W.shape[0], W.shape[1], (K + 31) // 32
-    _need(W.shape[2] == 16 * nb and scales.shape == (E, M, nb), "shapes of X, W, scales", X, W, scales)
+    _need(W.shape[2] == 16 * nb and scales.shape == (E, M, nb) and (xscales is None or X.shape[1] == W.shape[2]),
+          "shapes of X, W, scales", X, W, scales)
     x, xa = _mx4_activations(X, xscales, nb)
     _same_device(X, W, scales, offs, xscales)
     return (x, E, M, X.shape[0], K, *xa, *_stack(W, "W"), *_stack(scales, "scales"), _offsets(offs, E))

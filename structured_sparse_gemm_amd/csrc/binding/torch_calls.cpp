@@ -114,6 +114,7 @@ PyObject* mx4_product(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int64_t K = mx ? 2 * mx_x.cols : mx_x.cols, nb = (K + 31) / 32, N = mx_x.rows;
     if (mx) {
         const at::Tensor* xs = tensor(args[1], dev);
+        if (mx_x.cols % 16) return none();             // mx4 rows are whole blocks
         if (!xs || xs->scalar_type() != at::kByte || !mat(*xs, &mx_s) || mx_s.rows != N || mx_s.cols != nb) return none();
     }
     uint8_t* const xs = (uint8_t*)mx_s.p;

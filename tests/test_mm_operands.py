@@ -180,3 +180,25 @@ def test_weight_gradients_in_any_layout_that_keeps_them_apart():
         D.check(dW, *ref, 40, "dW")
     for dW in (torch.empty(1, 12, 24).cuda().expand(3, 12, 24), torch.empty(500).cuda().as_strided((3, 12, 24), (24, 24, 1))):
         assert status(ssg.ssg_grouped_mm_dw, dY.cuda(), X.cuda(), offs.cuda(), dW) == STRIDE
+
+
+@pytest.mark.parametrize("cols", [1, 15, 17, 31, 33])
+def test_mx4_activations_that_end_inside_a_block_are_refused(cols, host_tensors):
+    nb = (2 * cols + 31) // 32
+    X, xs = torch.zeros(6, 64, dtype=torch.uint8)[:, :cols], torch.zeros(6, nb, dtype=torch.uint8)
+    W, s = torch.zeros(2, 8, 16 * nb, dtype=torch.uint8), torch.zeros(2, 8, nb, dtype=torch.uint8)
+    offs = torch.zeros(3, dtype=torch.int32)
+    assert status(ssg.mm_mx4, X, W[0], s[0], xs) == SHAPE
+    assert status(ssg.grouped_mm_mx4, X, W, s, offs, xs) == SHAPE
+    assert status(ssg.ssg_mm_mx4_workspace_bytes, X, W[0], s[0], xs) == SHAPE
+
+
+@pytest.mark.gpu
+def test_mx4_activations_that_end_inside_a_block_are_refused_on_the_device():
+    X, xs = torch.zeros(6, 64, dtype=torch.uint8).cuda()[:, :17], torch.zeros(6, 2, dtype=torch.uint8).cuda()
+    W, s = torch.zeros(2, 8, 32, dtype=torch.uint8).cuda(), torch.zeros(2, 8, 2, dtype=torch.uint8).cuda()
+    offs, compiled = torch.zeros(3, dtype=torch.int32).cuda(), _abi.torch_calls()
+    for w, t, o in ((W[0], s[0], None), (W, s, offs)):
+        assert compiled.mx4_product(X, xs, w, t, o, torch.float32) is None
+    assert status(ssg.mm_mx4, X, W[0], s[0], xs) == SHAPE
+    assert status(ssg.grouped_mm_mx4, X, W, s, offs, xs) == SHAPE
