@@ -96,7 +96,7 @@ int64_t p_bytes(const MmArgs& a) {
     if (a.mode == ssg::MM_MX4) return blocks(a.C) * 16;
     return (a.pt ? a.P : a.C) * 2;
 }
-int64_t q_mats(const MmArgs& a) { return a.pt ? 1 : std::max<int64_t>(a.E, 1); }
+int64_t q_mats(const MmArgs& a) { return a.pt ? 1 : a.E; }   // (E is 1 without offsets)
 
 Plan plan(const MmArgs& a) {
     Plan p{};

@@ -202,3 +202,28 @@ def test_mx4_activations_that_end_inside_a_block_are_refused_on_the_device():
         assert compiled.mx4_product(X, xs, w, t, o, torch.float32) is None
     assert status(ssg.mm_mx4, X, W[0], s[0], xs) == SHAPE
     assert status(ssg.grouped_mm_mx4, X, W, s, offs, xs) == SHAPE
+
+
+def test_no_experts_need_no_copy_of_their_weights():
+    # the copy of an absent stack would begin at a null pointer: it shows as workspace
+    lib, at = _abi.load(), ctypes.c_void_p(0x1000)
+    for N in (200, 5000):
+        assert lib.ssg_grouped_mm_workspace_bytes(0, 0, 64, N, 33, at, 33, None, 33, 0, at) == -(-N * 80 // 256) * 256
+        assert lib.ssg_grouped_mm_dx_workspace_bytes(0, 0, 64, N, 33, at, 64, None, 33, 0, at) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [1, 200, 3000])
+@pytest.mark.parametrize("K", [33, 64, 100])
+def test_no_experts(N, K):
+    offs = torch.zeros(1, dtype=torch.int32).cuda()
+    for f, cols, out in ((ssg.grouped_mm, K, 66), (ssg.grouped_mm_dx, 66, K)):
+        X = torch.ones(N, cols, dtype=torch.float16).cuda()
+        Y = f(X, torch.empty(0, 66, K, dtype=torch.float16).cuda(), offs)
+        assert Y.shape == (N, out) and (Y == 0).all()
+    nb = (K + 31) // 32
+    W, s = torch.empty(0, 66, 16 * nb, dtype=torch.uint8).cuda(), torch.empty(0, 66, nb, dtype=torch.uint8).cuda()
+    Xe, Xs = torch.full((N, 16 * nb), 0x22, dtype=torch.uint8).cuda(), torch.full((N, nb), 127, dtype=torch.uint8).cuda()
+    for Y in (ssg.grouped_mm_mx4(torch.ones(N, K, dtype=torch.bfloat16).cuda(), W, s, offs),
+              ssg.grouped_mm_mx4(Xe, W, s, offs, xscales=Xs)):
+        assert Y.shape == (N, 66) and (Y == 0).all()
