@@ -1049,6 +1049,11 @@ def _compiled():
     return _calls
 
 
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """The rows of a stack [E, R, C] as a matrix."""
+    return t.reshape(t.shape[0] * t.shape[1], t.shape[2])
+
+
 def mx4_quantize(A: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(elements, scales) of A [R, K] or a stack [E, R, K] in the mx4 format:
     uint8 [.., 16 * ceil(K / 32)] and uint8 [.., ceil(K / 32)]."""
@@ -1057,8 +1062,8 @@ def mx4_quantize(A: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tens
         if done is not None:
             return done
     if A.dim() == 3:
-        e, s = mx4_quantize(A.reshape(-1, A.shape[2]), stream)
-        return e.view(*A.shape[:2], -1), s.view(*A.shape[:2], -1)
+        e, s = mx4_quantize(_rows(A), stream)
+        return e.view(*A.shape[:2], e.shape[1]), s.view(*A.shape[:2], s.shape[1])
     _need(A.dim() == 2, "A must be 2-D or 3-D", A)
     nb = (A.shape[1] + 31) // 32
     elems = _empty((A.shape[0], 16 * nb), torch.uint8, A, stream)
@@ -1075,7 +1080,7 @@ def mx4_dequantize(elems: torch.Tensor, scales: torch.Tensor, K: int, dtype: tor
         if done is not None:
             return done
     if elems.dim() == 3:
-        d = mx4_dequantize(elems.reshape(-1, elems.shape[2]), scales.reshape(-1, scales.shape[2]), K, dtype, stream)
+        d = mx4_dequantize(_rows(elems), _rows(scales), K, dtype, stream)
         return d.view(*elems.shape[:2], K)
     _need(elems.dim() == 2, "elems must be 2-D or 3-D", elems)
     D = _empty((elems.shape[0], K), dtype, elems, stream)

@@ -227,3 +227,24 @@ def test_no_experts(N, K):
     for Y in (ssg.grouped_mm_mx4(torch.ones(N, K, dtype=torch.bfloat16).cuda(), W, s, offs),
               ssg.grouped_mm_mx4(Xe, W, s, offs, xscales=Xs)):
         assert Y.shape == (N, 66) and (Y == 0).all()
+
+
+EMPTY = [(0, 5, 70), (3, 0, 70), (3, 5, 0), (0, 0, 0), (2, 0, 0)]
+
+
+def back_and_forth(E, R, K, device):
+    nb = (K + 31) // 32
+    e, s = ssg.mx4_quantize(torch.zeros(E, R, K, dtype=torch.bfloat16, device=device))
+    assert e.shape == (E, R, 16 * nb) and s.shape == (E, R, nb)
+    assert ssg.mx4_dequantize(e, s, K).shape == (E, R, K)
+
+
+@pytest.mark.parametrize("E,R,K", EMPTY)
+def test_empty_stacks(E, R, K, host_tensors):
+    back_and_forth(E, R, K, "cpu")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,R,K", EMPTY)
+def test_empty_stacks_on_the_device(E, R, K):
+    back_and_forth(E, R, K, "cuda")
