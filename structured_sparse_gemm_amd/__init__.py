@@ -1080,6 +1080,7 @@ def mx4_dequantize(elems: torch.Tensor, scales: torch.Tensor, K: int, dtype: tor
         if done is not None:
             return done
     if elems.dim() == 3:
+        _need(scales.dim() == 3 and scales.shape[:2] == elems.shape[:2], "shapes of elems, scales", elems, scales)
         d = mx4_dequantize(_rows(elems), _rows(scales), K, dtype, stream)
         return d.view(*elems.shape[:2], K)
     _need(elems.dim() == 2, "elems must be 2-D or 3-D", elems)

@@ -248,3 +248,9 @@ def test_empty_stacks(E, R, K, host_tensors):
 @pytest.mark.parametrize("E,R,K", EMPTY)
 def test_empty_stacks_on_the_device(E, R, K):
     back_and_forth(E, R, K, "cuda")
+
+
+def test_scales_of_another_stack_are_refused(host_tensors):
+    e = torch.zeros(2, 3, 32, dtype=torch.uint8)
+    for s in (torch.zeros(3, 2, 2, dtype=torch.uint8), torch.zeros(6, 2, dtype=torch.uint8)):
+        assert status(ssg.mx4_dequantize, e, s, 64) == SHAPE
