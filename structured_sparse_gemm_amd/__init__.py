@@ -13,6 +13,7 @@ allocate their outputs.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional, Tuple
 
@@ -858,11 +859,16 @@ def _raw_stream(t: torch.Tensor, stream) -> Optional[int]:
     return _stream(t, stream)
 
 
+def _on_stream(like: torch.Tensor, stream):
+    """What torch allocates and runs in this block goes to the stream that a call names."""
+    if stream is None or like.device.type != "cuda":    # host tensors are refused later
+        return contextlib.nullcontext()
+    return torch.cuda.stream(_torch_stream(like, stream))
+
+
 def _empty(shape, dtype, like: torch.Tensor, stream):
     """A new tensor, allocated on the stream the kernels run on."""
-    if stream is None or like.device.type != "cuda":    # host tensors are refused later
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(_torch_stream(like, stream)):
+    with _on_stream(like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
@@ -1049,9 +1055,11 @@ def _compiled():
     return _calls
 
 
-def _rows(t: torch.Tensor) -> torch.Tensor:
-    """The rows of a stack [E, R, C] as a matrix."""
-    return t.reshape(t.shape[0] * t.shape[1], t.shape[2])
+def _rows(t: torch.Tensor, stream) -> torch.Tensor:
+    """The rows of a stack [E, R, C] as a matrix; where they are not equally far
+    apart, a copy made on the stream the kernels run on."""
+    with _on_stream(t, stream):
+        return t.reshape(t.shape[0] * t.shape[1], t.shape[2])
 
 
 def mx4_quantize(A: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -1062,7 +1070,7 @@ def mx4_quantize(A: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tens
         if done is not None:
             return done
     if A.dim() == 3:
-        e, s = mx4_quantize(_rows(A), stream)
+        e, s = mx4_quantize(_rows(A, stream), stream)
         return e.view(*A.shape[:2], e.shape[1]), s.view(*A.shape[:2], s.shape[1])
     _need(A.dim() == 2, "A must be 2-D or 3-D", A)
     nb = (A.shape[1] + 31) // 32
@@ -1081,7 +1089,7 @@ def mx4_dequantize(elems: torch.Tensor, scales: torch.Tensor, K: int, dtype: tor
             return done
     if elems.dim() == 3:
         _need(scales.dim() == 3 and scales.shape[:2] == elems.shape[:2], "shapes of elems, scales", elems, scales)
-        d = mx4_dequantize(_rows(elems), _rows(scales), K, dtype, stream)
+        d = mx4_dequantize(_rows(elems, stream), _rows(scales, stream), K, dtype, stream)
         return d.view(*elems.shape[:2], K)
     _need(elems.dim() == 2, "elems must be 2-D or 3-D", elems)
     D = _empty((elems.shape[0], K), dtype, elems, stream)

@@ -1,5 +1,6 @@
 """Operands that the mx4 and expert-grouped calls have to refuse, or take, by
 their strides and extents.  Refusals come before anything is enqueued."""
+import contextlib
 import ctypes
 
 import pytest
@@ -254,3 +255,45 @@ def test_scales_of_another_stack_are_refused(host_tensors):
     e = torch.zeros(2, 3, 32, dtype=torch.uint8)
     for s in (torch.zeros(3, 2, 2, dtype=torch.uint8), torch.zeros(6, 2, dtype=torch.uint8)):
         assert status(ssg.mx4_dequantize, e, s, 64) == SHAPE
+
+
+@pytest.mark.gpu
+def test_stacks_are_read_on_the_stream_that_the_call_names():
+    # weights that `side` is still about to write, in stacks whose rows are not
+    # equally far apart
+    gen = torch.Generator().manual_seed(8)
+    wide = torch.randn(4, 40, 96, generator=gen).bfloat16().cuda()
+    e, s = ssg.mx4_quantize(wide[:, :30])
+    values = ssg.mx4_dequantize(e, s, 96)
+    late = torch.zeros(4, 40, 96, dtype=torch.bfloat16).cuda()
+    le, ls = (torch.zeros(4, 40, c, dtype=torch.uint8).cuda() for c in (48, 3))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        late.copy_(wide)
+        le[:, :30].copy_(e)
+        ls[:, :30].copy_(s)
+    e2, s2 = ssg.mx4_quantize(late[:, :30], stream=side)
+    got = ssg.mx4_dequantize(le[:, :30], ls[:, :30], 96, stream=side)
+    side.synchronize()
+    assert torch.equal(e2, e) and torch.equal(s2, s) and torch.equal(got, values)
+
+
+def test_copies_of_stacks_are_made_on_the_stream_that_the_call_names(host_tensors, monkeypatch):
+    inside, copied = [], []
+    real = torch.Tensor.reshape
+
+    @contextlib.contextmanager
+    def on_stream(like, stream):
+        inside.append(stream)
+        yield
+        inside.pop()
+
+    monkeypatch.setattr(ssg, "_on_stream", on_stream, raising=False)
+    monkeypatch.setattr(torch.Tensor, "reshape", lambda t, *a: (copied.append(list(inside)), real(t, *a))[1])
+    wide = torch.zeros(4, 40, 96, dtype=torch.bfloat16)
+    e, s = ssg.mx4_quantize(wide[:, :30], stream=77)
+    assert copied == [[77]]
+    ssg.mx4_dequantize(e[:, :9], s[:, :9], 96, stream=78)
+    assert copied[1:] == [[78], [78]]
