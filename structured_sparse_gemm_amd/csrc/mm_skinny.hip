@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, RT == 4 && NT == 1 ? 4 : 2) k_mm_ski
     // 16-bit rows that may begin inside a dword
     const bool half = (MODE != MM_MX4 && (reinterpret_cast<uintptr_t>(k.p) | a.ldp) & 2) ||
                       (MODE == MM_16 && (reinterpret_cast<uintptr_t>(k.q) | a.ldq) & 2);
-    if (tile.e >= 0) {
+    if (tile.e >= 0 && a.C > 0) {      // (no contraction: no rounds to share out, the sums are zero)
         k.odd = false;
         if constexpr (K::SHARED) {
             if (half) k.template run_rounds<false, MODE != MM_MX4>(wave, (int)split);

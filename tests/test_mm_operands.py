@@ -297,3 +297,22 @@ def test_copies_of_stacks_are_made_on_the_stream_that_the_call_names(host_tensor
     assert copied == [[77]]
     ssg.mx4_dequantize(e[:, :9], s[:, :9], 96, stream=78)
     assert copied[1:] == [[78], [78]]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [1, 40, 300])
+def test_contractions_of_no_elements(N):
+    def empty(*shape, dtype=torch.uint8):
+        return torch.empty(*shape, dtype=dtype).cuda()
+
+    offs = torch.tensor([0, 0, N], dtype=torch.int32).cuda()
+    e, s = empty(2, 70, 0), empty(2, 70, 0)
+    for X, xs in ((empty(N, 0, dtype=torch.float16), None), (empty(N, 0, dtype=torch.bfloat16), None),
+                  (empty(N, 0), empty(N, 0))):
+        for Y in (ssg.mm_mx4(X, e[0], s[0], xs), ssg.grouped_mm_mx4(X, e, s, offs, xs)):
+            assert Y.shape == (N, 70) and (Y == 0).all()
+    h = empty(N, 0, dtype=torch.float16)
+    Y = ssg.grouped_mm(h, empty(2, 70, 0, dtype=torch.float16), offs)
+    assert Y.shape == (N, 70) and (Y == 0).all()
+    dX = ssg.grouped_mm_dx(h, empty(2, 0, 70, dtype=torch.float16), offs)
+    assert dX.shape == (N, 70) and (dX == 0).all()
