@@ -113,7 +113,7 @@ struct Skinny {
     uint8_t* sc;                       // LDS: scales of 16 RT weight rows, then of 16 NT tokens (mx4 x mx4)
     int64_t nb;                        // scale bytes of a row
     int i, g;
-    bool odd;                          // met a scale that the 16-bit type cannot hold
+    bool odd;                          // met a scale that the 16-bit type may not hold
     f32x4 acc[RT][NT];
 
     // The scales of 128 blocks from `first` on, 16 bytes a thread: from memory,
@@ -271,7 +271,7 @@ struct Skinny {
                     for (int j = 0; j < 4; ++j) {
                         const uint32_t s = (s4 >> (8 * j)) & 0xFFu;
                         if constexpr (!ODD) {
-                            odd |= s - kSafeLo<DT> > kSafeHi<DT> - kSafeLo<DT>;
+                            odd |= mx4_unsafe<DT>(s);
                             const uint4 v = mx4_widen<DT>(d[j], __uint_as_float(s << 23));
 #pragma unroll
                             for (int t = 0; t < NT; ++t) acc[r][t] = mfma16<DT>(v, o.x[t][4 * u + j], acc[r][t]);
@@ -287,6 +287,13 @@ struct Skinny {
                     }
                 }
         }
+    }
+
+    // Whether an unsafe scale that was met matters: groups of `len` blocks, `step`
+    // apart from `first` on, by thread t of n.
+    __device__ __forceinline__ bool not_exact(uint32_t first, uint32_t len, uint32_t step, int t, int n) const {
+        return mx4_not_exact<DT>(q, a.ldq, qs, a.ldqs, (uint32_t)std::min<int64_t>(qrows, 16 * RT), first, len, step,
+                                 (uint32_t)nb, t, n);
     }
 
     __device__ __forceinline__ void zero() {
@@ -323,6 +330,10 @@ struct Skinny {
         }
     }
 
+    __device__ __forceinline__ int slice_of(int64_t rounds) const {
+        return (int)(((a.C + rounds * kWaves - 1) / (rounds * kWaves) + S - 1) / S * S);
+    }
+
     // The same with shared scales: slice `wave` of every round of this split.  Every wave
     // takes part in the barriers.
     template <bool ODD, bool HALF = false>
@@ -330,7 +341,7 @@ struct Skinny {
         const int64_t whole = MX ? nb * kMxBlock : a.C;
         // rounds of equal length, a wave's slices of them whole steps
         const int64_t rounds = (a.C + kRound - 1) / kRound;
-        const int slice = (int)(((a.C + rounds * kWaves - 1) / (rounds * kWaves) + S - 1) / S * S);
+        const int slice = slice_of(rounds);
         for (int64_t n = split; n < rounds; n += a.splits) {
             const int64_t k0 = (n * kWaves + wave) * slice;
             uint4 v[SPT];
@@ -406,8 +417,12 @@ __global__ void __launch_bounds__(kThreads, RT == 4 && NT == 1 ? 4 : 2) k_mm_ski
             else k.template run_rounds<false>(wave, (int)split);
             if constexpr (MODE == MM_W4) {
                 if (__syncthreads_or(k.odd)) {
-                    k.zero();
-                    k.template run_rounds<true>(wave, (int)split);
+                    const uint32_t round = kWaves * k.slice_of((a.C + kRound - 1) / kRound) / kMxBlock;
+                    if (__syncthreads_or(k.not_exact((uint32_t)split * round, round, (uint32_t)a.splits * round,
+                                                     threadIdx.x, kThreads))) {
+                        k.zero();
+                        k.template run_rounds<true>(wave, (int)split);
+                    }
                 }
             }
             __syncthreads();           // the scales give way to the sums
@@ -417,7 +432,8 @@ __global__ void __launch_bounds__(kThreads, RT == 4 && NT == 1 ? 4 : 2) k_mm_ski
             if (half) k.template run_steps<false, MODE != MM_MX4>(first, by);
             else k.template run_steps<false>(first, by);
             if constexpr (MODE == MM_W4) {
-                if (__any(k.odd)) {
+                constexpr uint32_t B = K::S / kMxBlock;
+                if (__any(k.odd) && __any(k.not_exact((uint32_t)first * B, B, (uint32_t)by * B, lane, 64))) {
                     k.zero();
                     k.template run_steps<true>(first, by);
                 }

@@ -418,7 +418,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
     auto widen = [&](auto xc, int b, const Ops& o) -> uint4 {
         constexpr int X = decltype(xc)::value;
         const uint32_t s = (wsc[X] >> (8 * b)) & 0xFFu;
-        odd |= s - kSafeLo<DT> > kSafeHi<DT> - kSafeLo<DT>;
+        odd |= mx4_unsafe<DT>(s);
         return mx4_widen<DT>(o.qd[X], __uint_as_float(s << 23));
     };
     auto mmas = [&](auto gc, const Ops& o, uint4 v) {
@@ -520,10 +520,18 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmWork& w, uint8_
 
     if constexpr (W4) {
         // Scales that the 16-bit type cannot hold (they never come from weights
-        // of ordinary magnitude): this wave's products once more, a block at a
-        // time from memory, unscaled, each sum scaled in fp32.  Kept out of the
-        // main loop, where a second path would double the accumulators.
-        if (__any(odd)) {
+        // of ordinary magnitude, but for blocks of zeros, which do not count):
+        // this wave's products once more, a block at a time from memory,
+        // unscaled, each sum scaled in fp32.  Kept out of the main loop, where a
+        // second path would double the accumulators.
+        auto matters = [&]() {
+            const int64_t row = w.q0 + fq0 * 16, rows = a.Q - row < L::FQ * 16 ? a.Q - row : L::FQ * 16;
+            return rows > 0 && mx4_not_exact<DT>(a.q + e * a.strideq + row * a.ldq, a.ldq,
+                                                 a.qs + e * a.strideqs + row * a.ldqs, a.ldqs, (uint32_t)rows,
+                                                 (uint32_t)w.st0, w.nst, w.nst,
+                                                 (uint32_t)(w.st0 + w.nst < nb ? w.st0 + w.nst : nb), lane, 64);
+        };
+        if (__any(odd) && __any(matters())) {
 #pragma unroll
             for (int x = 0; x < L::FQ; ++x)
 #pragma unroll
