@@ -666,6 +666,18 @@ int ssg_grouped_mm_dw(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, 
                       const void* X, int64_t ldx, const int32_t* offs, void* dW, int64_t lddw,
                       int64_t stridedw, void* ws, size_t ws_bytes, void* stream);
 
+/* The kernel that a product of these sizes takes with contiguous operands that
+ * begin at 16 bytes (as ssg_spmm_select_algo for the sparse products; E counts
+ * for the grouped calls only).  kernel[0]: 0 for the few-row kernel, 1 for the
+ * tiled ones; kernel[1], kernel[2]: columns and rows of the output that a
+ * workgroup owns; kernel[3]: parts that the contraction is split into.
+ */
+typedef enum {
+    SSG_OP_MM_MX4 = 0, SSG_OP_GROUPED_MM_MX4 = 1, SSG_OP_GROUPED_MM = 2, SSG_OP_GROUPED_MM_DX = 3,
+    SSG_OP_GROUPED_MM_DW = 4
+} ssg_mm_op;
+int ssg_mm_select_kernel(int op, int x, int64_t E, int64_t M, int64_t N, int64_t K, int64_t kernel[4]);
+
 #ifdef __cplusplus
 }
 #endif

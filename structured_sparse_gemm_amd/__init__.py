@@ -47,8 +47,8 @@ __all__ = [
     "ssg_mx4_quantize", "ssg_mx4_dequantize", "ssg_mm_mx4", "ssg_grouped_mm_mx4", "ssg_grouped_mm",
     "ssg_grouped_mm_dx", "ssg_grouped_mm_dw", "ssg_mx4_elem_cols", "ssg_mx4_scale_cols",
     "ssg_mm_mx4_workspace_bytes", "ssg_grouped_mm_mx4_workspace_bytes", "ssg_grouped_mm_workspace_bytes",
-    "ssg_grouped_mm_dx_workspace_bytes", "ssg_grouped_mm_dw_workspace_bytes", "mx4_quantize", "mx4_dequantize",
-    "mm_mx4", "grouped_mm_mx4", "grouped_mm", "grouped_mm_dx", "grouped_mm_dw",
+    "ssg_grouped_mm_dx_workspace_bytes", "ssg_grouped_mm_dw_workspace_bytes", "ssg_mm_select_kernel",
+    "mx4_quantize", "mx4_dequantize", "mm_mx4", "grouped_mm_mx4", "grouped_mm", "grouped_mm_dx", "grouped_mm_dw",
     "SSG_ALGO_AUTO", "SSG_ALGO_GENERIC", "SSG_ALGO_SMALL_N", "SSG_ALGO_LARGE_N", "library_path",
 ]
 
@@ -1035,6 +1035,19 @@ def ssg_grouped_mm_dw(dY, X, offs, dW, ws=None, stream=None) -> None:
     _same_device(dY, dW)
     _need(dW.shape == (offs.shape[0] - 1, dY.shape[1], X.shape[1]), "shapes of dY, X, dW", dY, X, dW)
     _run_with_workspace("ssg_grouped_mm_dw", ops, dW, _stack(dW, "dW"), ws, stream)
+
+
+_MM_OPS = {"mm_mx4": 0, "grouped_mm_mx4": 1, "grouped_mm": 2, "grouped_mm_dx": 3, "grouped_mm_dw": 4}
+
+
+def ssg_mm_select_kernel(op: str, x: torch.dtype, M: int, N: int, K: int, E: int = 1) -> Tuple[str, int, int, int]:
+    """("few" or "tiles", columns and rows of the output a workgroup owns, parts of
+    the contraction) of the kernel that the product `op` takes for activations
+    of type x (torch.uint8: mx4) and contiguous operands."""
+    dt = _abi.SSG_MX4 if x == torch.uint8 else _FLOAT.get(x, -1)
+    k = (ctypes.c_int64 * 4)()
+    _check(_lib().ssg_mm_select_kernel(_MM_OPS[op], dt, E, M, N, K, k), "ssg_mm_select_kernel")
+    return ("tiles" if k[0] else "few",) + tuple(k[1:])
 
 
 class _Unbuilt:

@@ -104,6 +104,7 @@ SIGNATURES = {
     "ssg_grouped_mm_dw_workspace_bytes": (_sz, [_i, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp]),
     "ssg_grouped_mm_dw": (_i, [_i, _i, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _sz,
           _vp]),
+    "ssg_mm_select_kernel": (_i, [_i, _i, _i64, _i64, _i64, _i64, ctypes.POINTER(_i64)]),
 }
 
 _lock = threading.Lock()

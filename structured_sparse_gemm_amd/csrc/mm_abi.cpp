@@ -529,4 +529,35 @@ int ssg_grouped_mm_dw(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, 
     return run(a, ws, ws_bytes, (hipStream_t)stream);
 }
 
+int ssg_mm_select_kernel(int op, int x, int64_t E, int64_t M, int64_t N, int64_t K, int64_t kernel[4]) {
+    if (!kernel) return fail(SSG_ERR_NULL, "kernel is NULL");
+    // an address at a 16-byte border stands for every operand; nothing reads it
+    void* const p = reinterpret_cast<void*>((uintptr_t)256);
+    const uint8_t* const b = (const uint8_t*)p;
+    const int32_t* const offs = (const int32_t*)p;
+    const int64_t nb = blocks(K);
+    MmArgs a{};
+    int rc;
+    switch (op) {
+        case SSG_OP_MM_MX4:
+        case SSG_OP_GROUPED_MM_MX4: {
+            const bool mx = x == SSG_MX4, grouped = op == SSG_OP_GROUPED_MM_MX4;
+            rc = mx4_args(x, grouped ? E : 1, M, N, K, p, mx ? nb * 16 : K, mx ? b : nullptr, mx ? nb : 0, b, nb * 16,
+                          M * nb * 16, b, nb, M * nb, offs, grouped, &a);
+            break;
+        }
+        case SSG_OP_GROUPED_MM: rc = grouped_args(FORWARD, x, E, M, N, K, p, K, p, K, M * K, offs, &a); break;
+        case SSG_OP_GROUPED_MM_DX: rc = grouped_args(DX, x, E, M, N, K, p, M, p, K, M * K, offs, &a); break;
+        case SSG_OP_GROUPED_MM_DW: rc = grouped_args(DW, x, E, M, N, K, p, M, p, K, 0, offs, &a); break;
+        default: return fail(SSG_ERR_ALGO, "unknown operator %d", op);
+    }
+    if (rc) return rc;
+    const Plan q = plan(a);
+    kernel[0] = q.skinny ? 0 : 1;
+    kernel[1] = q.skinny ? 16 * q.rt : ssg::kMmTileSizes[q.size].q;
+    kernel[2] = q.skinny ? 16 * q.nt : ssg::kMmTileSizes[q.size].p;
+    kernel[3] = q.splits;
+    return SSG_OK;
+}
+
 }  // extern "C"
