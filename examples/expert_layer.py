@@ -18,7 +18,8 @@ import structured_sparse_gemm_amd as ssg
 
 class GroupedLinear(torch.autograd.Function):
     """grouped_mm with its gradients; weight gradients come in fp32 and are
-    rounded to the weights' type."""
+    rounded to the weights' type.  The gradients have no gradients of their own:
+    asking for them is an error."""
 
     @staticmethod
     def forward(ctx, x, w, offs):
@@ -26,6 +27,7 @@ class GroupedLinear(torch.autograd.Function):
         return ssg.grouped_mm(x, w, offs)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, w, offs = ctx.saved_tensors
         dy = dy.contiguous()
