@@ -615,8 +615,12 @@ int ssg_mx4_dequantize(int dtype, int64_t R, int64_t K, const uint8_t* elems, in
  * product needs (0 for few rows and most 16-bit operands): partial sums where
  * the contraction is split, the scales of two mx4 operands rearranged, and
  * copies of operands whose rows do not begin at 16 bytes (mx4) or at 4 (16-bit;
- * also those contracted along an odd length).  ws may be NULL where it is 0.
+ * also those contracted along an odd length).  ws may be NULL where it is 0.  A
+ * call with ws NULL and ws_bytes SSG_WS_ASK runs if it needs no workspace; if it
+ * needs one, it returns SSG_ERR_WORKSPACE as an answer, not as a failure that
+ * ssg_last_error() would tell.
  */
+#define SSG_WS_ASK ((size_t)-1)
 size_t ssg_mm_mx4_workspace_bytes(int x, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
                                   const uint8_t* xscales, int64_t ldxs, const uint8_t* W, int64_t ldw,
                                   const uint8_t* scales, int64_t lds);

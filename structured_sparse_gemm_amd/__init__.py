@@ -881,7 +881,7 @@ def _run_with_workspace(name: str, operands, y: torch.Tensor, out, ws, stream) -
     if ws is not None:
         _check(fn(operands[0], ydt, *operands[1:], *out, _on_device(ws, "ws"), ws.numel() * ws.element_size(), s), name)
         return
-    rc = fn(operands[0], ydt, *operands[1:], *out, None, 0, s)
+    rc = fn(operands[0], ydt, *operands[1:], *out, None, _abi.SSG_WS_ASK, s)
     if rc == _abi.SSG_ERR_WORKSPACE:
         need = int(getattr(_lib(), name + "_workspace_bytes")(*operands))
         ws = _empty(need, torch.uint8, y, stream)

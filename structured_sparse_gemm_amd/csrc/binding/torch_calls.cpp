@@ -90,7 +90,7 @@ PyObject* none() { Py_RETURN_NONE; }
 // `call` with a workspace (pointer, bytes): none first, then of the size that `need` gives.
 template <typename Call, typename Need>
 int with_workspace(const at::Tensor& like, Call&& call, Need&& need) {
-    int rc = call(nullptr, (size_t)0);
+    int rc = call(nullptr, SSG_WS_ASK);
     if (rc == SSG_ERR_WORKSPACE) {
         const size_t n = need();
         const at::Tensor ws = at::empty({(int64_t)n}, like.options().dtype(at::kByte));

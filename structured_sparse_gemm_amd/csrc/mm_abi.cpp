@@ -240,6 +240,7 @@ int run(MmArgs a, void* ws, size_t ws_bytes, hipStream_t s) {
     if (a.P == 0 || a.Q == 0 || (a.pt && a.E == 0)) return SSG_OK;
     const Plan p = plan(a);
     if (p.bytes > 0) {
+        if (!ws && ws_bytes == SSG_WS_ASK) return SSG_ERR_WORKSPACE;
         if (!ws || ws_bytes < p.bytes)
             return fail(SSG_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws ? ws_bytes : (size_t)0, p.bytes);
         if (!al(ws, 16)) return fail(SSG_ERR_WORKSPACE, "workspace must be 16-byte aligned");

@@ -133,7 +133,7 @@ def test_rows_of_sparse_operands_that_repeat_or_overlap_are_refused(bad, host_te
     A, B, C = torch.ones(8, 64, dtype=torch.float16), torch.ones(64, 4, dtype=torch.float16), torch.empty(8, 4)
     v, m = torch.ones(8, 32, dtype=torch.float16), torch.full((8, 8), 0x44, dtype=torch.uint8)
     calls = [(ssg.ssg_prune_2to4, 0, A, A.clone()), (ssg.ssg_prune_2to4, 1, A, A.clone()),
-             (ssg.ssg_compress_2to4, 0, A, v, m), (ssg.ssg_compress_2to4, 1, A, v, m), (ssg.ssg_compress_2to4, 2, A, v, m),
+             *((ssg.ssg_compress_2to4, at, A, v, m) for at in range(3)),
              (ssg.ssg_decompress_2to4, 2, v, m, A), (ssg.ssg_compress_2to4_prefill, 0, A, v, m),
              (ssg.ssg_spmm_2to4_packed, 3, v, m, 8, B, C), (ssg.ssg_spmm_2to4_packed, 4, v, m, 8, B, C),
              (ssg.ssg_spmm_2to4_packed_bt, 3, v, m, 8, A, C), (ssg.ssg_spmm_2to4_prefill, 3, v, m, 8, B, C),
@@ -179,7 +179,8 @@ def test_weight_gradients_in_any_layout_that_keeps_them_apart():
     for dW in (between, apart):
         ssg.ssg_grouped_mm_dw(dY.cuda(), X.cuda(), offs.cuda(), dW)
         D.check(dW, *ref, 40, "dW")
-    for dW in (torch.empty(1, 12, 24).cuda().expand(3, 12, 24), torch.empty(500).cuda().as_strided((3, 12, 24), (24, 24, 1))):
+    inside = torch.empty(500).cuda().as_strided((3, 12, 24), (24, 24, 1))
+    for dW in (torch.empty(1, 12, 24).cuda().expand(3, 12, 24), inside):
         assert status(ssg.ssg_grouped_mm_dw, dY.cuda(), X.cuda(), offs.cuda(), dW) == STRIDE
 
 
@@ -224,7 +225,7 @@ def test_no_experts(N, K):
         assert Y.shape == (N, out) and (Y == 0).all()
     nb = (K + 31) // 32
     W, s = torch.empty(0, 66, 16 * nb, dtype=torch.uint8).cuda(), torch.empty(0, 66, nb, dtype=torch.uint8).cuda()
-    Xe, Xs = torch.full((N, 16 * nb), 0x22, dtype=torch.uint8).cuda(), torch.full((N, nb), 127, dtype=torch.uint8).cuda()
+    Xe, Xs = (torch.full((N, c), v, dtype=torch.uint8).cuda() for c, v in ((16 * nb, 0x22), (nb, 127)))
     for Y in (ssg.grouped_mm_mx4(torch.ones(N, K, dtype=torch.bfloat16).cuda(), W, s, offs),
               ssg.grouped_mm_mx4(Xe, W, s, offs, xscales=Xs)):
         assert Y.shape == (N, 66) and (Y == 0).all()
@@ -316,3 +317,32 @@ def test_contractions_of_no_elements(N):
     assert Y.shape == (N, 70) and (Y == 0).all()
     dX = ssg.grouped_mm_dx(h, empty(2, 0, 70, dtype=torch.float16), offs)
     assert dX.shape == (N, 70) and (dX == 0).all()
+
+
+def failed(lib):
+    """A failure for ssg_last_error() to tell."""
+    at = ctypes.c_void_p(0x1000)                               # never dereferenced
+    assert lib.ssg_mx4_quantize(3, 4, 64, at, 63, at, 32, at, 2, None) == STRIDE
+    return lib.ssg_last_error()
+
+
+def test_asking_for_a_workspace_records_no_error():
+    lib, at = _abi.load(), ctypes.c_void_p(0x1000)
+    product = (0, 3, 2, 70, 600, 333, at, 333, at, 333, 70 * 333, at, at, 70)      # odd rows: copied to a workspace
+    before = failed(lib)
+    assert lib.ssg_grouped_mm(*product, None, _abi.SSG_WS_ASK, None) == WORKSPACE
+    assert lib.ssg_last_error() == before
+    assert lib.ssg_grouped_mm(*product, None, 0, None) == WORKSPACE
+    assert b"workspace" in lib.ssg_last_error()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("stream", [False, True])
+def test_a_call_that_succeeds_records_no_error(stream):
+    lib = _abi.load()
+    before = failed(lib)
+    X, W = torch.ones(600, 333, dtype=torch.float16).cuda(), torch.ones(2, 70, 333, dtype=torch.float16).cuda()
+    offs = torch.tensor([0, 100, 600], dtype=torch.int32).cuda()
+    assert ssg.ssg_grouped_mm_workspace_bytes(X, W, offs) > 0
+    Y = ssg.grouped_mm(X, W, offs, stream=torch.cuda.current_stream() if stream else None)
+    assert (Y == 333).all() and lib.ssg_last_error() == before
