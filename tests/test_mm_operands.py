@@ -2,6 +2,8 @@
 their strides and extents.  Refusals come before anything is enqueued."""
 import contextlib
 import ctypes
+import sys
+import warnings
 
 import pytest
 import torch
@@ -346,3 +348,16 @@ def test_a_call_that_succeeds_records_no_error(stream):
     assert ssg.ssg_grouped_mm_workspace_bytes(X, W, offs) > 0
     Y = ssg.grouped_mm(X, W, offs, stream=torch.cuda.current_stream() if stream else None)
     assert (Y == 333).all() and lib.ssg_last_error() == before
+
+
+def test_missing_compiled_marshalling_is_told(monkeypatch):
+    monkeypatch.delattr(ssg, "_torch_calls", raising=False)
+    monkeypatch.setitem(sys.modules, ssg.__name__ + "._torch_calls", None)     # its import fails
+    monkeypatch.setattr(ssg, "_calls", None)
+    with pytest.warns(RuntimeWarning, match="compiled marshalling"):
+        assert _abi.torch_calls() is None
+    with pytest.warns(RuntimeWarning):
+        first = ssg._compiled()
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")                                         # once only
+        assert ssg._compiled() is first and first.mx4_quantize(None) is None
