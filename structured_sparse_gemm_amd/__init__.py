@@ -201,6 +201,15 @@ def _torch_stream(t: torch.Tensor, stream):
     return torch.cuda.ExternalStream(int(stream), device=t.device)
 
 
+def _workspace_size(ws: torch.Tensor, device) -> int:
+    """Bytes of a caller's workspace; the kernels write them one after the other."""
+    if not ws.is_contiguous():
+        raise SsgError(_abi.SSG_ERR_STRIDE, "ws must be contiguous")
+    if ws.device != torch.device(device):
+        raise SsgError(_abi.SSG_ERR_NULL, "ws is on %s, the operands on %s" % (ws.device, device))
+    return ws.numel() * ws.element_size()
+
+
 def _workspace(dt_t: torch.dtype, M, N, K, device, ws, stream=None):
     """The caller's workspace, or a new one allocated on the stream the
     kernels run on, so the caching allocator does not hand its memory to
@@ -210,7 +219,7 @@ def _workspace(dt_t: torch.dtype, M, N, K, device, ws, stream=None):
         probe = torch.empty(0, device=device)
         with torch.cuda.stream(_torch_stream(probe, stream)):
             ws = torch.empty(need, dtype=torch.uint8, device=device)
-    return ws, (ws.numel() * ws.element_size() if ws is not None else 0)
+    return ws, (_workspace_size(ws, device) if ws is not None else 0)
 
 
 def ssg_spmm_2to4(vals, meta, B, C, ws=None, algo: int = SSG_ALGO_AUTO, stream=None) -> None:
@@ -879,7 +888,8 @@ def _run_with_workspace(name: str, operands, y: torch.Tensor, out, ws, stream) -
     fn = getattr(_lib(), name)
     ydt, s = _float(y), _raw_stream(y, stream)
     if ws is not None:
-        _check(fn(operands[0], ydt, *operands[1:], *out, _on_device(ws, "ws"), ws.numel() * ws.element_size(), s), name)
+        size = _workspace_size(ws, y.device)
+        _check(fn(operands[0], ydt, *operands[1:], *out, _on_device(ws, "ws"), size, s), name)
         return
     rc = fn(operands[0], ydt, *operands[1:], *out, None, _abi.SSG_WS_ASK, s)
     if rc == _abi.SSG_ERR_WORKSPACE:

@@ -361,3 +361,19 @@ def test_missing_compiled_marshalling_is_told(monkeypatch):
     with warnings.catch_warnings():
         warnings.simplefilter("error")                                         # once only
         assert ssg._compiled() is first and first.mx4_quantize(None) is None
+
+
+def test_workspaces_that_are_not_one_piece_are_refused(host_tensors):
+    X, dY, W, e, s, xe, xs, offs = operands("cpu")
+    v, B, C = torch.ones(8, 32).half(), torch.ones(64, 4).half(), torch.empty(8, 4)
+    m = torch.full((8, 8), 0x44, dtype=torch.uint8)
+    calls = [lambda ws: ssg.ssg_mm_mx4(X, e[0], s[0], torch.empty(6, 8), ws=ws),
+             lambda ws: ssg.ssg_grouped_mm(X, W, offs, torch.empty(6, 8), ws=ws),
+             lambda ws: ssg.ssg_grouped_mm_dw(dY, X, offs, torch.empty(2, 8, 64), ws=ws),
+             lambda ws: ssg.ssg_spmm_2to4(v, m, B, C, ws=ws)]
+    for call in calls:
+        call(torch.empty(4096, dtype=torch.uint8))
+        # one byte that claims to be 4096, and every second one of 8192
+        assert status(call, torch.empty(1, dtype=torch.uint8).expand(4096)) == STRIDE
+        assert status(call, torch.empty(8192, dtype=torch.uint8)[::2]) == STRIDE
+        assert status(call, torch.empty(4096, dtype=torch.uint8, device="meta")) == _abi.SSG_ERR_NULL
