@@ -592,10 +592,12 @@ int ssg_lds_read_probe(const uint32_t* offsets, int64_t workgroups, int64_t iter
  *
  * ssg_mx4_quantize: each block's scale exponent is floor(log2 max|x|) - 2 (at
  * least -127), each element x / scale rounded to the nearest code (ties to
- * the even one), saturating at 6.  Infinities read back as infinities; a
- * block with a NaN reads back as NaN.  ssg_mx4_dequantize rounds to nearest
+ * the even one), saturating at 6.  A block with a NaN reads back as NaN.  The
+ * format has no infinity: one becomes 6 * 2^126, above fp32's range, and reads
+ * back as an infinity, but the products below take that number for what it is
+ * (times a weight of 0.01 it is finite).  ssg_mx4_dequantize rounds to nearest
  * even where the type is narrower than the product element * scale.  Matrices
- * of fp16, bf16 or fp32, any K, any row stride and alignment.
+ * of fp16, bf16 or fp32, K below 2^29, any row stride and alignment.
  */
 int64_t ssg_mx4_elem_cols(int64_t K);
 int64_t ssg_mx4_scale_cols(int64_t K);

@@ -1087,7 +1087,9 @@ def _rows(t: torch.Tensor, stream) -> torch.Tensor:
 
 def mx4_quantize(A: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(elements, scales) of A [R, K] or a stack [E, R, K] in the mx4 format:
-    uint8 [.., 16 * ceil(K / 32)] and uint8 [.., ceil(K / 32)]."""
+    uint8 [.., 16 * ceil(K / 32)] and uint8 [.., ceil(K / 32)].  A NaN makes its
+    block NaN; an infinity becomes 6 * 2^126, which dequantises to an infinity
+    but is multiplied as that number."""
     if stream is None:
         done = (_calls or _compiled()).mx4_quantize(A)
         if done is not None:
