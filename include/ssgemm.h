@@ -613,10 +613,16 @@ int ssg_mx4_dequantize(int dtype, int64_t R, int64_t K, const uint8_t* elems, in
  * weights' exact values.  Row strides of X: elements (bytes for SSG_MX4), of
  * W, scales and xscales: bytes.
  *
+ * Sizes from 2^29 on, and E from 2^20 on for the grouped products below, are
+ * refused with SSG_ERR_SHAPE; operands whose row stride is 2^22 bytes or more
+ * with SSG_ERR_STRIDE (the kernels address a tile with 31 bits).  Outputs may
+ * have any row stride.
+ *
  * The *_workspace_bytes call with the same operands gives the workspace a
- * product needs (0 for few rows and most 16-bit operands): partial sums where
- * the contraction is split, the scales of two mx4 operands rearranged, and
- * copies of operands whose rows do not begin at 16 bytes (mx4) or at 4 (16-bit;
+ * product needs (0 for most 16-bit operands, and for few rows unless they are
+ * so long that several workgroups share them): partial sums where the
+ * contraction is split, the scales of two mx4 operands rearranged, and copies
+ * of operands whose rows do not begin at 16 bytes (mx4) or at 4 (16-bit;
  * also those contracted along an odd length).  ws may be NULL where it is 0.  A
  * call with ws NULL and ws_bytes SSG_WS_ASK runs if it needs no workspace; if it
  * needs one, it returns SSG_ERR_WORKSPACE as an answer, not as a failure that

@@ -377,3 +377,24 @@ def test_workspaces_that_are_not_one_piece_are_refused(host_tensors):
         assert status(call, torch.empty(1, dtype=torch.uint8).expand(4096)) == STRIDE
         assert status(call, torch.empty(8192, dtype=torch.uint8)[::2]) == STRIDE
         assert status(call, torch.empty(4096, dtype=torch.uint8, device="meta")) == _abi.SSG_ERR_NULL
+
+
+def test_limits():
+    # the largest operands that the header allows, and the smallest that it does not
+    lib, at, k = _abi.load(), ctypes.c_void_p(0x1000), (ctypes.c_int64 * 4)()
+
+    def choice(op, E=1, M=64, N=64, K=64):
+        return lib.ssg_mm_select_kernel(op, 0, E, M, N, K, k)
+
+    for op in range(5):
+        for size in ("M", "N", "K"):
+            assert choice(op, **{size: 2 ** 29}) == SHAPE
+        assert choice(op, N=2 ** 29 - 1) == 0
+        if op > 0:
+            assert choice(op, E=2 ** 20 - 1) == 0 and choice(op, E=2 ** 20) == SHAPE
+    assert choice(0, K=2 ** 21 - 1) == 0 and choice(0, K=2 ** 21) == STRIDE
+    assert choice(3, M=2 ** 21) == STRIDE and choice(4, K=2 ** 21) == STRIDE and choice(2, M=2 ** 21) == 0
+    # (no rows: nothing is enqueued)
+    for ld, rc in ((2 ** 21 - 1, 0), (2 ** 21, STRIDE)):
+        assert lib.ssg_mm_mx4(0, 3, 8, 0, 64, at, ld, None, 0, at, 32, at, 2, at, 8, None, 0, None) == rc
+    assert lib.ssg_mm_mx4(0, 3, 8, 0, 64, at, 64, None, 0, at, 32, at, 2, at, 2 ** 40, None, 0, None) == 0
