@@ -35,10 +35,10 @@
 //   elements) every fourth stage and stay 4-bit in LDS; a wave widens its
 //   fragment (4 conversions) on the way into the MFMA.
 //
-// Measured: 16-bit 4096^3 114 us, 1.2 PFLOP/s (the vendor's product 97 us), its
-// input gradient 122 to 127 us, weight gradient 119 to 127; mx4 x mx4 45 us, 3.05
-// PFLOP/s; mx4 x 16-bit 109 us.  8192^3: 1.34 to 1.39 PFLOP/s (vendor: 1.3 to 1.6 on
-// the same cards), mx4 x mx4 4.3.  The matrix units are busy 39 to 49% of the
+// Measured, by card: 16-bit 4096^3 108 to 114 us, 1.2 to 1.27 PFLOP/s (the vendor's
+// product 94 to 97 us), its input gradient 109 to 127 us, weight gradient 111 to
+// 127; mx4 x mx4 44 us, 3.1 PFLOP/s; mx4 x 16-bit 104 to 109 us.  8192^3: 1.29 to
+// 1.39 PFLOP/s (vendor: 1.3 to 1.6 on the same cards), mx4 x mx4 4.2 to 4.3.  The matrix units are busy 39 to 49% of the
 // cycles of the cases of a layer's size.
 //
 // Workgroups are dealt round-robin to the 8 XCDs; tile numbers are dealt so
@@ -650,7 +650,8 @@ __device__ __forceinline__ void mm_walk(uint32_t id, uint32_t np, uint32_t nq, u
 
 // The expert with the n-th most rows (ties by number).  A tile of the weight
 // gradient takes as long as its expert has rows, so the large ones go first:
-// begun last, one alone would keep the launch going.
+// begun last, one alone would keep the launch going.  (Up to 64 experts, a lane
+// each; more go in their own order.)
 __device__ __forceinline__ uint32_t mm_by_size(const MmArgs& a, uint32_t n) {
     if (!a.offs || a.E > 64) return n;
     const int lane = threadIdx.x & 63;
