@@ -203,8 +203,8 @@ def _torch_stream(t: torch.Tensor, stream):
 
 def _workspace_size(ws: torch.Tensor, device) -> int:
     """Bytes of a caller's workspace; the kernels write them one after the other."""
-    if not ws.is_contiguous():
-        raise SsgError(_abi.SSG_ERR_STRIDE, "ws must be contiguous")
+    if ws.numel() and sum((n - 1) * d for n, d in zip(ws.shape, ws.stride())) + 1 != ws.numel():
+        raise SsgError(_abi.SSG_ERR_STRIDE, "ws must be one piece of memory")
     if ws.device != torch.device(device):
         raise SsgError(_abi.SSG_ERR_NULL, "ws is on %s, the operands on %s" % (ws.device, device))
     return ws.numel() * ws.element_size()

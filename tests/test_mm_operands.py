@@ -372,7 +372,8 @@ def test_workspaces_that_are_not_one_piece_are_refused(host_tensors):
              lambda ws: ssg.ssg_grouped_mm_dw(dY, X, offs, torch.empty(2, 8, 64), ws=ws),
              lambda ws: ssg.ssg_spmm_2to4(v, m, B, C, ws=ws)]
     for call in calls:
-        call(torch.empty(4096, dtype=torch.uint8))
+        for ws in (torch.empty(4096, dtype=torch.uint8), torch.empty(32, 128).t(), torch.empty(0), torch.empty(3, 0)):
+            call(ws)
         # one byte that claims to be 4096, and every second one of 8192
         assert status(call, torch.empty(1, dtype=torch.uint8).expand(4096)) == STRIDE
         assert status(call, torch.empty(8192, dtype=torch.uint8)[::2]) == STRIDE
