@@ -121,10 +121,19 @@ def _ld(t: torch.Tensor, name: str) -> int:
     return _row_stride(*t.shape, *t.stride(), name)
 
 
+def _handle(t: torch.Tensor, raw: int) -> Optional[int]:
+    """The stream handle `raw`.  The null stream is that of the current device,
+    which tensors of another one must not meet."""
+    if raw == 0 and t.device.index != torch.cuda.current_device():
+        raise SsgError(_abi.SSG_ERR_NULL, "operands on %s, but the current device is cuda:%d (see torch.cuda.device)"
+                       % (t.device, torch.cuda.current_device()))
+    return raw or None
+
+
 def _stream(t: torch.Tensor, stream) -> Optional[int]:
     if stream is None:
         stream = torch.cuda.current_stream(t.device)
-    return getattr(stream, "cuda_stream", stream) or None
+    return _handle(t, getattr(stream, "cuda_stream", stream))
 
 
 def vals_cols(K: int) -> int:
@@ -864,7 +873,7 @@ def _raw_stream(t: torch.Tensor, stream) -> Optional[int]:
     """_stream without building a stream object: these calls may take less
     time on the GPU than that."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.device.index) or None
+        return _handle(t, torch._C._cuda_getCurrentRawStream(t.device.index))
     return _stream(t, stream)
 
 

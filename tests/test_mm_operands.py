@@ -399,3 +399,26 @@ def test_limits():
     for ld, rc in ((2 ** 21 - 1, 0), (2 ** 21, STRIDE)):
         assert lib.ssg_mm_mx4(0, 3, 8, 0, 64, at, ld, None, 0, at, 32, at, 2, at, 8, None, 0, None) == rc
     assert lib.ssg_mm_mx4(0, 3, 8, 0, 64, at, 64, None, 0, at, 32, at, 2, at, 2 ** 40, None, 0, None) == 0
+
+
+def test_operands_off_the_current_device_do_not_meet_its_null_stream(monkeypatch):
+    class Tensor:
+        device = torch.device("cuda:1")
+
+    class Stream:
+        def __init__(self, raw):
+            self.cuda_stream = raw
+
+    current = {"raw": 0, "device": 0}
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: current["raw"], raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: Stream(current["raw"]))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current["device"])
+    for handle in (ssg._stream, ssg._raw_stream):
+        current.update(raw=0, device=0)
+        assert status(handle, Tensor, None) == _abi.SSG_ERR_NULL
+        assert status(handle, Tensor, Stream(0)) == _abi.SSG_ERR_NULL
+        assert handle(Tensor, Stream(5)) == 5                # a stream knows its device
+        current.update(raw=7)
+        assert handle(Tensor, None) == 7
+        current.update(raw=0, device=1)
+        assert handle(Tensor, None) is None
