@@ -38,8 +38,8 @@
 // Measured, by card: 16-bit 4096^3 108 to 114 us, 1.2 to 1.27 PFLOP/s (the vendor's
 // product 94 to 97 us), its input gradient 109 to 127 us, weight gradient 111 to
 // 127; mx4 x mx4 44 us, 3.1 PFLOP/s; mx4 x 16-bit 104 to 109 us.  8192^3: 1.29 to
-// 1.39 PFLOP/s (vendor: 1.3 to 1.6 on the same cards), mx4 x mx4 4.2 to 4.3.  The matrix units are busy 39 to 49% of the
-// cycles of the cases of a layer's size.
+// 1.39 PFLOP/s (vendor: 1.3 to 1.6 on the same cards), mx4 x mx4 4.2 to 4.3.  The
+// matrix units are busy 39 to 49% of the cycles of the cases of a layer's size.
 //
 // Workgroups are dealt round-robin to the 8 XCDs; tile numbers are dealt so
 // that each XCD gets a contiguous range, walked 8 row tiles at a time, which

@@ -422,3 +422,40 @@ def test_operands_off_the_current_device_do_not_meet_its_null_stream(monkeypatch
         assert handle(Tensor, None) == 7
         current.update(raw=0, device=1)
         assert handle(Tensor, None) is None
+
+
+# clamped to the rows that there are: [0, 3, 3, N], [N, N, N, N], [0, 0, 0, 0]; and
+# offsets that descend, whose results are anything inside the outputs
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,K", [(20, 96), (400, 96), (400, 97)])
+@pytest.mark.parametrize("offs", [[-5, 3, 3, 1 << 30], [2000, 2000, 3000, 4000], [-9, -8, -7, -6], [17, 3, 400, 2]])
+def test_offsets_out_of_range_are_clamped(N, K, offs):
+    M, E = 70, 3
+    gen = torch.Generator().manual_seed(N + K)
+    X, W, dY = (torch.randn(*n, generator=gen).half() for n in ((N, K), (E, M, K), (N, M)))
+    clamped = torch.tensor(offs, dtype=torch.int32).clamp(0, N)
+    og = torch.tensor(offs, dtype=torch.int32).cuda()
+    e, s = D.random_mx4((E, M, K), 3)
+    We, Ws = torch.from_numpy(e).cuda(), torch.from_numpy(s).cuda()
+    Xe, Xs = ssg.mx4_quantize(X.cuda())
+    x, w, d = (t.double().numpy() for t in (X, W, dY))
+    outs = {name: torch.full((rows + 2, cols + 2), 7.0).cuda() for name, rows, cols in
+            (("Y", N, M), ("dX", N, K), ("dW", E * M, K), ("w4", N, M), ("mx", N, M))}
+    inner = {name: t[1:-1, 1:-1] for name, t in outs.items()}
+    dW = inner["dW"].unflatten(0, (E, M))
+    ssg.ssg_grouped_mm(X.cuda(), W.cuda(), og, inner["Y"])
+    ssg.ssg_grouped_mm_dx(dY.cuda(), W.cuda(), og, inner["dX"])
+    ssg.ssg_grouped_mm_dw(dY.cuda(), X.cuda(), og, dW)
+    ssg.ssg_grouped_mm_mx4(X.cuda(), We, Ws, og, inner["w4"])
+    ssg.ssg_grouped_mm_mx4(Xe, We, Ws, og, inner["mx"], xscales=Xs)
+    for t in outs.values():
+        assert (t[0] == 7).all() and (t[-1] == 7).all() and (t[:, 0] == 7).all() and (t[:, -1] == 7).all()
+    if sorted(offs) != offs:
+        return
+    w4 = D.mx4_values(e, s, K)
+    x4 = D.mx4_values(Xe.cpu().numpy(), Xs.cpu().numpy(), K)
+    D.check(inner["Y"], *D.grouped(x, w, clamped), K, "Y")
+    D.check(inner["dX"], *D.grouped_dx(d, w, clamped), M, "dX")
+    D.check(dW, *D.grouped_dw(d, x, clamped), N, "dW")
+    D.check(inner["w4"], *D.grouped(x, w4, clamped), K, "mx4 weights")
+    D.check(inner["mx"], *D.grouped(x4, w4, clamped), K, "mx4 x mx4")
