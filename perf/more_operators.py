@@ -330,7 +330,7 @@ def _run_own(s):
         return out
     if op == "dispatch":
         offs, rows, pos = ssg.expert_order(s["experts"], s["E"])
-        return {"offs": offs, "rows": rows, "pos": pos, "X": ssg.expert_gather(s["X"], rows, s["k"])}
+        return {"offs": offs, "rows": rows, "pos": pos, "X": ssg.expert_gather(s["X"], pos, rows)}
     if op == "combine":
         out = {"O": ssg.expert_combine(s["Y"], s["pos"], s["w"])}
         if s["grad"]:
