@@ -690,6 +690,72 @@ typedef enum {
 } ssg_mm_op;
 int ssg_mm_select_kernel(int op, int x, int64_t E, int64_t M, int64_t N, int64_t K, int64_t kernel[4]);
 
+/* ---------------------------------------------------------------------------
+ * Around the expert-grouped products: routing, the order of the rows, the copies
+ * into it and the sums out of it.  Matrices are fp16, bf16 or fp32 with any row
+ * stride (in elements) and alignment; at most 1024 experts, 64 choices a token
+ * and 2^31 - 1 pairs of a token and a choice (SSG_ERR_SHAPE).
+ *
+ * ssg_route: each of N tokens chooses k of E experts by its logits [N, E].
+ * The scores s are the softmax or the sigmoids of a token's logits.  The choice
+ * is made by c = s + bias (bias [E] fp32 or NULL: then by the logits
+ * themselves); the experts are `groups` groups of E / groups neighbours, of
+ * which the top_groups with the largest score stay (SSG_GROUP_MAX: a group's
+ * largest c; SSG_GROUP_TOP2: the sum of its two largest c, without a bias of
+ * its two largest s); of those the k experts with the largest c are chosen, in
+ * descending order, ties to the lower number (groups too).  c and sums of c are
+ * formed and compared in 64 bits.
+ *   weights [N, k] = scale * s of the chosen; with renorm != 0 scale * s / (the
+ *   sum of s over the chosen), a number also where all s underflow
+ *   experts [N, k]
+ * An expert whose logit or bias is -inf is never chosen; a slot for which none
+ * is left gets expert -1 and weight 0 (all slots of a token whose logits are all
+ * -inf: padding).  NaN ranks before everything and makes weights NaN, as the
+ * formulas do, and so does a softmax over a logit of +inf.
+ * ssg_route_backward: the gradient of the logits from that of the weights, for
+ * the experts that were chosen (the bias and the choice have none).  Experts out
+ * of range, or whose logit is -inf, count for nothing; one that a token names
+ * twice counts twice in its gradient's sum.
+ */
+typedef enum { SSG_SCORE_SOFTMAX = 0, SSG_SCORE_SIGMOID = 1 } ssg_score;
+typedef enum { SSG_GROUP_MAX = 0, SSG_GROUP_TOP2 = 1 } ssg_group_score;
+int ssg_route(int dt, int64_t N, int64_t E, const void* logits, int64_t ldl, const float* bias, int score,
+              int64_t k, int64_t groups, int64_t top_groups, int group_score, int renorm, float scale,
+              float* weights, int64_t ldw, int32_t* experts, int64_t lde, void* stream);
+int ssg_route_backward(int dt, int64_t N, int64_t E, const float* dweights, int64_t lddw, const void* logits,
+                       int64_t ldl, const int32_t* experts, int64_t lde, int score, int64_t k, int renorm,
+                       float scale, void* dlogits, int64_t ldd, void* stream);
+
+/* ssg_expert_order: pair n * k + j is choice j of token n.  The pairs sorted by
+ * expert, in their own order within one, are the rows of the grouped products:
+ *   offs [E + 1]  rows offs[e] .. offs[e + 1] - 1 are expert e's
+ *   rows [N * k]  the pair of each row, -1 from row offs[E] on
+ *   pos  [N, k]   the row of each pair, -1 for an expert outside 0 .. E - 1
+ * rows and pos are contiguous.  The workspace (0 bytes for up to 8192 pairs) holds
+ * the counts of parts of the pairs; SSG_WS_ASK as for the products.
+ * ssg_expert_gather: Y[pos[n, j]] = X[n]; rows r of Y [N * k, D] with rows[r] = -1
+ * get zeros.
+ * ssg_expert_combine: O[n] = sum_j weights[n, j] Y[pos[n, j]] over the pairs that
+ * have a row, in slot order, fp32 sums; weights NULL: ones (the gradient of the
+ * gather).  O is fp32 or Y's type.
+ * ssg_expert_combine_backward: dY[pos[n, j]] = weights[n, j] dO[n], zeros in rows
+ * of nobody; dweights[n, j] = sum_d dO[n, d] Y[pos[n, j], d], 0 for a pair without
+ * a row.  dO, Y and dY have one type.
+ * pos and rows outside 0 .. N * k - 1 count as -1; a pos and rows that are not an
+ * order of each other give wrong rows but no access out of range.
+ */
+size_t ssg_expert_order_workspace_bytes(int64_t N, int64_t k, int64_t E);
+int ssg_expert_order(int64_t N, int64_t k, int64_t E, const int32_t* experts, int64_t lde, int32_t* offs,
+                     int32_t* rows, int32_t* pos, void* ws, size_t ws_bytes, void* stream);
+int ssg_expert_gather(int dt, int64_t N, int64_t k, int64_t D, const void* X, int64_t ldx, const int32_t* pos,
+                      const int32_t* rows, void* Y, int64_t ldy, void* stream);
+int ssg_expert_combine(int dt, int out, int64_t N, int64_t k, int64_t D, const void* Y, int64_t ldy,
+                       const int32_t* pos, const float* weights, int64_t ldw, void* O, int64_t ldo, void* stream);
+int ssg_expert_combine_backward(int dt, int64_t N, int64_t k, int64_t D, const void* dO, int64_t lddo,
+                                const void* Y, int64_t ldy, const int32_t* pos, const int32_t* rows,
+                                const float* weights, int64_t ldw, void* dY, int64_t lddy, float* dweights,
+                                int64_t lddw, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

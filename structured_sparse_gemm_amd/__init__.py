@@ -106,7 +106,7 @@ def _row_stride(R: int, C: int, ld: int, unit: int, name: str) -> int:
     """Row stride of R rows of C columns; that of a single row, or of rows
     without columns, means nothing.  Rows that repeat or overlap (expanded or
     unfolded tensors) are refused."""
-    if unit != 1 and C > 1:
+    if unit != 1 and C > 1 and R > 0:
         raise SsgError(_abi.SSG_ERR_STRIDE, "%s must have unit column stride" % name)
     if R <= 1 or C == 0:
         return C
@@ -1194,3 +1194,9 @@ def grouped_mm_dw(dY, X, offs, out_dtype: Optional[torch.dtype] = None, stream=N
     dW = _empty((offs.shape[0] - 1, dY.shape[1], X.shape[1]), out_dtype or dY.dtype, dY, stream)
     ssg_grouped_mm_dw(dY, X, offs, dW, stream=stream)
     return dW
+
+
+from . import experts as _experts
+from .experts import *  # noqa: F401,F403
+
+__all__ += _experts.__all__

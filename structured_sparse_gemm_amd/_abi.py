@@ -106,6 +106,16 @@ SIGNATURES = {
     "ssg_grouped_mm_dw_workspace_bytes": (_sz, [_i, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp]),
     "ssg_grouped_mm_dw": (_i, [_i, _i, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _sz,
           _vp]),
+    "ssg_route": (_i, [_i, _i64, _i64, _vp, _i64, _vp, _i, _i64, _i64, _i64, _i, _i, ctypes.c_float, _vp, _i64, _vp,
+          _i64, _vp]),
+    "ssg_route_backward": (_i, [_i, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i, _i64, _i, ctypes.c_float, _vp,
+          _i64, _vp]),
+    "ssg_expert_order_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "ssg_expert_order": (_i, [_i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "ssg_expert_gather": (_i, [_i, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp]),
+    "ssg_expert_combine": (_i, [_i, _i, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp]),
+    "ssg_expert_combine_backward": (_i, [_i, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64,
+          _vp, _i64, _vp]),
     "ssg_mm_select_kernel": (_i, [_i, _i, _i64, _i64, _i64, _i64, ctypes.POINTER(_i64)]),
 }
 
