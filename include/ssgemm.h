@@ -756,6 +756,62 @@ int ssg_expert_combine_backward(int dt, int64_t N, int64_t k, int64_t D, const v
                                 const float* weights, int64_t ldw, void* dY, int64_t lddy, float* dweights,
                                 int64_t lddw, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit floats (e4m3) with an fp32 scale for each block of 128 along the
+ * contraction: of one row (block = 1; activations) or of 128 rows (block = 128;
+ * weights).  A matrix [R, K] is
+ *   elems   [R, K] bytes, row stride lde
+ *   scales  [R or ceil(R / 128), ceil(K / 128)] with any strides `row` and `blk`
+ *           (in floats)
+ * and B of them may be stacked, stride* apart.  Quantising: a block's scale is
+ * max(amax / 448, 2^-126), amax the largest magnitude of its numbers, rounded to
+ * fp32; an element is the e4m3 number nearest to x / scale (the exact quotient),
+ * ties to even.  A NaN stays a NaN and does not count for amax; an infinity makes
+ * its block's scale infinite and its products NaN.  transpose != 0: elements and
+ * scales are those of the transpose, [K, R].  Matrices of fp16, bf16 or fp32, any
+ * row stride and alignment.  ssg_fp8_dequantize: element * scale in fp32, rounded to
+ * the type.
+ *
+ * ssg_mm_fp8: Y[n, m] = sum_b xs[n, b] ws[m, b] (sum over block b of X[n, k] W[m, k]),
+ * X [N, K] with a scale for each row, W [M, K] with one for each row (wblock 1) or
+ * 128 rows (wblock 128).  x is SSG_E4M3, or SSG_F16, SSG_BF16, SSG_F32 (xs NULL):
+ * X is then rounded in the call as ssg_fp8_quantize would.  Y is fp32, fp16 or bf16.
+ * Sums are fp32; into a 16-bit Y of many rows they are the 8-bit matrix
+ * instruction's, which adds eight products at a time aligned to the largest of
+ * them, 13 bits below it (1.3e-5 of the norm for normal numbers; the output's
+ * rounding is 1.7e-3 for bf16, 2e-4 for fp16).  ssg_grouped_mm_fp8: by expert, as
+ * the grouped products above; scales of W `strides` floats apart.
+ *
+ * Sizes from 2^29 on, and E from 2^20 on, are refused with SSG_ERR_SHAPE; operands
+ * whose row stride is 2^22 bytes or more, and strides of scales from 2^29 on, with
+ * SSG_ERR_STRIDE.  The workspace holds activations that are rounded in the call
+ * (not for few rows), operands whose rows do not begin at 4 bytes and scales of
+ * rows that are not neighbours (row != 1) where many rows need them rearranged;
+ * SSG_WS_ASK as above.
+ */
+int64_t ssg_fp8_scale_cols(int64_t K);
+int ssg_fp8_quantize(int dtype, int64_t B, int64_t R, int64_t K, const void* A, int64_t lda, int64_t stridea,
+                     int block, int transpose, uint8_t* elems, int64_t lde, int64_t stridee, float* scales,
+                     int64_t row, int64_t blk, int64_t strides, void* stream);
+int ssg_fp8_dequantize(int dtype, int64_t B, int64_t R, int64_t K, const uint8_t* elems, int64_t lde,
+                       int64_t stridee, int block, const float* scales, int64_t row, int64_t blk,
+                       int64_t strides, void* D, int64_t ldd, int64_t strided, void* stream);
+size_t ssg_mm_fp8_workspace_bytes(int x, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+                                  const float* xs, int64_t xsr, int64_t xsk, const uint8_t* W, int64_t ldw,
+                                  int wblock, const float* wsc, int64_t wsr, int64_t wsk);
+int ssg_mm_fp8(int x, int y, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const float* xs,
+               int64_t xsr, int64_t xsk, const uint8_t* W, int64_t ldw, int wblock, const float* wsc,
+               int64_t wsr, int64_t wsk, void* Y, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+size_t ssg_grouped_mm_fp8_workspace_bytes(int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* X,
+                                          int64_t ldx, const float* xs, int64_t xsr, int64_t xsk,
+                                          const uint8_t* W, int64_t ldw, int64_t stridew, int wblock,
+                                          const float* wsc, int64_t wsr, int64_t wsk, int64_t strides,
+                                          const int32_t* offs);
+int ssg_grouped_mm_fp8(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+                       const float* xs, int64_t xsr, int64_t xsk, const uint8_t* W, int64_t ldw,
+                       int64_t stridew, int wblock, const float* wsc, int64_t wsr, int64_t wsk, int64_t strides,
+                       const int32_t* offs, void* Y, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1196,7 +1196,8 @@ def grouped_mm_dw(dY, X, offs, out_dtype: Optional[torch.dtype] = None, stream=N
     return dW
 
 
-from . import experts as _experts
+from . import experts as _experts, fp8 as _fp8
 from .experts import *  # noqa: F401,F403
+from .fp8 import *  # noqa: F401,F403
 
-__all__ += _experts.__all__
+__all__ += _experts.__all__ + _fp8.__all__

@@ -1,0 +1,170 @@
+// fp8.hpp -- 8-bit floats (e4m3) with an fp32 scale for each block of 128: device
+// helpers, arguments and launchers (fp8_quantize.hip, mm_fp8_few.hip,
+// mm_fp8_tiles.hip).
+#pragma once
+
+#include "mm_args.hpp"
+
+namespace ssg {
+
+constexpr int kFp8Block = 128;
+enum Fp8Src { SRC8_F16 = 0, SRC8_BF16 = 1, SRC8_F32 = 2 };
+
+struct Fp8Scales {
+    const float* p;
+    int64_t row, blk, mat;             // strides in elements: of rows (or blocks of rows), of blocks, of matrices
+};
+
+// Y = X W^T: m describes the elements (q: W, p: X), their scales here.
+struct MmFp8Args {
+    MmArgs m;
+    Fp8Scales w, x;
+    bool w_rows;                       // a scale for each row of W, else for each 128 rows
+    int x_src;                         // few rows: Fp8Src of X that the kernel rounds itself, or -1
+    bool exact;                        // tiles: sums as fp32's (fp8_mfma_exact)
+};
+// Tiles of the kernels: of 8-bit products, of exact ones.
+constexpr MmTileSize kFp8TileSizes[2][2] = {{{256, 256, 1, 1.0, 0.3}, {128, 128, 2, 0.6, 0.3}},
+                                            {{256, 128, 1, 1.0, 0.3}, {128, 128, 2, 0.8, 0.3}}};
+hipError_t launch_mm_fp8_few(const MmFp8Args& a, int rt, int nt, hipStream_t s);
+hipError_t launch_mm_fp8_tiles(const MmFp8Args& a, int size, hipStream_t s);
+
+struct Fp8Matrix {
+    int type;                          // Fp8Src of the matrix
+    int64_t mats, R, K;                // of the matrix in its own type
+    const void* a;
+    int64_t lda, stridea;              // elements
+    int block;                         // rows that share a scale: 1 or 128
+    bool transpose;                    // the 8-bit form is that of the transpose, [K, R]
+    uint8_t* e;
+    int64_t lde, stridee;              // bytes
+    float* s;
+    int64_t row, blk, mat;             // strides of the scales, as in Fp8Scales
+};
+hipError_t launch_fp8_quantize(const Fp8Matrix& a, hipStream_t s);
+hipError_t launch_fp8_dequantize(const Fp8Matrix& a, hipStream_t s);
+// Scales [rows][nb] of `mats` matrices to planes [nb][plane] (zeros past the rows).
+hipError_t launch_fp8_planes(const Fp8Scales& src, int64_t mats, int64_t rows, int64_t nb, float* dst, int64_t plane,
+                             hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// Rounding.  A block with largest magnitude m has the scale
+// s = max(m / 448, 2^-126) (448 is the largest e4m3 number; the bound keeps 1 / s
+// finite and gives blocks of zeros a scale), and its elements are the e4m3 numbers
+// nearest to x / s, ties to even.
+//
+// The nearest to the exact quotient, so that every kernel (and a definition in
+// 64 bits) gives the same bytes: x times the reciprocal of s is off by up to two
+// steps of fp32, which matters where x / s lies that near to the border of two
+// codes.  So x is multiplied by a slightly smaller and a slightly larger
+// reciprocal; where the codes agree they are right, and where one does not (one
+// element in 70000) the border times s, exact in fp64, is compared with x.
+// Costs two products and a conversion an element instead of a division's ten.
+// NaN stays NaN and does not enter m; an infinity makes the scale infinite, and
+// with it every product that meets the block (0 * inf) NaN.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float fp8_scale(float top) { return fmaxf(top / 448.0f, 0x1p-126f); }
+
+struct Fp8Recip {
+    float s, lo, hi;
+};
+__device__ __forceinline__ Fp8Recip fp8_recip(float s) {
+    const float r = __builtin_amdgcn_rcpf(s);      // within a step of 2^-23
+    return {s, r * (1.0f - 0x1p-21f), r * (1.0f + 0x1p-21f)};
+}
+
+// The code of x where lo and hi (adjacent codes, or the same) bracket x / s.
+__device__ __forceinline__ uint32_t fp8_between(float x, float s, uint32_t lo, uint32_t hi) {
+    if (lo == hi) return lo;
+    const double border = 0.5 * ((double)e4m3_bits_to_f32(lo & 0x7Fu) + (double)e4m3_bits_to_f32(hi & 0x7Fu)) * (double)s;
+    const double m = fabs((double)x);
+    return m > border ? hi : m < border ? lo : (lo & 1u) ? hi : lo;
+}
+
+// Eight codes, in element order.
+__device__ __forceinline__ uint2 fp8_pack8(const float (&v)[8], const Fp8Recip& r) {
+    uint32_t lo[2], hi[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        int a = 0, b = 0;
+        a = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h] * r.lo, v[4 * h + 1] * r.lo, a, false);
+        a = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2] * r.lo, v[4 * h + 3] * r.lo, a, true);
+        b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h] * r.hi, v[4 * h + 1] * r.hi, b, false);
+        b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2] * r.hi, v[4 * h + 3] * r.hi, b, true);
+        lo[h] = (uint32_t)a;
+        hi[h] = (uint32_t)b;
+    }
+    if (((lo[0] ^ hi[0]) | (lo[1] ^ hi[1])) != 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int sh = 8 * (e & 3);
+            const uint32_t c = fp8_between(v[e], r.s, (lo[e >> 2] >> sh) & 0xFFu, (hi[e >> 2] >> sh) & 0xFFu);
+            lo[e >> 2] = (lo[e >> 2] & ~(0xFFu << sh)) | (c << sh);
+        }
+    }
+    return make_uint2(lo[0], lo[1]);
+}
+
+// 16 bytes of 16-bit elements as eight fp32 values.
+template <int SRC>
+__device__ __forceinline__ void fp8_widen8(uint4 d, float (&v)[8]) {
+    const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (SRC == SRC8_BF16) {
+            v[2 * e] = __uint_as_float(w[e] << 16);
+            v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        } else {
+            v[2 * e] = f16_bits_to_f32((uint16_t)w[e]);
+            v[2 * e + 1] = f16_bits_to_f32((uint16_t)(w[e] >> 16));
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// 16 x 16 x 128 products of e4m3 operands: lane (i = l % 16, g = l / 16) holds 32
+// elements of row i of both, the same ones for the same g; the result as in mfma16.
+//
+// * fp8_mfma: the 8-bit matrix instruction.  It adds eight neighbouring products
+//   at a time, aligned to the largest exponent among them and cut 13 bits below
+//   it (a check of the instruction: 2^16 + 2^3 is kept, 2^16 + 2^2 is not, and only
+//   within eight), then in fp32.  Products within 2^7 of the largest are exact;
+//   over blocks of normal numbers the sums are off by 1.3e-5 of their norm.  Taken
+//   where the result is rounded to 16 bits (half a step: 2^-9, 2^-12) anyway.
+// * fp8_mfma_exact: elements widened to fp16, where each is exact, and four
+//   16-bit instructions, whose sums are fp32's: half the rate.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ f32x4 fp8_mfma(uint4 a0, uint4 a1, uint4 b0, uint4 b1) {
+    const i32x8 x = {(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w, (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
+    const i32x8 y = {(int)b0.x, (int)b0.y, (int)b0.z, (int)b0.w, (int)b1.x, (int)b1.y, (int)b1.z, (int)b1.w};
+    // (scales of 0: the form without)
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+}
+
+// 32 elements as fp16, eight a 16 bytes.
+struct Fp8Wide {
+    uint4 v[4];
+};
+__device__ __forceinline__ Fp8Wide fp8_widen(uint4 lo, uint4 hi) {
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    const uint32_t d[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    Fp8Wide r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        union { f16x2 h[4]; uint4 u; } w;
+        w.h[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(d[2 * k], 1.0f, false);
+        w.h[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(d[2 * k], 1.0f, true);
+        w.h[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(d[2 * k + 1], 1.0f, false);
+        w.h[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(d[2 * k + 1], 1.0f, true);
+        r.v[k] = w.u;
+    }
+    return r;
+}
+__device__ __forceinline__ f32x4 fp8_mfma_exact(const Fp8Wide& a, const Fp8Wide& b) {
+    f32x4 d = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) d = mfma16<DT_F16>(a.v[k], b.v[k], d);
+    return d;
+}
+
+}  // namespace ssg

@@ -1,0 +1,330 @@
+// fp8_abi.cpp -- the C ABI of 8-bit floats with a scale for each block of 128:
+// host-side checks, the choice of kernel, and the workspace (activations rounded
+// in the call, operands and scales in another layout, partials of a split
+// contraction).
+#include "ssgemm.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "fp8.hpp"
+#include "ssg_abi.hpp"
+
+namespace {
+
+using ssg::abi_failf;
+using ssg::Fp8Matrix;
+using ssg::MmFp8Args;
+
+typedef long long ll;
+
+constexpr int64_t kMaxDim = (int64_t)1 << 29;
+constexpr int kCUs = 256;
+
+int hip_status(hipError_t e) {
+    return e == hipSuccess ? SSG_OK : abi_failf(SSG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
+}
+
+bool al(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+int64_t blocks(int64_t n) { return (n + ssg::kFp8Block - 1) / ssg::kFp8Block; }
+
+int source(int dt) {
+    return dt == SSG_F16 ? ssg::SRC8_F16 : dt == SSG_BF16 ? ssg::SRC8_BF16 : dt == SSG_F32 ? ssg::SRC8_F32 : -1;
+}
+int64_t float_bytes(int dt) { return dt == SSG_F32 ? 4 : 2; }
+
+// ------------------------------------------------------------------ checks
+
+int check_mat(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld) {
+    if (rows > 0 && cols > 0 && !p) return abi_failf(SSG_ERR_NULL, "%s is NULL", name);
+    if (ld < cols) return abi_failf(SSG_ERR_STRIDE, "row stride of %s: %lld < %lld", name, (ll)ld, (ll)cols);
+    return SSG_OK;
+}
+
+// Scales are read (and written) one by one where their layout asks for it; their
+// strides only have to be addressable.
+int check_scales(const char* name, const void* p, int64_t rows, int64_t nb, int64_t row, int64_t blk) {
+    if (rows > 0 && nb > 0 && !p) return abi_failf(SSG_ERR_NULL, "%s is NULL", name);
+    if (row < 0 || blk < 0 || row >= kMaxDim || blk >= kMaxDim)
+        return abi_failf(SSG_ERR_STRIDE, "strides of %s: %lld, %lld", name, (ll)row, (ll)blk);
+    return SSG_OK;
+}
+
+int check_fp8(int dtype, int64_t B, int64_t R, int64_t K, int block, const void* A, int64_t lda, bool transpose,
+              const void* e, int64_t lde, const void* s, int64_t row, int64_t blk) {
+    if (source(dtype) < 0) return abi_failf(SSG_ERR_DTYPE, "element type %d", dtype);
+    if (block != 1 && block != ssg::kFp8Block) return abi_failf(SSG_ERR_FORMAT, "%d rows to a scale (1 or 128)", block);
+    if (B < 0 || R < 0 || K < 0 || B >= (1 << 20) || R >= kMaxDim || K >= kMaxDim)
+        return abi_failf(SSG_ERR_SHAPE, "size B=%lld R=%lld K=%lld", (ll)B, (ll)R, (ll)K);
+    const int64_t er = transpose ? K : R, ec = transpose ? R : K;
+    int rc;
+    if ((rc = check_mat("the matrix", A, B * R, K, lda)) || (rc = check_mat("elems", e, B * er, ec, lde)) ||
+        (rc = check_scales("scales", s, B * er, ec, row, blk)))
+        return rc;
+    // scales of different places must not be one: either direction may be the outer one
+    const int64_t rows = block == 1 ? er : blocks(er), cols = blocks(ec);
+    if (rows > 1 && cols > 1 && row < (cols - 1) * blk + 1 && blk < (rows - 1) * row + 1)
+        return abi_failf(SSG_ERR_STRIDE, "scales overlap: strides %lld, %lld", (ll)row, (ll)blk);
+    if ((rows > 1 && row == 0) || (cols > 1 && blk == 0))
+        return abi_failf(SSG_ERR_STRIDE, "scales overlap: strides %lld, %lld", (ll)row, (ll)blk);
+    // workgroups of a launch are counted in 32 bits
+    if (B > 0 && blocks(R) > 0 && blocks(K) * ((R + 15) / 16) > 0xffffffffLL / B)
+        return abi_failf(SSG_ERR_SHAPE, "size too large: B=%lld R=%lld K=%lld", (ll)B, (ll)R, (ll)K);
+    return SSG_OK;
+}
+
+// ------------------------------------------------------------------ the products
+
+struct Call {
+    MmFp8Args a;
+    int x;                             // type of X
+    int64_t ldx;                       // bytes
+};
+
+int mm_args(int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const float* xs, int64_t xsr,
+            int64_t xsk, const uint8_t* W, int64_t ldw, int64_t stridew, int wblock, const float* wsc, int64_t wsr,
+            int64_t wsk, int64_t strides, const int32_t* offs, bool grouped, Call* out) {
+    if (x != SSG_E4M3 && source(x) < 0) return abi_failf(SSG_ERR_DTYPE, "activations of type %d", x);
+    if (wblock != 1 && wblock != ssg::kFp8Block) return abi_failf(SSG_ERR_FORMAT, "%d rows to a scale (1 or 128)", wblock);
+    if (E < 0 || M < 0 || N < 0 || K < 0)
+        return abi_failf(SSG_ERR_SHAPE, "negative size E=%lld M=%lld N=%lld K=%lld", (ll)E, (ll)M, (ll)N, (ll)K);
+    if (E >= (1 << 20) || M >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
+        return abi_failf(SSG_ERR_SHAPE, "size too large: E=%lld M=%lld N=%lld K=%lld", (ll)E, (ll)M, (ll)N, (ll)K);
+    const int64_t xb = x == SSG_E4M3 ? 1 : float_bytes(x);
+    int rc;
+    if ((rc = check_mat("X", X, N, K, ldx)) || (rc = check_mat("W", W, E * M, K, ldw))) return rc;
+    // a tile's rows are addressed with 31 bits
+    if (ldx * xb >= (int64_t)1 << 22) return abi_failf(SSG_ERR_STRIDE, "rows of X are 2^22 bytes apart or more");
+    if (ldw >= (int64_t)1 << 22) return abi_failf(SSG_ERR_STRIDE, "rows of W are 2^22 bytes apart or more");
+    if (x == SSG_E4M3) {
+        if ((rc = check_scales("xscales", xs, N, K, xsr, xsk))) return rc;
+    } else if (xs) {
+        return abi_failf(SSG_ERR_FORMAT, "xscales with activations that are not e4m3");
+    }
+    if ((rc = check_scales("wscales", wsc, E * M, K, wsr, wsk))) return rc;
+    if (grouped && !offs) return abi_failf(SSG_ERR_NULL, "offs is NULL");
+    Call c{};
+    ssg::MmArgs& m = c.a.m;
+    m.mode = ssg::MM_FP8;
+    m.Q = M; m.P = N; m.C = K;
+    m.q = W; m.ldq = ldw; m.strideq = stridew;
+    m.p = (const uint8_t*)X; m.ldp = ldx * xb;
+    m.E = E; m.offs = grouped ? offs : nullptr;
+    m.splits = 1;
+    c.a.w = {wsc, wsr, wsk, strides};
+    c.a.x = {xs, xsr, xsk, 0};
+    c.a.w_rows = wblock == 1 && M > 1;
+    c.a.x_src = -1;
+    c.x = x;
+    *out = c;
+    return SSG_OK;
+}
+
+// ------------------------------------------------------------------ the choice of kernel
+
+struct Plan {
+    bool few;
+    int rt, nt, size, splits;
+    bool round, copy_q, copy_p, planes_q, planes_p;
+    int64_t at_x, ldx, at_xs, xplane, at_q, ldq, at_p, ldp, at_ws, wplane, at_part;
+    size_t bytes;
+};
+
+Plan plan(const Call& c) {
+    const ssg::MmArgs& m = c.a.m;
+    Plan p{};
+    p.splits = 1;
+    p.nt = p.rt = 1;
+    // experts that have rows, if rows choose them at random, and their rows
+    const double E = m.offs ? std::max<double>(1, (double)m.E) : 1;
+    const double busy = m.offs ? std::max(1.0, E * (1 - std::exp(-(double)m.P / E))) : 1;
+    const double avg = (double)m.P / busy;
+    p.few = avg <= 32 && ((m.Q + 15) / 16) * ssg::mm_tile_bound(m, 16) < (int64_t)1 << 23;
+    const int64_t nb = blocks(m.C);
+    int64_t at = 0;
+    auto take = [&](int64_t n) {
+        const int64_t r = at;
+        at += up(n, 256);
+        return r;
+    };
+    p.round = c.x != SSG_E4M3 && !(p.few && c.x != SSG_F32);
+    if (p.round) {
+        p.ldx = up(m.C, 16);
+        p.xplane = up(m.P, 4);
+        p.at_x = take(m.P * p.ldx);
+        p.at_xs = take(nb * p.xplane * 4);
+    }
+    if (!p.few) {
+        // tiles load rows 16 bytes at a time from any dword
+        p.copy_q = !al(m.q, 4) || m.ldq % 4 || (m.E > 1 && m.strideq % 4);
+        p.copy_p = !p.round && (!al(m.p, 4) || m.ldp % 4);
+        p.planes_q = c.a.w_rows && c.a.w.row != 1;
+        p.planes_p = !p.round && c.a.x.row != 1 && m.P > 1;
+        if (p.copy_q) {
+            p.ldq = up(m.C, 16);
+            p.at_q = take(m.E * m.Q * p.ldq);
+        }
+        if (p.copy_p) {
+            p.ldp = up(m.C, 16);
+            p.at_p = take(m.P * p.ldp);
+        }
+        if (p.planes_q) {
+            p.wplane = up(m.Q, 4);
+            p.at_ws = take(m.E * nb * p.wplane * 4);
+        }
+        if (p.planes_p) {
+            p.xplane = up(m.P, 4);
+            p.at_xs = take(nb * p.xplane * 4);
+        }
+        const int64_t big = ((m.Q + 255) / 256) * ssg::mm_tile_bound(m, 256);   // (fp32 outputs: 256 x 128)
+        p.size = big >= kCUs / 2 ? 0 : 1;
+    }
+    if (p.splits > 1) p.at_part = take((int64_t)p.splits * m.P * m.Q * 4);
+    p.bytes = (size_t)at;
+    return p;
+}
+
+int run(Call c, void* ws, size_t ws_bytes, hipStream_t s) {
+    ssg::MmArgs& m = c.a.m;
+    if (m.P == 0 || m.Q == 0) return SSG_OK;
+    const Plan p = plan(c);
+    if (p.bytes > 0) {
+        if (!ws && ws_bytes == SSG_WS_ASK) return SSG_ERR_WORKSPACE;
+        if (!ws || ws_bytes < p.bytes)
+            return abi_failf(SSG_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws ? ws_bytes : (size_t)0, p.bytes);
+        if (!al(ws, 16)) return abi_failf(SSG_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+    }
+    uint8_t* const w = (uint8_t*)ws;
+    const int64_t nb = blocks(m.C);
+    hipError_t e = hipSuccess;
+    m.splits = p.splits;
+    if (p.splits > 1) m.part = (float*)(w + p.at_part);
+    if (p.round) {
+        if (m.C > 0) {
+            Fp8Matrix q{};
+            q.type = source(c.x);
+            q.mats = 1; q.R = m.P; q.K = m.C;
+            q.a = m.p; q.lda = m.ldp / float_bytes(c.x);
+            q.block = 1;
+            q.e = w + p.at_x; q.lde = p.ldx;
+            q.s = (float*)(w + p.at_xs); q.row = 1; q.blk = p.xplane;
+            e = ssg::launch_fp8_quantize(q, s);
+        }
+        m.p = w + p.at_x;
+        m.ldp = p.ldx;
+        c.a.x = {(const float*)(w + p.at_xs), 1, p.xplane, 0};
+    } else if (c.x != SSG_E4M3) {
+        c.a.x_src = source(c.x);
+    }
+    if (p.few) {
+        if (e == hipSuccess) e = ssg::launch_mm_fp8_few(c.a, p.rt, p.nt, s);
+    } else {
+        if (p.copy_q && e == hipSuccess) {
+            e = ssg::launch_mm_repack(m.q, m.E, m.strideq, m.Q, m.C, m.ldq, w + p.at_q, p.ldq, 0, m.offs, s);
+            m.q = w + p.at_q;
+            m.ldq = p.ldq;
+            m.strideq = m.Q * p.ldq;
+        }
+        if (p.copy_p && e == hipSuccess) {
+            e = ssg::launch_mm_repack(m.p, 1, 0, m.P, m.C, m.ldp, w + p.at_p, p.ldp, 0, nullptr, s);
+            m.p = w + p.at_p;
+            m.ldp = p.ldp;
+        }
+        if (p.planes_q && e == hipSuccess) {
+            e = ssg::launch_fp8_planes(c.a.w, m.E, m.Q, nb, (float*)(w + p.at_ws), p.wplane, s);
+            c.a.w = {(const float*)(w + p.at_ws), 1, p.wplane, nb * p.wplane};
+        }
+        if (p.planes_p && e == hipSuccess) {
+            e = ssg::launch_fp8_planes(c.a.x, 1, m.P, nb, (float*)(w + p.at_xs), p.xplane, s);
+            c.a.x = {(const float*)(w + p.at_xs), 1, p.xplane, 0};
+        }
+        if (e == hipSuccess) e = ssg::launch_mm_fp8_tiles(c.a, p.size, s);
+    }
+    if (e == hipSuccess && p.splits > 1) e = ssg::launch_mm_reduce(m, s);
+    return hip_status(e);
+}
+
+int check_y(int y, const void* Y, int64_t N, int64_t M, int64_t ldy, Call* c) {
+    if (source(y) < 0) return abi_failf(SSG_ERR_DTYPE, "output of type %d", y);
+    const int rc = check_mat("Y", Y, N, M, ldy);
+    if (rc) return rc;
+    c->a.exact = y == SSG_F32;         // a 16-bit output's own rounding hides the 8-bit instruction's
+    c->a.m.out = y == SSG_F32 ? ssg::OUT_F32 : y == SSG_F16 ? ssg::OUT_F16 : ssg::OUT_BF16;
+    c->a.m.y = const_cast<void*>(Y);
+    c->a.m.ldy = ldy;
+    return SSG_OK;
+}
+
+size_t bytes_of(int rc, const Call& c) { return rc || c.a.m.P == 0 || c.a.m.Q == 0 ? 0 : plan(c).bytes; }
+
+}  // namespace
+
+extern "C" {
+
+int64_t ssg_fp8_scale_cols(int64_t K) { return blocks(K); }
+
+int ssg_fp8_quantize(int dtype, int64_t B, int64_t R, int64_t K, const void* A, int64_t lda, int64_t stridea, int block,
+                     int transpose, uint8_t* elems, int64_t lde, int64_t stridee, float* scales, int64_t row,
+                     int64_t blk, int64_t strides, void* stream) {
+    const int rc = check_fp8(dtype, B, R, K, block, A, lda, transpose != 0, elems, lde, scales, row, blk);
+    if (rc || B == 0 || R == 0 || K == 0) return rc;
+    Fp8Matrix a{source(dtype), B, R, K, A, lda, stridea, block, transpose != 0, elems, lde, stridee, scales, row, blk, strides};
+    return hip_status(ssg::launch_fp8_quantize(a, (hipStream_t)stream));
+}
+
+int ssg_fp8_dequantize(int dtype, int64_t B, int64_t R, int64_t K, const uint8_t* elems, int64_t lde, int64_t stridee,
+                       int block, const float* scales, int64_t row, int64_t blk, int64_t strides, void* D, int64_t ldd,
+                       int64_t strided, void* stream) {
+    if (source(dtype) < 0) return abi_failf(SSG_ERR_DTYPE, "element type %d", dtype);
+    if (block != 1 && block != ssg::kFp8Block) return abi_failf(SSG_ERR_FORMAT, "%d rows to a scale (1 or 128)", block);
+    if (B < 0 || R < 0 || K < 0 || B >= (1 << 20) || R >= kMaxDim || K >= kMaxDim)
+        return abi_failf(SSG_ERR_SHAPE, "size B=%lld R=%lld K=%lld", (ll)B, (ll)R, (ll)K);
+    int rc;
+    if ((rc = check_mat("elems", elems, B * R, K, lde)) || (rc = check_scales("scales", scales, B * R, K, row, blk)) ||
+        (rc = check_mat("D", D, B * R, K, ldd)))
+        return rc;
+    if (B == 0 || R == 0 || K == 0) return SSG_OK;
+    Fp8Matrix a{source(dtype), B, R, K, D, ldd, strided, block, false, const_cast<uint8_t*>(elems), lde, stridee,
+                const_cast<float*>(scales), row, blk, strides};
+    return hip_status(ssg::launch_fp8_dequantize(a, (hipStream_t)stream));
+}
+
+size_t ssg_mm_fp8_workspace_bytes(int x, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const float* xs,
+                                  int64_t xsr, int64_t xsk, const uint8_t* W, int64_t ldw, int wblock, const float* wsc,
+                                  int64_t wsr, int64_t wsk) {
+    Call c{};
+    return bytes_of(mm_args(x, 1, M, N, K, X, ldx, xs, xsr, xsk, W, ldw, 0, wblock, wsc, wsr, wsk, 0, nullptr, false, &c), c);
+}
+
+int ssg_mm_fp8(int x, int y, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const float* xs, int64_t xsr,
+               int64_t xsk, const uint8_t* W, int64_t ldw, int wblock, const float* wsc, int64_t wsr, int64_t wsk,
+               void* Y, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+    Call c{};
+    int rc = mm_args(x, 1, M, N, K, X, ldx, xs, xsr, xsk, W, ldw, 0, wblock, wsc, wsr, wsk, 0, nullptr, false, &c);
+    if (rc || (rc = check_y(y, Y, N, M, ldy, &c))) return rc;
+    return run(c, ws, ws_bytes, (hipStream_t)stream);
+}
+
+size_t ssg_grouped_mm_fp8_workspace_bytes(int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+                                          const float* xs, int64_t xsr, int64_t xsk, const uint8_t* W, int64_t ldw,
+                                          int64_t stridew, int wblock, const float* wsc, int64_t wsr, int64_t wsk,
+                                          int64_t strides, const int32_t* offs) {
+    Call c{};
+    return bytes_of(mm_args(x, E, M, N, K, X, ldx, xs, xsr, xsk, W, ldw, stridew, wblock, wsc, wsr, wsk, strides, offs, true, &c), c);
+}
+
+int ssg_grouped_mm_fp8(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+                       const float* xs, int64_t xsr, int64_t xsk, const uint8_t* W, int64_t ldw, int64_t stridew,
+                       int wblock, const float* wsc, int64_t wsr, int64_t wsk, int64_t strides, const int32_t* offs,
+                       void* Y, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+    Call c{};
+    int rc = mm_args(x, E, M, N, K, X, ldx, xs, xsr, xsk, W, ldw, stridew, wblock, wsc, wsr, wsk, strides, offs, true, &c);
+    if (rc || (rc = check_y(y, Y, N, M, ldy, &c))) return rc;
+    return run(c, ws, ws_bytes, (hipStream_t)stream);
+}
+
+}  // extern "C"

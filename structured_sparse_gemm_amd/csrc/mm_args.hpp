@@ -13,8 +13,8 @@
 namespace ssg {
 
 // What the two operands hold: 16-bit floats both; mx4 both; mx4 weights (Q)
-// against 16-bit activations (P).
-enum MmMode { MM_16 = 0, MM_MX4 = 1, MM_W4 = 2 };
+// against 16-bit activations (P); e4m3 both (fp8.hpp).
+enum MmMode { MM_16 = 0, MM_MX4 = 1, MM_W4 = 2, MM_FP8 = 3 };
 enum MmOut { OUT_F32 = 0, OUT_F16 = 1, OUT_BF16 = 2 };
 
 constexpr int kMxBlock = 32;           // elements that share one scale byte
