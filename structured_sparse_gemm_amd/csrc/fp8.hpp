@@ -23,9 +23,6 @@ struct MmFp8Args {
     int x_src;                         // few rows: Fp8Src of X that the kernel rounds itself, or -1
     bool exact;                        // tiles: sums as fp32's (fp8_mfma_exact)
 };
-// Tiles of the kernels: of 8-bit products, of exact ones.
-constexpr MmTileSize kFp8TileSizes[2][2] = {{{256, 256, 1, 1.0, 0.3}, {128, 128, 2, 0.6, 0.3}},
-                                            {{256, 128, 1, 1.0, 0.3}, {128, 128, 2, 0.8, 0.3}}};
 hipError_t launch_mm_fp8_few(const MmFp8Args& a, int rt, int nt, hipStream_t s);
 hipError_t launch_mm_fp8_tiles(const MmFp8Args& a, int size, hipStream_t s);
 

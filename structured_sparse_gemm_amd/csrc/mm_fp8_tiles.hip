@@ -9,13 +9,16 @@
 // four multiplications more.
 //
 // A workgroup owns a TQ x TP tile of one expert's Y; both operands stream through
-// LDS a block (128 bytes of every row) at a time by direct-to-LDS loads, two
-// slots.  A slot is freed in two phases: a wave keeps its weight fragments of the
-// block in registers and goes through the tokens' fragments in two halves, so
-// after the first half the weights' part and the first tokens' part of the slot
-// take the loads of the block after next, after the second half the rest.  Every
-// load thus has one and a half blocks' time to arrive in LDS for two.  (Tiles of few
-// token fragments have one phase.)
+// LDS a block (128 bytes of every row) at a time by direct-to-LDS loads.  A wave
+// has the weights' fragments of a block in registers and goes through the tokens'
+// one by one: a fragment's MFMAs are issued with the multiply-adds of two MFMAs
+// before, the LDS reads of the next fragment and of the next block's weights, and
+// a few of the loads of blocks to come between them.
+//
+// 256 x 256 tiles fill LDS with two blocks, so a block is freed in halves: its
+// weights once every wave has them (before it starts on the block), the first four
+// token fragments of each wave after the first half, the others after the second.
+// Smaller tiles have three blocks in LDS (or two, and two workgroups on a CU).
 //
 // LDS image, the row order of fragments, the order of tiles and the cut of the
 // last round are those of mm_tiles.hpp: a block is two of its 64-byte stages, and a
@@ -65,15 +68,16 @@ struct Walk {
 template <int TQ, int TP, int WQ, int WP>
 struct Fp8Lay {
     static constexpr int NW = WQ * WP, FQ = TQ / WQ / 16, FP = TP / WP / 16;
-    static constexpr int NPH = FP > 4 ? 2 : 1, YP = FP / NPH;        // phases of a block, token fragments of each
+    static constexpr int NPH = FP > 4 ? 2 : 1, YP = FP / NPH;        // halves of a block, token fragments of each
     static constexpr int Q_BYTES = TQ * 128, P_BYTES = TP * 128;
     static constexpr int P_AT = Q_BYTES, SLOT = P_AT + P_BYTES;
-    // Scales: read in both phases of a block, but loaded with its first part, so
-    // the block after next must not take their place.
-    static constexpr int S_AT = 2 * SLOT, WS_AT = 1024, S_SLOT = 2048;
+    static constexpr int SLOTS = NPH == 2 || NW < 8 ? 2 : 3;
+    static constexpr bool PRE = NPH == 2 || SLOTS == 3;              // the next block is in LDS while this one is multiplied
+    // Scales in four slots: they are loaded with a block's first part and read until its end.
+    static constexpr int S_AT = SLOTS * SLOT, WS_AT = 1024, S_SLOT = 2048;
     static constexpr int LDS = S_AT + 4 * S_SLOT;
-    static constexpr int QL = TQ / 16 * 2 / NW, PL = YP * WP * 2 / NW;   // loads of a wave: weights, tokens of a phase
-    static constexpr int FIRST = QL + PL + 1;                            // and in all, with a scale load
+    static constexpr int QL = TQ / 16 * 2 / NW, PL = YP * WP * 2 / NW;   // loads of a wave: weights, tokens of a half
+    static constexpr int ALL = QL + PL + 1;                              // of a block of one half, with a scale load
     static_assert(FQ == 4 && QL % 2 == 0 && PL % 2 == 0 && TQ <= 256 && TP <= 256, "tile");
     static_assert(NW * 8192 <= LDS && LDS <= 160 * 1024, "LDS");
 };
@@ -134,7 +138,8 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
             pf[h][j] = n / L::YP * L::FP + h * L::YP + n % L::YP;
             poff[h][j] = (uint32_t)(row_of(pf[h][j] * 16 + (lane >> 2)) * m.ldp + chunk);
         }
-    auto slot_of = [&](int b) { return lds32 + (b & 1) * L::SLOT; };
+    auto slot_at = [&](int b) { return (uint32_t)(L::SLOTS == 2 ? b & 1 : b % 3) * L::SLOT; };
+    auto slot_of = [&](int b) { return lds32 + slot_at(b); };
     auto scales_of = [&](int b) { return L::S_AT + (b & 3) * L::S_SLOT; };
     auto issue_q = [&](int b) {
         const i32x4 r = bq.at(b, true);
@@ -166,7 +171,7 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
     };
     using H0 = std::integral_constant<int, 0>;
     using H1 = std::integral_constant<int, L::NPH - 1>;
-    auto issue_first = [&](int b) {
+    auto issue_block = [&](int b) {    // of one half
         issue_q(b);
         issue_p(H0{}, b);
         issue_s(b);
@@ -178,14 +183,14 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
     const int tail = tail64 < kFp8Block ? (int)tail64 : kFp8Block;
     auto clear = [&](uint8_t* piece, int half) {
         const int n = tail - 64 * half - chunk;        // bytes of the lane's chunk that stay
-        if (n >= 16) return;
-        uint32_t* const d = reinterpret_cast<uint32_t*>(piece + lane * 16);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int keep = n - 4 * k;
-            if (keep <= 0) d[k] = 0;
-            else if (keep < 4) d[k] &= (1u << (8 * keep)) - 1;
-        }
+        uint4* const d = reinterpret_cast<uint4*>(piece + lane * 16);
+        uint4 v = *d;
+        auto mask = [&](int k) { return n >= 4 * k + 4 ? ~0u : n <= 4 * k ? 0u : (1u << (8 * (n - 4 * k))) - 1; };
+        v.x &= mask(0);
+        v.y &= mask(1);
+        v.z &= mask(2);
+        v.w &= mask(3);
+        *d = v;
     };
     auto clear_q = [&](uint8_t* s) {
 #pragma unroll
@@ -210,89 +215,198 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
         for (int y = 0; y < L::FP; ++y) acc[x][y] = f32x4{0, 0, 0, 0};
 
     const int fq0 = wq * L::FQ, fp0 = wp * L::FP;
-    auto frag = [&](const uint8_t* at, int f) -> uint4 {
-        return *reinterpret_cast<const uint4*>(at + f * 1024 + i * 64 + ((g ^ mm_swz(i)) << 4));
+    const int at_lane = i * 64 + ((g ^ mm_swz(i)) << 4);
+    struct Raw {
+        uint4 lo, hi;
     };
-    uint4 q[EX ? 1 : L::FQ][2];
-    Fp8Wide qx[EX ? L::FQ : 1];
-    float ws = 0.0f;
-    f32x4 wr[WR ? 4 : 1];              // scales of rows 16 g + 4 r + x of the wave's 64: [r][x]
-    auto phase = [&](auto hc, int b) {
-        constexpr int H = decltype(hc)::value;
-        const uint8_t *const s = lds + (b & 1) * L::SLOT, *const sc = lds + scales_of(b);
-        if constexpr (H == 0) {
+    auto frag = [](const uint8_t* at, int rows) -> Raw {
+        return {*reinterpret_cast<const uint4*>(at), *reinterpret_cast<const uint4*>(at + rows * 64)};
+    };
+    // Where a block is in LDS: this lane's fragments in its slot, and its scales.
+    struct Place {
+        const uint8_t *slot, *sc;
+    };
+    auto place = [&](int b) -> Place { return {lds + slot_at(b) + at_lane, lds + scales_of(b)}; };
+    // weights of a block: fragments, and scales (of 128 rows, or of rows
+    // 16 g + 4 r + x of the wave's 64: [r][x])
+    struct Weights {
+        Raw q[L::FQ];
+        float s;
+        f32x4 r[WR ? 4 : 1];
+    };
+    const int q_at = fq0 * 1024, p_at = L::P_AT + fp0 * 1024;
+    const int ws_at = L::WS_AT + (WR ? (wq * 64 + 16 * g) * 4 : wq * 64 / kFp8Block * 4);
+    const int xs_at = (fp0 / 4 * 64 + 4 * i + fp0 % 4) * 4;
+    auto read_q = [&](auto xc, const Place& at, Weights& w_) {
+        constexpr int X = decltype(xc)::value;
+        w_.q[X] = frag(at.slot + q_at + X * 1024, TQ);
+        if constexpr (WR) w_.r[X] = *reinterpret_cast<const f32x4*>(at.sc + ws_at + 16 * X);
+        else if constexpr (X == 0) w_.s = *reinterpret_cast<const float*>(at.sc + ws_at);
+    };
+    struct Tokens {
+        Raw p;
+        float s;
+    };
+    auto read_p = [&](auto yc, const Place& at) -> Tokens {
+        constexpr int Y = decltype(yc)::value;
+        return {frag(at.slot + p_at + Y * 1024, TP), *reinterpret_cast<const float*>(at.sc + xs_at + (Y / 4 * 64 + Y % 4) * 4)};
+    };
+
+    Weights wt[2];                     // of blocks (even, odd)
+    Fp8Wide qx[EX ? L::FQ : 1], px[EX ? 2 : 1];
+    Tokens tok[2];                     // of fragments y (even, odd)
+    f32x4 t[4];                        // sums of the last MFMAs, by step number
+    float f[2];                        // of the tokens of fragments (even, odd): their scale, times the weights' if that is one
 #pragma unroll
-            for (int x = 0; x < L::FQ; ++x) {
-                const uint4 a0 = frag(s, fq0 + x), a1 = frag(s + TQ * 64, fq0 + x);
-                if constexpr (EX) {
-                    qx[x] = fp8_widen(a0, a1);
-                } else {
-                    q[x][0] = a0;
-                    q[x][1] = a1;
-                }
-            }
-            if constexpr (WR) {
+    for (int k = 0; k < 4; ++k) t[k] = f32x4{0, 0, 0, 0};
+    f[0] = f[1] = 0.0f;
+    if constexpr (WR) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    wr[r] = *reinterpret_cast<const f32x4*>(sc + L::WS_AT + (wq * 64 + 16 * g + 4 * r) * 4);
-            } else {
-                ws = *reinterpret_cast<const float*>(sc + L::WS_AT + (wq * 64 / kFp8Block) * 4);
+        for (int k = 0; k < 4; ++k) wt[1].r[k] = f32x4{0, 0, 0, 0};
+    }
+    // One step: fragment Y of the tokens with X of the weights, and the multiply-adds of two steps before.
+    auto add = [&](auto yc, auto xc, const Weights& of) {
+        constexpr int Y = decltype(yc)::value, X = decltype(xc)::value, K = Y * L::FQ + X;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            acc[X][Y][r] = WR ? fmaf(t[K & 3][r] * f[Y & 1], of.r[WR ? r : 0][X], acc[X][Y][r])
+                              : fmaf(t[K & 3][r], f[Y & 1], acc[X][Y][r]);
+        asm volatile("" : "+v"(acc[X][Y]));            // here: the compiler would collect them behind the next branch
+    };
+    // Fragment Y of the tokens of a block at `at` (the next one: `to`) with weights
+    // `cur`, four steps; `loads` issues its share of the loads.
+    auto group = [&](auto yc, const Place& at, const Place& to, const Weights& cur, Weights& nxt, auto&& loads) {
+        constexpr int Y = decltype(yc)::value;
+        f[Y & 1] = WR ? tok[Y & 1].s : cur.s * tok[Y & 1].s;
+        mm_for<L::FQ>([&](auto xc) {
+            constexpr int X = decltype(xc)::value, K = Y * L::FQ + X, J = (K + L::FQ * L::FP - 2) % (L::FQ * L::FP);
+            if constexpr (EX) t[K & 3] = fp8_mfma_exact(qx[X], px[Y & 1]);
+            else t[K & 3] = fp8_mfma(cur.q[X].lo, cur.q[X].hi, tok[Y & 1].p.lo, tok[Y & 1].p.hi);
+            add(std::integral_constant<int, J / L::FQ>{}, std::integral_constant<int, J % L::FQ>{}, K >= 2 ? cur : nxt);
+            if constexpr (X == 0) {
+                if constexpr (Y + 1 < L::FP) tok[(Y + 1) & 1] = read_p(std::integral_constant<int, Y + 1>{}, at);
+                else if constexpr (L::PRE) tok[0] = read_p(std::integral_constant<int, 0>{}, to);
+            } else if constexpr (X == 1) {
+                loads();
+            } else if constexpr (X == 2 && L::PRE) {
+                // the next block's weights, over the last FQ fragments; exact products widen
+                // them in the last one, and have them a fragment earlier
+                constexpr int N = (EX ? 2 : 1) * (L::FP < L::FQ ? L::FQ / L::FP : 1);
+                constexpr int AT = (Y - (L::FP - L::FQ / N - (EX && L::FP > 2))) * N;
+                if constexpr (AT >= 0 && AT < L::FQ)
+                    mm_for<N>([&](auto n) { read_q(std::integral_constant<int, (AT < 0 ? 0 : AT) + decltype(n)::value>{}, to, nxt); });
             }
+            if constexpr (EX) {
+                // what has had its last use, and the next tokens
+                if constexpr (Y + 1 == L::FP && L::PRE) qx[X] = fp8_widen(nxt.q[X].lo, nxt.q[X].hi);
+                if constexpr (X == 3 && (Y + 1 < L::FP || L::PRE)) px[(Y + 1) & 1] = fp8_widen(tok[(Y + 1) & 1].p.lo, tok[(Y + 1) & 1].p.hi);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    auto widen_block = [&](const Weights& w_) {        // weights and first tokens that were read ahead
+        if constexpr (EX) {
+            mm_for<L::FQ>([&](auto xc) {
+                constexpr int X = decltype(xc)::value;
+                qx[X] = fp8_widen(w_.q[X].lo, w_.q[X].hi);
+            });
+            px[0] = fp8_widen(tok[0].p.lo, tok[0].p.hi);
         }
-#pragma unroll
-        for (int yy = 0; yy < L::YP; ++yy) {
-            const int y = H * L::YP + yy, f = fp0 + y;
-            const uint4 p0 = frag(s + L::P_AT, f), p1 = frag(s + L::P_AT + TP * 64, f);
-            const float xs = *reinterpret_cast<const float*>(sc + (f / 4 * 64 + 4 * i + f % 4) * 4);
-            Fp8Wide px;
-            if constexpr (EX) px = fp8_widen(p0, p1);
-#pragma unroll
-            for (int x = 0; x < L::FQ; ++x) {
-                f32x4 d;
-                if constexpr (EX) d = fp8_mfma_exact(qx[x], px);
-                else d = fp8_mfma(q[x][0], q[x][1], p0, p1);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[x][y][r] = fmaf(d[r], xs * (WR ? wr[WR ? r : 0][x] : ws), acc[x][y][r]);
-            }
+    };
+    auto read_block = [&](const Place& at, Weights& w_) {
+        mm_for<L::FQ>([&](auto xc) { read_q(xc, at, w_); });
+        tok[0] = read_p(std::integral_constant<int, 0>{}, at);
+        widen_block(w_);
+    };
+    auto none = [] {};
+    auto by_twos = [&](auto&& block) {                 // block(b, this one's weights, the next one's)
+        int b = 0;
+        for (; b + 2 <= w.nst; b += 2) {
+            block(b, wt[0], wt[1]);
+            block(b + 1, wt[1], wt[0]);
         }
+        if (b < w.nst) block(b, wt[0], wt[1]);
     };
 
     if (w.nst > 0) {
-        uint8_t* const last_slot = lds + (last & 1) * L::SLOT;
+        auto tail_first = [&](int b) {                 // weights and first tokens of block b have landed
+            if (b != last || tail == kFp8Block) return;
+            uint8_t* const s = lds + slot_at(b);
+            clear_q(s);
+            clear_p(H0{}, s);
+        };
         if constexpr (L::NPH == 2) {
-            issue_first(0);
+            issue_q(0);
+            issue_p(H0{}, 0);
+            issue_s(0);
             issue_p(H1{}, 0);
-            issue_first(1);
-            constexpr int V = L::FIRST + L::PL;
-            for (int b = 0; b < w.nst; ++b) {
-                // newer than what this phase reads: the other half's loads and the next block's first
-                wait_vm<V>();
-                if (b == last && tail < kFp8Block) {
-                    clear_q(last_slot);
-                    clear_p(H0{}, last_slot);
-                }
-                lds_barrier();         // this half has landed, every wave has read the last one
-                issue_p(H1{}, b + 1);
-                phase(H0{}, b);
-                wait_vm<V>();
-                if (b == last && tail < kFp8Block) clear_p(H1{}, last_slot);
+            issue_q(1);
+            issue_p(H0{}, 1);
+            issue_s(1);
+            wait_vm<2 * L::PL + L::QL + 1>();
+            tail_first(0);
+            lds_barrier();
+            read_block(place(0), wt[0]);
+            by_twos([&](int b, const Weights& cur, Weights& nxt) {
+                const Place at = place(b), to = place(b + 1);
+                auto go = [&](auto yc, auto&& loads) { group(yc, at, to, cur, nxt, loads); };
+                // the second half of this block has landed; every wave has its weights, and
+                // has read the second half of the last block
+                wait_vm<L::QL + L::PL + 1>();
+                if (b == last && tail < kFp8Block) clear_p(H1{}, lds + slot_at(b));
                 lds_barrier();
-                issue_first(b + 2);
-                phase(H1{}, b);
-            }
+                go(std::integral_constant<int, 0>{}, [&] { issue_p(H1{}, b + 1); });
+                go(std::integral_constant<int, 1>{}, [&] { issue_q(b + 2); });
+                go(std::integral_constant<int, 2>{}, none);
+                go(std::integral_constant<int, 3>{}, none);
+                // the next block's weights and first half have landed; every wave has read this one's
+                wait_vm<L::QL + L::PL>();
+                tail_first(b + 1);
+                lds_barrier();
+                go(std::integral_constant<int, 4>{}, [&] { issue_p(H0{}, b + 2); });
+                go(std::integral_constant<int, 5>{}, [&] { issue_s(b + 2); });
+                go(std::integral_constant<int, 6>{}, none);
+                go(std::integral_constant<int, 7>{}, none);
+            });
+        } else if constexpr (L::PRE) {
+            issue_block(0);
+            issue_block(1);
+            wait_vm<L::ALL>();
+            tail_first(0);
+            lds_barrier();
+            read_block(place(0), wt[0]);
+            by_twos([&](int b, const Weights& cur, Weights& nxt) {
+                const Place at = place(b), to = place(b + 1);
+                wait_vm<0>();          // the next block has landed, every wave is done with the last one
+                tail_first(b + 1);
+                lds_barrier();
+                mm_for<L::FP>([&](auto yc) {
+                    if constexpr (decltype(yc)::value == 0) group(yc, at, to, cur, nxt, [&] { issue_block(b + 2); });
+                    else group(yc, at, to, cur, nxt, none);
+                });
+            });
         } else {
-            issue_first(0);
-            for (int b = 0; b < w.nst; ++b) {
+            issue_block(0);
+            by_twos([&](int b, Weights& cur, Weights& nxt) {
+                const Place at = place(b);
                 wait_vm<0>();
-                if (b == last && tail < kFp8Block) {
-                    clear_q(last_slot);
-                    clear_p(H0{}, last_slot);
-                }
+                tail_first(b);
                 lds_barrier();
-                issue_first(b + 1);
-                phase(H0{}, b);
-            }
+                read_block(at, cur);
+                mm_for<L::FP>([&](auto yc) {
+                    if constexpr (decltype(yc)::value == 0) group(yc, at, at, cur, nxt, [&] { issue_block(b + 1); });
+                    else group(yc, at, at, cur, nxt, none);
+                });
+            });
         }
+        // the last two steps
+        constexpr int N = L::FQ * L::FP;
+        auto rest = [&](const Weights& of) {
+            add(std::integral_constant<int, (N - 2) / L::FQ>{}, std::integral_constant<int, (N - 2) % L::FQ>{}, of);
+            add(std::integral_constant<int, (N - 1) / L::FQ>{}, std::integral_constant<int, (N - 1) % L::FQ>{}, of);
+        };
+        if (last & 1) rest(wt[1]);
+        else rest(wt[0]);
         wait_vm<0>();                  // no load of this workgroup may land after it ends
     }
 
@@ -343,13 +457,15 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
     else write_out(std::integral_constant<int, 2>{}, std::false_type{});
 }
 
-// Large products: 256 x 256 tiles, the last round's cut where they fit (k_mm_large).
-template <bool WR>
+// Large products: 256 x TP tiles, the last round's cut where they fit (k_mm_large).
+template <bool WR, bool EX, int TP>
 __global__ void __launch_bounds__(512, 2) k_mm_fp8_large(MmFp8Args a, uint32_t nq, uint32_t np) {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[Fp8Lay<256, 256, 4, 2>::LDS];
-    const uint32_t rows = a.m.offs ? (uint32_t)mm_count_tiles(a.m, 256) : np, total = rows * nq;
+    using A = Fp8Lay<256, TP, 4, 2>;
+    using B = Fp8Lay<256, 128, 4, 2>;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[A::LDS > B::LDS ? A::LDS : B::LDS];
+    const uint32_t rows = a.m.offs ? (uint32_t)mm_count_tiles(a.m, TP) : np, total = rows * nq;
     const uint32_t full = total / kMmCUs * kMmCUs, rem = total - full;
-    const uint32_t cut = rem <= kMmCUs / 4 ? 4 : rem <= kMmCUs / 2 ? 2 : 1;
+    const uint32_t cut = TP == 256 && rem <= kMmCUs / 4 ? 4 : rem <= kMmCUs / 2 ? 2 : 1;
     uint32_t id, part = 0, parts = 1;
     if (blockIdx.x < full) {
         if (!mm_xcd(blockIdx.x, full, &id)) return;
@@ -360,21 +476,24 @@ __global__ void __launch_bounds__(512, 2) k_mm_fp8_large(MmFp8Args a, uint32_t n
         id = full + id / cut;
     }
     MmWork w;
-    if (!mm_work<false, 256, 256>(a.m, id, rows, nq, 0, kFp8Block, &w)) return;
+    if (!mm_work<false, 256, TP>(a.m, id, rows, nq, 0, kFp8Block, &w)) return;
     if (parts > 1) {
-        const int64_t mid = w.r0 + 128;
-        if (part & 1) {
-            w.r0 = mid;
-            w.v0 = w.v0 > mid ? w.v0 : mid;
-        } else {
-            w.r1 = w.r1 < mid ? w.r1 : mid;
+        // of 256 rows the upper or lower half, and (in four) columns of one half; of 128 rows the columns
+        if (TP == 256) {
+            const int64_t mid = w.r0 + 128;
+            if (part & 1) {
+                w.r0 = mid;
+                w.v0 = w.v0 > mid ? w.v0 : mid;
+            } else {
+                w.r1 = w.r1 < mid ? w.r1 : mid;
+            }
         }
-        if (part & 2) w.q0 += 128;
+        if (part & (TP == 256 ? 2 : 1)) w.q0 += 128;
         if (w.v0 >= w.r1 || w.q0 >= a.m.Q) return;
     }
-    if (parts == 4) fp8_tile<WR, false, 128, 128, 2, 4>(a, w, lds);
-    else if (parts == 2 || w.r1 - w.r0 <= 128) fp8_tile<WR, false, 256, 128, 4, 2>(a, w, lds);
-    else fp8_tile<WR, false, 256, 256, 4, 2>(a, w, lds);
+    if (parts == (TP == 256 ? 4 : 2)) fp8_tile<WR, EX, 128, 128, 2, 4>(a, w, lds);
+    else if (TP == 128 || parts == 2 || w.r1 - w.r0 <= 128) fp8_tile<WR, EX, 256, 128, 4, 2>(a, w, lds);
+    else fp8_tile<WR, EX, 256, TP, 4, 2>(a, w, lds);
 }
 
 // Small products: one tile size, the contraction split where tiles are few.
@@ -392,18 +511,16 @@ __global__ void __launch_bounds__(WQ* WP * 64, 2) k_mm_fp8_tiles(MmFp8Args a, ui
 
 template <bool WR, bool EX>
 hipError_t go(const MmFp8Args& a, int size, hipStream_t s) {
-    const MmTileSize t = kFp8TileSizes[EX][size];
-    const int64_t nq = (a.m.Q + t.q - 1) / t.q, np = (a.m.P + t.p - 1) / t.p;
-    const int64_t total = mm_tile_bound(a.m, t.p) * nq * a.m.splits + (size == 0 ? 3 * kMmCUs / 4 : 0);
+    constexpr int TP = WR || EX ? 128 : 256;
+    const int tq = size == 0 ? 256 : 128, tp = size == 0 ? TP : 128;
+    const int64_t nq = (a.m.Q + tq - 1) / tq, np = (a.m.P + tp - 1) / tp;
+    // cutting the last round adds at most 3 workgroups for each of 64 tiles
+    const int64_t total = mm_tile_bound(a.m, tp) * nq * a.m.splits + (size == 0 ? 3 * kMmCUs / 4 : 0);
     if (total >= (int64_t)1 << 23) return hipErrorInvalidValue;
     const dim3 grid((unsigned)((total + 7) / 8 * 8));
     const uint32_t q = (uint32_t)nq, p = (uint32_t)np;
-    if (size == 0) {
-        if constexpr (EX) hipLaunchKernelGGL((k_mm_fp8_tiles<WR, true, 256, 128, 4, 2>), grid, dim3(512), 0, s, a, q, p);
-        else hipLaunchKernelGGL((k_mm_fp8_large<WR>), grid, dim3(512), 0, s, a, q, p);
-    } else {
-        hipLaunchKernelGGL((k_mm_fp8_tiles<WR, EX, 128, 128, 2, 2>), grid, dim3(256), 0, s, a, q, p);
-    }
+    if (size == 0) hipLaunchKernelGGL((k_mm_fp8_large<WR, EX, TP>), grid, dim3(512), 0, s, a, q, p);
+    else hipLaunchKernelGGL((k_mm_fp8_tiles<WR, EX, 128, 128, 2, 2>), grid, dim3(256), 0, s, a, q, p);
     return hipGetLastError();
 }
 
