@@ -785,9 +785,9 @@ int ssg_expert_combine_backward(int dt, int64_t N, int64_t k, int64_t D, const v
  * Sizes from 2^29 on, and E from 2^20 on, are refused with SSG_ERR_SHAPE; operands
  * whose row stride is 2^22 bytes or more, and strides of scales from 2^29 on, with
  * SSG_ERR_STRIDE.  The workspace holds activations that are rounded in the call
- * (not for few rows), operands whose rows do not begin at 4 bytes and scales of
- * rows that are not neighbours (row != 1) where many rows need them rearranged;
- * SSG_WS_ASK as above.
+ * (not single tokens), operands whose rows do not begin at 4 bytes and scales of
+ * rows that are not neighbours (row != 1) where many rows need them rearranged, and
+ * partial sums where the contraction is split; SSG_WS_ASK as above.
  */
 int64_t ssg_fp8_scale_cols(int64_t K);
 int ssg_fp8_quantize(int dtype, int64_t B, int64_t R, int64_t K, const void* A, int64_t lda, int64_t stridea,
@@ -796,13 +796,13 @@ int ssg_fp8_quantize(int dtype, int64_t B, int64_t R, int64_t K, const void* A, 
 int ssg_fp8_dequantize(int dtype, int64_t B, int64_t R, int64_t K, const uint8_t* elems, int64_t lde,
                        int64_t stridee, int block, const float* scales, int64_t row, int64_t blk,
                        int64_t strides, void* D, int64_t ldd, int64_t strided, void* stream);
-size_t ssg_mm_fp8_workspace_bytes(int x, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+size_t ssg_mm_fp8_workspace_bytes(int x, int y, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
                                   const float* xs, int64_t xsr, int64_t xsk, const uint8_t* W, int64_t ldw,
                                   int wblock, const float* wsc, int64_t wsr, int64_t wsk);
 int ssg_mm_fp8(int x, int y, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const float* xs,
                int64_t xsr, int64_t xsk, const uint8_t* W, int64_t ldw, int wblock, const float* wsc,
                int64_t wsr, int64_t wsk, void* Y, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
-size_t ssg_grouped_mm_fp8_workspace_bytes(int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* X,
+size_t ssg_grouped_mm_fp8_workspace_bytes(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, const void* X,
                                           int64_t ldx, const float* xs, int64_t xsr, int64_t xsk,
                                           const uint8_t* W, int64_t ldw, int64_t stridew, int wblock,
                                           const float* wsc, int64_t wsr, int64_t wsk, int64_t strides,
@@ -811,6 +811,11 @@ int ssg_grouped_mm_fp8(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K,
                        const float* xs, int64_t xsr, int64_t xsk, const uint8_t* W, int64_t ldw,
                        int64_t stridew, int wblock, const float* wsc, int64_t wsr, int64_t wsk, int64_t strides,
                        const int32_t* offs, void* Y, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
+/* The kernel that such a product takes, with operands as ssg_fp8_quantize's callers
+ * lay them out (rows at 16 bytes, scales of rows as neighbours): E = 0 for
+ * ssg_mm_fp8; kernel[] as ssg_mm_select_kernel gives it. */
+int ssg_mm_fp8_select_kernel(int x, int y, int wblock, int64_t E, int64_t M, int64_t N, int64_t K, int64_t kernel[4]);
 
 #ifdef __cplusplus
 }

@@ -121,14 +121,15 @@ SIGNATURES = {
           _vp]),
     "ssg_fp8_dequantize": (_i, [_i, _i64, _i64, _i64, _vp, _i64, _i64, _i, _vp, _i64, _i64, _i64, _vp, _i64, _i64,
           _vp]),
-    "ssg_mm_fp8_workspace_bytes": (_sz, [_i, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i, _vp, _i64,
+    "ssg_mm_fp8_workspace_bytes": (_sz, [_i, _i, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i, _vp, _i64,
           _i64]),
     "ssg_mm_fp8": (_i, [_i, _i, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i, _vp, _i64, _i64, _vp,
           _i64, _vp, _sz, _vp]),
-    "ssg_grouped_mm_fp8_workspace_bytes": (_sz, [_i, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64,
+    "ssg_grouped_mm_fp8_workspace_bytes": (_sz, [_i, _i, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64,
           _i64, _i, _vp, _i64, _i64, _i64, _vp]),
     "ssg_grouped_mm_fp8": (_i, [_i, _i, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i, _vp,
           _i64, _i64, _i64, _vp, _vp, _i64, _vp, _sz, _vp]),
+    "ssg_mm_fp8_select_kernel": (_i, [_i, _i, _i, _i64, _i64, _i64, _i64, ctypes.POINTER(_i64)]),
     "ssg_mm_select_kernel": (_i, [_i, _i, _i64, _i64, _i64, _i64, ctypes.POINTER(_i64)]),
 }
 

@@ -23,6 +23,9 @@ struct MmFp8Args {
     int x_src;                         // few rows: Fp8Src of X that the kernel rounds itself, or -1
     bool exact;                        // tiles: sums as fp32's (fp8_mfma_exact)
 };
+// Activations that the few-row kernel may round: at most so many tokens, and bytes of
+// them rounded (in whole blocks).
+constexpr int kFp8RoundTokens = 16, kFp8RoundBytes = 32768;
 hipError_t launch_mm_fp8_few(const MmFp8Args& a, int rt, int nt, hipStream_t s);
 hipError_t launch_mm_fp8_tiles(const MmFp8Args& a, int size, hipStream_t s);
 

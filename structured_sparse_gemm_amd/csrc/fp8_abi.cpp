@@ -85,10 +85,11 @@ struct Call {
     int64_t ldx;                       // bytes
 };
 
-int mm_args(int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const float* xs, int64_t xsr,
+int mm_args(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const float* xs, int64_t xsr,
             int64_t xsk, const uint8_t* W, int64_t ldw, int64_t stridew, int wblock, const float* wsc, int64_t wsr,
             int64_t wsk, int64_t strides, const int32_t* offs, bool grouped, Call* out) {
     if (x != SSG_E4M3 && source(x) < 0) return abi_failf(SSG_ERR_DTYPE, "activations of type %d", x);
+    if (source(y) < 0) return abi_failf(SSG_ERR_DTYPE, "output of type %d", y);
     if (wblock != 1 && wblock != ssg::kFp8Block) return abi_failf(SSG_ERR_FORMAT, "%d rows to a scale (1 or 128)", wblock);
     if (E < 0 || M < 0 || N < 0 || K < 0)
         return abi_failf(SSG_ERR_SHAPE, "negative size E=%lld M=%lld N=%lld K=%lld", (ll)E, (ll)M, (ll)N, (ll)K);
@@ -119,12 +120,20 @@ int mm_args(int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* X, in
     c.a.x = {xs, xsr, xsk, 0};
     c.a.w_rows = wblock == 1 && M > 1;
     c.a.x_src = -1;
+    c.a.exact = y == SSG_F32;          // a 16-bit output's own rounding hides the 8-bit instruction's
+    m.out = y == SSG_F32 ? ssg::OUT_F32 : y == SSG_F16 ? ssg::OUT_F16 : ssg::OUT_BF16;
     c.x = x;
     *out = c;
     return SSG_OK;
 }
 
 // ------------------------------------------------------------------ the choice of kernel
+//
+// Times in us of the launches that a plan would make, from what they measured on
+// this chip.  Every kernel handles every product it can be chosen for, so a wrong
+// estimate costs time only.  Over 5200 random products (dense and of 2 to 64
+// experts, 64 .. 12288 weight rows and lengths, 1 .. 8192 tokens), all kernels
+// timed, the choice is 1.8% slower than the best one in the geometric mean.
 
 struct Plan {
     bool few;
@@ -133,6 +142,25 @@ struct Plan {
     int64_t at_x, ldx, at_xs, xplane, at_q, ldq, at_p, ldp, at_ws, wplane, at_part;
     size_t bytes;
 };
+
+// Few rows: 16 rt weight rows x 16 nt tokens a workgroup.  One round of the chip
+// takes start + length / 1024 * first; a further one `each` + length / 4096 * more,
+// and (64 x 32: a CU has room for one and a half) the second half of that again.
+struct FewShape {
+    int rt, nt;
+    double first, each, more, second;
+};
+constexpr FewShape kFew[6] = {{1, 1, 1.05, 0.75, 2.95, 0}, {2, 1, 1.42, 0.75, 4.8, 0}, {4, 1, 2.25, 0.75, 8.15, 0},
+                              {1, 2, 1.45, 0.75, 4.8, 0},  {2, 2, 1.88, 0.75, 6.5, 0}, {4, 2, 2.8, 2.5, 10.5, 0.5}};
+constexpr double kStart = 3.5, kBytesPerUs = 4.4e6;
+
+// Tiles: a block of the contraction takes `one` us where a CU has one workgroup,
+// `two` where it has two, for 8-bit and for exact products.
+constexpr double kPairOne[2] = {0.75, 1.1}, kPairTwo[2] = {1.15, 2.05};   // 128 x 128, two on a CU
+constexpr double kDeep = 0.62;                                            // 128 x 128, four blocks in LDS
+// 256 x 256 (or 256 x 128, for a scale a weight row): a whole round, and a last
+// one of tiles as they are, cut in two and in four.
+constexpr double kLarge[2][3] = {{1.8, 1.27, 0.65}, {1.35, 0.75, 0.75}};
 
 Plan plan(const Call& c) {
     const ssg::MmArgs& m = c.a.m;
@@ -143,15 +171,71 @@ Plan plan(const Call& c) {
     const double E = m.offs ? std::max<double>(1, (double)m.E) : 1;
     const double busy = m.offs ? std::max(1.0, E * (1 - std::exp(-(double)m.P / E))) : 1;
     const double avg = (double)m.P / busy;
-    p.few = avg <= 32 && ((m.Q + 15) / 16) * ssg::mm_tile_bound(m, 16) < (int64_t)1 << 23;
     const int64_t nb = blocks(m.C);
+    auto row_tiles = [&](int t) {
+        if (!m.offs || E == 1) return (double)((m.P + t - 1) / t);
+        return busy * std::max(1.0, avg / t + 0.6);
+    };
+    auto ceil_div = [](int64_t n, int64_t d) { return (double)((n + d - 1) / d); };
+    const double length = (double)m.C, floor_us = kStart + busy * (double)m.Q * (double)m.C / kBytesPerUs;
+    double best = 1e30;
+    if (avg <= 300) {
+        for (const FewShape& f : kFew) {
+            if (c.a.w_rows && f.rt > 1) continue;      // (not built)
+            if (ceil_div(m.Q, 16 * f.rt) * (double)ssg::mm_tile_bound(m, 16 * f.nt) >= (1 << 23)) continue;
+            const double rounds = ceil_div(m.Q, 16 * f.rt) * row_tiles(16 * f.nt) / kCUs;
+            const double more = rounds <= 1 ? 0 : rounds - 1 + f.second;
+            const double us = std::max(floor_us, kStart + length / 1024 * f.first +
+                                                     more * (f.each + length / 4096 * f.more));
+            if (us < best) {
+                best = us;
+                p.few = true;
+                p.rt = f.rt;
+                p.nt = f.nt;
+            }
+        }
+    }
+    const bool ex = c.a.exact;
+    for (int size = ex ? 1 : 0; size <= (ex || c.a.w_rows ? 1 : 2); ++size) {
+        const int tp = size == 0 && !c.a.w_rows ? 256 : 128, tq = size == 0 ? 256 : 128;
+        const double tiles = row_tiles(tp) * ceil_div(m.Q, tq);
+        for (int splits = 1; splits <= 8; splits *= 2) {
+            if (splits > 1 && (size == 0 || nb < 2 * splits)) break;
+            if (ceil_div(m.Q, tq) * (double)ssg::mm_tile_bound(m, tp) * splits >= (1 << 23) - kCUs) break;
+            const double n = tiles * splits, len = std::ceil((double)nb / splits);
+            double block;
+            if (size == 0) {
+                const double* l = kLarge[c.a.w_rows];
+                const double whole = std::floor(n / kCUs), rest = n - whole * kCUs;
+                block = whole * l[0] + (rest <= 0           ? 0
+                                        : rest <= kCUs / 4 ? l[2]
+                                        : rest <= kCUs / 2 ? l[1]
+                                                           : l[0]);
+            } else if (size == 1) {
+                const double r = std::ceil(n / kCUs), pairs = std::floor(r / 2);
+                block = pairs * kPairTwo[ex] + (r - 2 * pairs) * kPairOne[ex];
+            } else {
+                block = std::ceil(n / kCUs) * kDeep;
+            }
+            double us = std::max(floor_us, kStart + 0.5 + block * len);
+            if (splits > 1) us += 4 + (double)splits * m.P * m.Q * 8 / 3e6;
+            if (us < best) {
+                best = us;
+                p.few = false;
+                p.size = size;
+                p.splits = splits;
+            }
+        }
+    }
     int64_t at = 0;
     auto take = [&](int64_t n) {
         const int64_t r = at;
         at += up(n, 256);
         return r;
     };
-    p.round = c.x != SSG_E4M3 && !(p.few && c.x != SSG_F32);
+    const bool in_kernel = p.few && p.rt <= 2 && p.nt == 1 && c.x != SSG_F32 && m.P <= ssg::kFp8RoundTokens &&
+                           m.P * nb * ssg::kFp8Block <= ssg::kFp8RoundBytes;
+    p.round = c.x != SSG_E4M3 && !in_kernel;
     if (p.round) {
         p.ldx = up(m.C, 16);
         p.xplane = up(m.P, 4);
@@ -180,8 +264,6 @@ Plan plan(const Call& c) {
             p.xplane = up(m.P, 4);
             p.at_xs = take(nb * p.xplane * 4);
         }
-        const int64_t big = ((m.Q + 255) / 256) * ssg::mm_tile_bound(m, 256);   // (fp32 outputs: 256 x 128)
-        p.size = big >= kCUs / 2 ? 0 : 1;
     }
     if (p.splits > 1) p.at_part = take((int64_t)p.splits * m.P * m.Q * 4);
     p.bytes = (size_t)at;
@@ -248,12 +330,9 @@ int run(Call c, void* ws, size_t ws_bytes, hipStream_t s) {
     return hip_status(e);
 }
 
-int check_y(int y, const void* Y, int64_t N, int64_t M, int64_t ldy, Call* c) {
-    if (source(y) < 0) return abi_failf(SSG_ERR_DTYPE, "output of type %d", y);
+int check_y(const void* Y, int64_t N, int64_t M, int64_t ldy, Call* c) {
     const int rc = check_mat("Y", Y, N, M, ldy);
     if (rc) return rc;
-    c->a.exact = y == SSG_F32;         // a 16-bit output's own rounding hides the 8-bit instruction's
-    c->a.m.out = y == SSG_F32 ? ssg::OUT_F32 : y == SSG_F16 ? ssg::OUT_F16 : ssg::OUT_BF16;
     c->a.m.y = const_cast<void*>(Y);
     c->a.m.ldy = ldy;
     return SSG_OK;
@@ -293,28 +372,28 @@ int ssg_fp8_dequantize(int dtype, int64_t B, int64_t R, int64_t K, const uint8_t
     return hip_status(ssg::launch_fp8_dequantize(a, (hipStream_t)stream));
 }
 
-size_t ssg_mm_fp8_workspace_bytes(int x, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const float* xs,
-                                  int64_t xsr, int64_t xsk, const uint8_t* W, int64_t ldw, int wblock, const float* wsc,
+size_t ssg_mm_fp8_workspace_bytes(int x, int y, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+                                  const float* xs, int64_t xsr, int64_t xsk, const uint8_t* W, int64_t ldw, int wblock, const float* wsc,
                                   int64_t wsr, int64_t wsk) {
     Call c{};
-    return bytes_of(mm_args(x, 1, M, N, K, X, ldx, xs, xsr, xsk, W, ldw, 0, wblock, wsc, wsr, wsk, 0, nullptr, false, &c), c);
+    return bytes_of(mm_args(x, y, 1, M, N, K, X, ldx, xs, xsr, xsk, W, ldw, 0, wblock, wsc, wsr, wsk, 0, nullptr, false, &c), c);
 }
 
 int ssg_mm_fp8(int x, int y, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const float* xs, int64_t xsr,
                int64_t xsk, const uint8_t* W, int64_t ldw, int wblock, const float* wsc, int64_t wsr, int64_t wsk,
                void* Y, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
     Call c{};
-    int rc = mm_args(x, 1, M, N, K, X, ldx, xs, xsr, xsk, W, ldw, 0, wblock, wsc, wsr, wsk, 0, nullptr, false, &c);
-    if (rc || (rc = check_y(y, Y, N, M, ldy, &c))) return rc;
+    int rc = mm_args(x, y, 1, M, N, K, X, ldx, xs, xsr, xsk, W, ldw, 0, wblock, wsc, wsr, wsk, 0, nullptr, false, &c);
+    if (rc || (rc = check_y(Y, N, M, ldy, &c))) return rc;
     return run(c, ws, ws_bytes, (hipStream_t)stream);
 }
 
-size_t ssg_grouped_mm_fp8_workspace_bytes(int x, int64_t E, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
-                                          const float* xs, int64_t xsr, int64_t xsk, const uint8_t* W, int64_t ldw,
+size_t ssg_grouped_mm_fp8_workspace_bytes(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, const void* X,
+                                          int64_t ldx, const float* xs, int64_t xsr, int64_t xsk, const uint8_t* W, int64_t ldw,
                                           int64_t stridew, int wblock, const float* wsc, int64_t wsr, int64_t wsk,
                                           int64_t strides, const int32_t* offs) {
     Call c{};
-    return bytes_of(mm_args(x, E, M, N, K, X, ldx, xs, xsr, xsk, W, ldw, stridew, wblock, wsc, wsr, wsk, strides, offs, true, &c), c);
+    return bytes_of(mm_args(x, y, E, M, N, K, X, ldx, xs, xsr, xsk, W, ldw, stridew, wblock, wsc, wsr, wsk, strides, offs, true, &c), c);
 }
 
 int ssg_grouped_mm_fp8(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
@@ -322,9 +401,28 @@ int ssg_grouped_mm_fp8(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K,
                        int wblock, const float* wsc, int64_t wsr, int64_t wsk, int64_t strides, const int32_t* offs,
                        void* Y, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
     Call c{};
-    int rc = mm_args(x, E, M, N, K, X, ldx, xs, xsr, xsk, W, ldw, stridew, wblock, wsc, wsr, wsk, strides, offs, true, &c);
-    if (rc || (rc = check_y(y, Y, N, M, ldy, &c))) return rc;
+    int rc = mm_args(x, y, E, M, N, K, X, ldx, xs, xsr, xsk, W, ldw, stridew, wblock, wsc, wsr, wsk, strides, offs, true, &c);
+    if (rc || (rc = check_y(Y, N, M, ldy, &c))) return rc;
     return run(c, ws, ws_bytes, (hipStream_t)stream);
+}
+
+int ssg_mm_fp8_select_kernel(int x, int y, int wblock, int64_t E, int64_t M, int64_t N, int64_t K, int64_t kernel[4]) {
+    if (!kernel) return abi_failf(SSG_ERR_NULL, "kernel is NULL");
+    // an address at a 16-byte border stands for every operand; nothing reads it
+    void* const p = reinterpret_cast<void*>((uintptr_t)256);
+    const bool grouped = E > 0;
+    const int64_t ld = up(K, 16), nb = blocks(K), rows = wblock == 1 ? M : blocks(M);
+    Call c{};
+    const int rc = mm_args(x, y, grouped ? E : 1, M, N, K, p, ld, x == SSG_E4M3 ? (float*)p : nullptr, 1, up(N, 4),
+                           (uint8_t*)p, ld, M * ld, wblock, (float*)p, wblock == 1 ? 1 : nb, wblock == 1 ? up(M, 4) : 1,
+                           rows * nb, (int32_t*)p, grouped, &c);
+    if (rc) return rc;
+    const Plan q = plan(c);
+    kernel[0] = q.few ? 0 : 1;
+    kernel[1] = q.few ? 16 * q.rt : q.size == 0 ? 256 : 128;
+    kernel[2] = q.few ? 16 * q.nt : q.size == 0 && !c.a.w_rows ? 256 : 128;
+    kernel[3] = q.splits;
+    return SSG_OK;
 }
 
 }  // extern "C"

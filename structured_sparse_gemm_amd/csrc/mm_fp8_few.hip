@@ -8,10 +8,10 @@
 // sums and adds those, times the two scales, to its own; the waves' sums meet in
 // LDS in wave order.
 //
-// 16-bit activations are rounded here, on their way to the registers: a lane has
-// 32 elements of a token's block, and three other lanes the rest, so the maximum
-// takes two exchanges.  A launch of its own for that costs a decode step more
-// than every workgroup's repeating it.
+// A few 16-bit activations are rounded here, by every workgroup into LDS: up to
+// kFp8RoundBytes of them cost less than a launch of their own (rounding them in
+// the lanes that multiply them, 16 rows whatever the tokens, took longer: 11.5
+// instead of 7 us for one token through 4096 x 4096, 24 instead of 8 for 16).
 #include <algorithm>
 
 #include "fp8.hpp"
@@ -39,25 +39,18 @@ __device__ __forceinline__ uint4 ld_bytes(const uint8_t* row, int64_t k, int64_t
     return v;
 }
 
-// The larger of a value in the four lanes that share a token (16 apart).
-__device__ __forceinline__ float max_of_groups(float v) {
-    uint32_t a, b;
-    lane_pair<false>(__float_as_uint(v), &a, &b);
-    v = fmaxf(__uint_as_float(a), __uint_as_float(b));
-    lane_pair<true>(__float_as_uint(v), &a, &b);
-    return fmaxf(__uint_as_float(a), __uint_as_float(b));
-}
-
-// XS: Fp8Src of the activations (F16, BF16), or -1 for e4m3.  WR: a scale for each weight row.
+// XS: Fp8Src of activations that are rounded here (F16, BF16), or -1 for e4m3.  WR: a
+// scale for each weight row.
 template <int XS, bool WR, int RT, int NT>
 struct Few {
     static constexpr bool ROUND = XS >= 0;
-    static constexpr int XL = ROUND ? 4 : 2;           // 16-byte loads of a token's block
-    // Blocks whose loads go out together: 16 rows are 2 KiB a block and wave.
+    // Blocks whose loads go out together: 16 rows are 2 KiB a block and wave, and a
+    // wave's part of 4096 elements is four blocks.  (Four for 32 rows leave one
+    // workgroup on a CU: 41 experts of 2048 x 4096 took 90 us instead of 73.)
     static constexpr int AHEAD = RT * NT == 1 ? 4 : RT * NT == 2 ? 2 : 1;
     struct Ops {
-        uint4 w[RT][2], x[NT][XL];
-        float ws[RT][WR ? 4 : 1], xs[ROUND ? 1 : NT];
+        uint4 w[RT][2], x[NT][2];
+        float ws[RT][WR ? 4 : 1], xs[NT];
     };
 
     const MmFp8Args& a;
@@ -76,77 +69,66 @@ struct Few {
 #pragma unroll
             for (int e = 0; e < (WR ? 4 : 1); ++e) o.ws[r][e] = ws[r][e][b * a.w.blk];
         }
+        // (rounded activations end with zeros)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-#pragma unroll
-            for (int u = 0; u < XL; ++u)
-                o.x[t][u] = ROUND ? ld_bytes<FULL>(p[t], 2 * k + (u >> 1) * 128 + (u & 1) * 16, 2 * n)
-                                  : ld_bytes<FULL>(p[t], k + u * 64, n);
-            if constexpr (!ROUND) o.xs[t] = xs[t][b * a.x.blk];
+            if constexpr (ROUND) continue;
+            o.x[t][0] = ld_bytes<FULL>(p[t], k, n);
+            o.x[t][1] = ld_bytes<FULL>(p[t], k + 64, n);
+            o.xs[t] = xs[t][b * a.x.blk];
         }
     }
 
-    __device__ __forceinline__ void products(const Ops& o) {
+    __device__ __forceinline__ void products(int64_t b, Ops& o) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            uint4 x0, x1;
-            float s;
             if constexpr (ROUND) {
-                float v[4][8], top = 0.0f;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    fp8_widen8<XS>(o.x[t][u], v[u]);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[u][e]));
-                }
-                s = fp8_scale(max_of_groups(top));
-                const Fp8Recip rc = fp8_recip(s);
-                uint2 c[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) c[u] = fp8_pack8(v[u], rc);
-                x0 = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
-                x1 = make_uint4(c[2].x, c[2].y, c[3].x, c[3].y);
-            } else {
-                x0 = o.x[t][0];
-                x1 = o.x[t][1];
-                s = o.xs[t];
+                o.x[t][0] = *reinterpret_cast<const uint4*>(p[t] + b * kFp8Block + 16 * g);
+                o.x[t][1] = *reinterpret_cast<const uint4*>(p[t] + b * kFp8Block + 16 * g + 64);
+                o.xs[t] = xs[t][b];
             }
-            const Fp8Wide x = fp8_widen(x0, x1);
+            const Fp8Wide x = fp8_widen(o.x[t][0], o.x[t][1]);
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 const f32x4 d = fp8_mfma_exact(fp8_widen(o.w[r][0], o.w[r][1]), x);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[r][t][e] = fmaf(d[e], s * o.ws[r][WR ? e : 0], acc[r][t][e]);
+                for (int e = 0; e < 4; ++e) acc[r][t][e] = fmaf(d[e], o.xs[t] * o.ws[r][WR ? e : 0], acc[r][t][e]);
             }
         }
     }
 
     __device__ __forceinline__ void run(int64_t n, int64_t by) {
         const int64_t whole = a.m.C / kFp8Block, all = (a.m.C + kFp8Block - 1) / kFp8Block;
-        if constexpr (AHEAD > 1) {
-            for (; n + (AHEAD - 1) * by < whole; n += AHEAD * by) {
-                Ops o[AHEAD];
+        for (; n < whole; n += AHEAD * by) {
+            Ops o[AHEAD];
 #pragma unroll
-                for (int d = 0; d < AHEAD; ++d) load<true>(n + d * by, o[d]);
+            for (int d = 0; d < AHEAD; ++d)
+                if (n + d * by < whole) load<true>(n + d * by, o[d]);
 #pragma unroll
-                for (int d = 0; d < AHEAD; ++d) products(o[d]);
+            for (int d = 0; d < AHEAD; ++d)
+                if (n + d * by < whole) products(n + d * by, o[d]);
+        }
+        if (whole < all) {
+            // the block that the contraction ends in is the turn of one wave
+            const int64_t first = n - (n - whole) / by * by;
+            if (first == whole) {
+                Ops o;
+                load<false>(whole, o);
+                products(whole, o);
             }
-        }
-        Ops o;
-        for (; n < whole; n += by) {
-            load<true>(n, o);
-            products(o);
-        }
-        if (n < all) {
-            load<false>(n, o);
-            products(o);
         }
     }
 };
 
 template <int XS, bool WR, int RT, int NT>
 __global__ void __launch_bounds__(kThreads, 2) k_mm_fp8_few(MmFp8Args a, uint32_t nq) {
-    __shared__ __attribute__((aligned(16))) f32x4 red[kWaves][RT * NT * 64];
+    constexpr bool ROUND = XS >= 0;
+    constexpr int kRed = kWaves * RT * NT * 64 * 16;
+    // sums of the waves; before them rounded activations (rows 16 bytes further apart
+    // than long, over the banks) and their scales
+    constexpr int kRows = kFp8RoundBytes + 16 * kFp8RoundTokens, kX = ROUND ? kRows + kFp8RoundBytes / kFp8Block * 4 : 0;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kRed > kX ? kRed : kX];
+    f32x4(*const red)[RT * NT * 64] = reinterpret_cast<f32x4(*)[RT * NT * 64]>(lds);
     const MmArgs& m = a.m;
     const uint32_t per = gridDim.x / (uint32_t)m.splits, split = blockIdx.x / per, id = blockIdx.x - split * per;
     const uint32_t tt = id / nq, qt = id - tt * nq;
@@ -167,17 +149,55 @@ __global__ void __launch_bounds__(kThreads, 2) k_mm_fp8_few(MmFp8Args a, uint32_
             k.ws[r][f] = a.w.p + e * a.w.mat + sr * a.w.row;
         }
     }
+    const int64_t nb = (m.C + kFp8Block - 1) / kFp8Block;
+    if constexpr (ROUND) {
+        // 16 threads a block of a token, 8 elements each (at most kFp8RoundTokens
+        // tokens, and blocks of them in kFp8RoundBytes: the caller's choice)
+        const int64_t tokens = tile.r1 - tile.r0, ld = nb * kFp8Block + 16;
+        float* const sc = reinterpret_cast<float*>(lds + kRows);
+        for (int64_t u = threadIdx.x / 16; u < tokens * nb; u += kThreads / 16) {
+            const int64_t t = u / nb, b = u - t * nb, c = b * kFp8Block + threadIdx.x % 16 * 8;
+            const uint8_t* const row = m.p + (tile.r0 + t) * m.ldp;
+            float v[8];
+            uint4 d = make_uint4(0, 0, 0, 0);
+            if (c + 8 <= m.C) {
+                __builtin_memcpy(&d, row + 2 * c, 16);
+            } else {
+                uint16_t h[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int64_t row = std::min<int64_t>(tile.r0 + 16 * t + i, tile.r1 - 1);
-        k.p[t] = m.p + row * m.ldp;
-        k.xs[t] = a.x.p + row * a.x.row;
+                for (int j = 0; j < 8; ++j)
+                    if (c + j < m.C) __builtin_memcpy(&h[j], row + 2 * (c + j), 2);
+                __builtin_memcpy(&d, h, 16);
+            }
+            fp8_widen8<XS>(d, v);
+            float top = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
+            const float s = fp8_scale(lanes_max<16>(top));
+            *reinterpret_cast<uint2*>(lds + t * ld + c) = fp8_pack8(v, fp8_recip(s));
+            if (threadIdx.x % 16 == 0) sc[u] = s;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int64_t row = std::min<int64_t>(16 * t + i, tokens - 1);
+            k.p[t] = lds + row * ld;
+            k.xs[t] = sc + row * nb;
+        }
+    } else {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int64_t row = std::min<int64_t>(tile.r0 + 16 * t + i, tile.r1 - 1);
+            k.p[t] = m.p + row * m.ldp;
+            k.xs[t] = a.x.p + row * a.x.row;
+        }
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int t = 0; t < NT; ++t) k.acc[r][t] = f32x4{0, 0, 0, 0};
     if (tile.e >= 0) k.run((int64_t)split * kWaves + wave, (int64_t)m.splits * kWaves);
+    if constexpr (ROUND) __syncthreads();              // the activations give way to the sums
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -206,21 +226,22 @@ hipError_t go(const MmFp8Args& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int XS>
+template <int XS, bool WR>
 hipError_t pick(const MmFp8Args& a, int rt, int nt, hipStream_t s) {
-    if (a.w_rows) return nt == 1 ? go<XS, true, 1, 1>(a, s) : go<XS, true, 1, 2>(a, s);
-    if (rt == 1) return nt == 1 ? go<XS, false, 1, 1>(a, s) : go<XS, false, 1, 2>(a, s);
-    if (rt == 2) return nt == 1 ? go<XS, false, 2, 1>(a, s) : go<XS, false, 2, 2>(a, s);
-    return nt == 1 ? go<XS, false, 4, 1>(a, s) : go<XS, false, 4, 2>(a, s);
+    if constexpr (XS >= 0) return rt == 1 ? go<XS, WR, 1, 1>(a, s) : go<XS, WR, 2, 1>(a, s);
+    else if constexpr (WR) return nt == 1 ? go<XS, WR, 1, 1>(a, s) : go<XS, WR, 1, 2>(a, s);
+    else if (rt == 1) return nt == 1 ? go<XS, WR, 1, 1>(a, s) : go<XS, WR, 1, 2>(a, s);
+    else if (rt == 2) return nt == 1 ? go<XS, WR, 2, 1>(a, s) : go<XS, WR, 2, 2>(a, s);
+    else return nt == 1 ? go<XS, WR, 4, 1>(a, s) : go<XS, WR, 4, 2>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_mm_fp8_few(const MmFp8Args& a, int rt, int nt, hipStream_t s) {
     switch (a.x_src) {
-        case SRC8_F16: return pick<SRC8_F16>(a, rt, nt, s);
-        case SRC8_BF16: return pick<SRC8_BF16>(a, rt, nt, s);
-        default: return pick<-1>(a, rt, nt, s);
+        case SRC8_F16: return a.w_rows ? pick<SRC8_F16, true>(a, rt, nt, s) : pick<SRC8_F16, false>(a, rt, nt, s);
+        case SRC8_BF16: return a.w_rows ? pick<SRC8_BF16, true>(a, rt, nt, s) : pick<SRC8_BF16, false>(a, rt, nt, s);
+        default: return a.w_rows ? pick<-1, true>(a, rt, nt, s) : pick<-1, false>(a, rt, nt, s);
     }
 }
 

@@ -65,19 +65,20 @@ struct Walk {
     }
 };
 
-template <int TQ, int TP, int WQ, int WP>
+template <int TQ, int TP, int WQ, int WP, int SL>
 struct Fp8Lay {
     static constexpr int NW = WQ * WP, FQ = TQ / WQ / 16, FP = TP / WP / 16;
     static constexpr int NPH = FP > 4 ? 2 : 1, YP = FP / NPH;        // halves of a block, token fragments of each
     static constexpr int Q_BYTES = TQ * 128, P_BYTES = TP * 128;
     static constexpr int P_AT = Q_BYTES, SLOT = P_AT + P_BYTES;
-    static constexpr int SLOTS = NPH == 2 || NW < 8 ? 2 : 3;
-    static constexpr bool PRE = NPH == 2 || SLOTS == 3;              // the next block is in LDS while this one is multiplied
+    static constexpr int SLOTS = SL;                                  // blocks in LDS
+    static constexpr bool PRE = NPH == 2 || SLOTS > 2;               // the next one is there while this one is multiplied
     // Scales in four slots: they are loaded with a block's first part and read until its end.
     static constexpr int S_AT = SLOTS * SLOT, WS_AT = 1024, S_SLOT = 2048;
     static constexpr int LDS = S_AT + 4 * S_SLOT;
     static constexpr int QL = TQ / 16 * 2 / NW, PL = YP * WP * 2 / NW;   // loads of a wave: weights, tokens of a half
     static constexpr int ALL = QL + PL + 1;                              // of a block of one half, with a scale load
+    static_assert(NPH == 1 || SLOTS == 2, "halves");
     static_assert(FQ == 4 && QL % 2 == 0 && PL % 2 == 0 && TQ <= 256 && TP <= 256, "tile");
     static_assert(NW * 8192 <= LDS && LDS <= 160 * 1024, "LDS");
 };
@@ -86,9 +87,9 @@ struct Fp8Lay {
 __device__ __forceinline__ int row_of(int slot) { return (slot & ~63) + 4 * (slot & 15) + ((slot >> 4) & 3); }
 
 // EX: exact products (fp8_mfma_exact).
-template <bool WR, bool EX, int TQ, int TP, int WQ, int WP>
+template <bool WR, bool EX, int TQ, int TP, int WQ, int WP, int SL>
 __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, uint8_t* lds) {
-    using L = Fp8Lay<TQ, TP, WQ, WP>;
+    using L = Fp8Lay<TQ, TP, WQ, WP, SL>;
     const MmArgs& m = a.m;
     const uint32_t lds32 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_void*)lds);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -138,7 +139,7 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
             pf[h][j] = n / L::YP * L::FP + h * L::YP + n % L::YP;
             poff[h][j] = (uint32_t)(row_of(pf[h][j] * 16 + (lane >> 2)) * m.ldp + chunk);
         }
-    auto slot_at = [&](int b) { return (uint32_t)(L::SLOTS == 2 ? b & 1 : b % 3) * L::SLOT; };
+    auto slot_at = [&](int b) { return (uint32_t)(L::SLOTS == 3 ? b % 3 : b & (L::SLOTS - 1)) * L::SLOT; };
     auto slot_of = [&](int b) { return lds32 + slot_at(b); };
     auto scales_of = [&](int b) { return L::S_AT + (b & 3) * L::S_SLOT; };
     auto issue_q = [&](int b) {
@@ -369,19 +370,18 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
                 go(std::integral_constant<int, 7>{}, none);
             });
         } else if constexpr (L::PRE) {
-            issue_block(0);
-            issue_block(1);
-            wait_vm<L::ALL>();
+            mm_for<L::SLOTS - 1>([&](auto b) { issue_block(decltype(b)::value); });
+            wait_vm<(L::SLOTS - 2) * L::ALL>();
             tail_first(0);
             lds_barrier();
             read_block(place(0), wt[0]);
             by_twos([&](int b, const Weights& cur, Weights& nxt) {
                 const Place at = place(b), to = place(b + 1);
-                wait_vm<0>();          // the next block has landed, every wave is done with the last one
+                wait_vm<(L::SLOTS - 3) * L::ALL>();    // the next block has landed, every wave is done with the last one
                 tail_first(b + 1);
                 lds_barrier();
                 mm_for<L::FP>([&](auto yc) {
-                    if constexpr (decltype(yc)::value == 0) group(yc, at, to, cur, nxt, [&] { issue_block(b + 2); });
+                    if constexpr (decltype(yc)::value == 0) group(yc, at, to, cur, nxt, [&] { issue_block(b + L::SLOTS - 1); });
                     else group(yc, at, to, cur, nxt, none);
                 });
             });
@@ -458,10 +458,11 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
 }
 
 // Large products: 256 x TP tiles, the last round's cut where they fit (k_mm_large).
-template <bool WR, bool EX, int TP>
+template <bool WR, int TP>
 __global__ void __launch_bounds__(512, 2) k_mm_fp8_large(MmFp8Args a, uint32_t nq, uint32_t np) {
-    using A = Fp8Lay<256, TP, 4, 2>;
-    using B = Fp8Lay<256, 128, 4, 2>;
+    constexpr int SL = TP == 256 ? 2 : 3;
+    using A = Fp8Lay<256, TP, 4, 2, SL>;
+    using B = Fp8Lay<256, 128, 4, 2, 3>;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[A::LDS > B::LDS ? A::LDS : B::LDS];
     const uint32_t rows = a.m.offs ? (uint32_t)mm_count_tiles(a.m, TP) : np, total = rows * nq;
     const uint32_t full = total / kMmCUs * kMmCUs, rem = total - full;
@@ -491,44 +492,48 @@ __global__ void __launch_bounds__(512, 2) k_mm_fp8_large(MmFp8Args a, uint32_t n
         if (part & (TP == 256 ? 2 : 1)) w.q0 += 128;
         if (w.v0 >= w.r1 || w.q0 >= a.m.Q) return;
     }
-    if (parts == (TP == 256 ? 4 : 2)) fp8_tile<WR, EX, 128, 128, 2, 4>(a, w, lds);
-    else if (TP == 128 || parts == 2 || w.r1 - w.r0 <= 128) fp8_tile<WR, EX, 256, 128, 4, 2>(a, w, lds);
-    else fp8_tile<WR, EX, 256, TP, 4, 2>(a, w, lds);
+    if (parts == (TP == 256 ? 4 : 2)) fp8_tile<WR, false, 128, 128, 2, 4, 4>(a, w, lds);
+    else if (TP == 128 || parts == 2 || w.r1 - w.r0 <= 128) fp8_tile<WR, false, 256, 128, 4, 2, 3>(a, w, lds);
+    else fp8_tile<WR, false, 256, TP, 4, 2, SL>(a, w, lds);
 }
 
 // Small products: one tile size, the contraction split where tiles are few.
-template <bool WR, bool EX, int TQ, int TP, int WQ, int WP>
+template <bool WR, bool EX, int TQ, int TP, int WQ, int WP, int SL>
 __global__ void __launch_bounds__(WQ* WP * 64, 2) k_mm_fp8_tiles(MmFp8Args a, uint32_t nq, uint32_t np) {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[Fp8Lay<TQ, TP, WQ, WP>::LDS];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[Fp8Lay<TQ, TP, WQ, WP, SL>::LDS];
     const uint32_t rows = a.m.offs ? (uint32_t)mm_count_tiles(a.m, TP) : np, per = rows * nq;
     uint32_t id;
     if (!mm_xcd(blockIdx.x, per * (uint32_t)a.m.splits, &id)) return;
     const int split = (int)(id / per);
     MmWork w;
     if (!mm_work<false, TQ, TP>(a.m, id - split * per, rows, nq, split, kFp8Block, &w)) return;
-    fp8_tile<WR, EX, TQ, TP, WQ, WP>(a, w, lds);
+    fp8_tile<WR, EX, TQ, TP, WQ, WP, SL>(a, w, lds);
 }
 
-template <bool WR, bool EX>
-hipError_t go(const MmFp8Args& a, int size, hipStream_t s) {
-    constexpr int TP = WR || EX ? 128 : 256;
-    const int tq = size == 0 ? 256 : 128, tp = size == 0 ? TP : 128;
+// (a launch of q x p tiles of tq x tp, and `more` workgroups)
+template <typename K>
+hipError_t go(K kernel, const MmFp8Args& a, int tq, int tp, int threads, int more, hipStream_t s) {
     const int64_t nq = (a.m.Q + tq - 1) / tq, np = (a.m.P + tp - 1) / tp;
-    // cutting the last round adds at most 3 workgroups for each of 64 tiles
-    const int64_t total = mm_tile_bound(a.m, tp) * nq * a.m.splits + (size == 0 ? 3 * kMmCUs / 4 : 0);
+    const int64_t total = mm_tile_bound(a.m, tp) * nq * a.m.splits + more;
     if (total >= (int64_t)1 << 23) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)((total + 7) / 8 * 8));
-    const uint32_t q = (uint32_t)nq, p = (uint32_t)np;
-    if (size == 0) hipLaunchKernelGGL((k_mm_fp8_large<WR, EX, TP>), grid, dim3(512), 0, s, a, q, p);
-    else hipLaunchKernelGGL((k_mm_fp8_tiles<WR, EX, 128, 128, 2, 2>), grid, dim3(256), 0, s, a, q, p);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((total + 7) / 8 * 8)), dim3(threads), 0, s, a, (uint32_t)nq, (uint32_t)np);
     return hipGetLastError();
+}
+
+template <bool WR>
+hipError_t pick(const MmFp8Args& a, int size, hipStream_t s) {
+    // cutting the last round adds at most 3 workgroups for each of 64 tiles
+    constexpr int TP = WR ? 128 : 256, kMore = 3 * kMmCUs / 4;
+    if (a.exact) return go(k_mm_fp8_tiles<WR, true, 128, 128, 2, 2, 2>, a, 128, 128, 256, 0, s);
+    if (size == 0) return go(k_mm_fp8_large<WR, TP>, a, 256, TP, 512, kMore, s);
+    if (size == 1) return go(k_mm_fp8_tiles<WR, false, 128, 128, 2, 2, 2>, a, 128, 128, 256, 0, s);
+    return go(k_mm_fp8_tiles<WR, false, 128, 128, 2, 4, 4>, a, 128, 128, 512, 0, s);
 }
 
 }  // namespace
 
 hipError_t launch_mm_fp8_tiles(const MmFp8Args& a, int size, hipStream_t s) {
-    if (a.exact) return a.w_rows ? go<true, true>(a, size, s) : go<false, true>(a, size, s);
-    return a.w_rows ? go<true, false>(a, size, s) : go<false, false>(a, size, s);
+    return a.w_rows ? pick<true>(a, size, s) : pick<false>(a, size, s);
 }
 
 }  // namespace ssg

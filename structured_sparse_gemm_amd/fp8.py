@@ -16,16 +16,17 @@ quantised along the other direction:
 """
 from __future__ import annotations
 
+import ctypes
 from typing import Optional, Tuple
 
 import torch
 
 from . import _abi
-from . import (SsgError, _check, _empty, _float, _lib, _mat, _need, _offsets, _on_device, _out, _raw_stream,
-               _run_with_workspace, _same_device, _stack)
+from . import (_FLOAT, SsgError, _check, _empty, _float, _lib, _mat, _need, _offsets, _on_device, _out, _raw_stream,
+               _same_device, _stack, _workspace_size)
 
 __all__ = ["ssg_fp8_scale_cols", "ssg_fp8_quantize", "ssg_fp8_dequantize", "ssg_mm_fp8", "ssg_mm_fp8_workspace_bytes",
-           "ssg_grouped_mm_fp8", "ssg_grouped_mm_fp8_workspace_bytes",
+           "ssg_grouped_mm_fp8", "ssg_grouped_mm_fp8_workspace_bytes", "ssg_mm_fp8_select_kernel",
            "fp8_quantize", "fp8_dequantize", "mm_fp8", "grouped_mm_fp8"]
 
 FP8 = torch.float8_e4m3fn
@@ -130,22 +131,51 @@ def _grouped_mm_fp8_operands(X, W, wscales, offs, xscales):
     return (x, E, M, X.shape[0], K, *xa, *xs, *_stack(W, "W"), block, *ws, _offsets(offs, E))
 
 
-def ssg_mm_fp8_workspace_bytes(X, W, wscales, xscales=None) -> int:
-    return int(_lib().ssg_mm_fp8_workspace_bytes(*_mm_fp8_operands(X, W, wscales, xscales)))
+def ssg_mm_fp8_workspace_bytes(X, W, wscales, xscales=None, out_dtype: torch.dtype = torch.float32) -> int:
+    x, *ops = _mm_fp8_operands(X, W, wscales, xscales)
+    return int(_lib().ssg_mm_fp8_workspace_bytes(x, _FLOAT.get(out_dtype, -1), *ops))
 
 
-def ssg_grouped_mm_fp8_workspace_bytes(X, W, wscales, offs, xscales=None) -> int:
-    return int(_lib().ssg_grouped_mm_fp8_workspace_bytes(*_grouped_mm_fp8_operands(X, W, wscales, offs, xscales)))
+def ssg_grouped_mm_fp8_workspace_bytes(X, W, wscales, offs, xscales=None, out_dtype: torch.dtype = torch.float32) -> int:
+    x, *ops = _grouped_mm_fp8_operands(X, W, wscales, offs, xscales)
+    return int(_lib().ssg_grouped_mm_fp8_workspace_bytes(x, _FLOAT.get(out_dtype, -1), *ops))
+
+
+def _run(name: str, operands, Y, out, ws, stream) -> None:
+    """_run_with_workspace, whose workspace here depends on the output's type too."""
+    fn, s = getattr(_lib(), name), _raw_stream(Y, stream)
+    x, y, ops = operands[0], _float(Y), operands[1:]
+    if ws is not None:
+        size = _workspace_size(ws, Y.device)
+        _check(fn(x, y, *ops, *out, _on_device(ws, "ws"), size, s), name)
+        return
+    rc = fn(x, y, *ops, *out, None, _abi.SSG_WS_ASK, s)
+    if rc == _abi.SSG_ERR_WORKSPACE:
+        need = int(getattr(_lib(), name + "_workspace_bytes")(x, y, *ops))
+        ws = _empty(need, torch.uint8, Y, stream)
+        rc = fn(x, y, *ops, *out, ws.data_ptr(), need, s)
+    if rc:
+        _check(rc, name)
 
 
 def ssg_mm_fp8(X, W, wscales, Y, xscales=None, ws=None, stream=None) -> None:
     ops = _mm_fp8_operands(X, W, wscales, xscales)
-    _run_with_workspace("ssg_mm_fp8", ops, Y, _out(Y, "Y", X.shape[0], W.shape[0], X), ws, stream)
+    _run("ssg_mm_fp8", ops, Y, _out(Y, "Y", X.shape[0], W.shape[0], X), ws, stream)
 
 
 def ssg_grouped_mm_fp8(X, W, wscales, offs, Y, xscales=None, ws=None, stream=None) -> None:
     ops = _grouped_mm_fp8_operands(X, W, wscales, offs, xscales)
-    _run_with_workspace("ssg_grouped_mm_fp8", ops, Y, _out(Y, "Y", X.shape[0], W.shape[1], X), ws, stream)
+    _run("ssg_grouped_mm_fp8", ops, Y, _out(Y, "Y", X.shape[0], W.shape[1], X), ws, stream)
+
+
+def ssg_mm_fp8_select_kernel(x: torch.dtype, out_dtype: torch.dtype, M: int, N: int, K: int, E: int = 0,
+                             block: int = 128) -> Tuple[str, int, int, int]:
+    """("few" or "tiles", columns and rows of the output a workgroup owns, parts of
+    the contraction) of the kernel that mm_fp8 (E = 0) or grouped_mm_fp8 takes."""
+    k = (ctypes.c_int64 * 4)()
+    dt = _abi.SSG_E4M3 if x == FP8 else _FLOAT.get(x, -1)
+    _check(_lib().ssg_mm_fp8_select_kernel(dt, _FLOAT.get(out_dtype, -1), block, E, M, N, K, k), "ssg_mm_fp8_select_kernel")
+    return ("tiles" if k[0] else "few",) + tuple(k[1:])
 
 
 # ---------------------------------------------------------------- calls that allocate their outputs

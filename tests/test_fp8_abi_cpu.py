@@ -81,6 +81,7 @@ def test_product_refusals(lib):
 def test_workspace(lib):
     f = lib.ssg_mm_fp8_workspace_bytes
     args = (4096, FAKE, 4096, None, 0, 0, FAKE, 4096, 128, FAKE, 32, 1)
+    f = lambda x, *a, f=f: f(x, BF16, *a)                         # noqa: E731
     assert f(BF16, 4096, 1, *args) == 0                          # few rows are rounded on the way
     need = f(BF16, 4096, 2048, *args)
     assert need >= 2048 * 4096 + 2048 * 32 * 4                   # many in a pass of their own
@@ -91,7 +92,7 @@ def test_workspace(lib):
     assert f(E4M3, 4096, 2048, 4096, FAKE, 4096, FAKE, 32, 1, FAKE, 4096, 128, FAKE, 32, 1) == 2048 * 32 * 4
     assert f(I8, 4096, 2048, *args) == 0
     g = lib.ssg_mm_fp8
-    call = (BF16, F32, 4096, 2048, *args, FAKE, 4096)
+    call = (BF16, BF16, 4096, 2048, *args, FAKE, 4096)
     assert g(*call, None, 0, None) == WS and g(*call, FAKE, need - 1, None) == WS
     assert g(*call, ctypes.c_void_p(0x1008), need, None) == WS
     assert g(*call, None, _abi.SSG_WS_ASK, None) == WS
