@@ -17,8 +17,8 @@ from typing import Optional, Tuple
 import torch
 
 from . import _abi
-from . import (SsgError, _check, _empty, _float, _lib, _mat, _need, _on_device, _raw_stream, _same_device,
-               _workspace_size)
+from . import (SsgError, _check, _compiled, _empty, _float, _lib, _mat, _need, _on_device, _raw_stream,
+               _same_device, _workspace_size)
 
 __all__ = ["ssg_route", "ssg_route_backward", "ssg_expert_order", "ssg_expert_order_workspace_bytes",
            "ssg_expert_gather", "ssg_expert_combine", "ssg_expert_combine_backward",
@@ -158,9 +158,14 @@ def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, to
     A weight is scale times the expert's score without the bias, with renorm
     divided by the sum over the chosen ones.  A logit (or bias) of -inf: never
     chosen; slots left over get expert -1 and weight 0."""
+    if stream is None:
+        done = _compiled().route(logits, k, score, bias, groups, top_groups, group_score, renorm, scale)
+        if done is not None:
+            return done
     _need(logits.dim() == 2, "logits must be 2-D", logits)
-    weights = _empty((logits.shape[0], max(k, 0)), torch.float32, logits, stream)
-    experts = _empty((logits.shape[0], max(k, 0)), torch.int32, logits, stream)
+    _need(0 <= k <= logits.shape[1], "k = %d of the experts" % k, logits)
+    weights = _empty((logits.shape[0], k), torch.float32, logits, stream)
+    experts = _empty((logits.shape[0], k), torch.int32, logits, stream)
     ssg_route(logits, weights, experts, score, bias, groups, top_groups, group_score, renorm, scale, stream)
     return weights, experts
 
@@ -168,6 +173,10 @@ def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, to
 def route_backward(dweights, logits, experts, score: str = "softmax", renorm: bool = True, scale: float = 1.0,
                    stream=None) -> torch.Tensor:
     """Gradient of route's weights with respect to the logits, in their type."""
+    if stream is None:
+        done = _compiled().route_backward(dweights, logits, experts, score, renorm, scale)
+        if done is not None:
+            return done
     _need(logits.dim() == 2 and experts.dim() == 2, "logits and experts must be 2-D", logits, experts)
     dlogits = _empty(logits.shape, logits.dtype, logits, stream)
     ssg_route_backward(dweights, logits, experts, dlogits, score, renorm, scale, stream)
@@ -180,9 +189,14 @@ def expert_order(experts, E: int, stream=None) -> Tuple[torch.Tensor, torch.Tens
     offs[e] .. offs[e + 1] - 1 are expert e's, rows[r] is the pair of row r, pos
     the row of a pair; -1 for pairs whose expert is not 0 .. E - 1, and for as
     many rows at the end."""
+    if stream is None:
+        done = _compiled().expert_order(experts, E)
+        if done is not None:
+            return done
     _need(experts.dim() == 2, "experts must be 2-D", experts)
     N, k = experts.shape
-    offs = _empty((max(E, 0) + 1,), torch.int32, experts, stream)
+    _need(0 <= E < 1 << 20, "E = %d" % E, experts)
+    offs = _empty((E + 1,), torch.int32, experts, stream)
     rows, pos = _empty((N * k,), torch.int32, experts, stream), _empty((N, k), torch.int32, experts, stream)
     ssg_expert_order(experts, E, offs, rows, pos, stream=stream)
     return offs, rows, pos
@@ -190,6 +204,10 @@ def expert_order(experts, E: int, stream=None) -> Tuple[torch.Tensor, torch.Tens
 
 def expert_gather(X, pos, rows, stream=None) -> torch.Tensor:
     """[N * k, D]: row pos[n, j] is X[n]; rows of nobody are zeros."""
+    if stream is None:
+        done = _compiled().expert_gather(X, pos, rows)
+        if done is not None:
+            return done
     _need(X.dim() == 2 and pos.dim() == 2, "X and pos must be 2-D", X, pos)
     Y = _empty((pos.numel(), X.shape[1]), X.dtype, X, stream)
     ssg_expert_gather(X, pos, rows, Y, stream)
@@ -199,6 +217,10 @@ def expert_gather(X, pos, rows, stream=None) -> torch.Tensor:
 def expert_combine(Y, pos, weights=None, out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
     """[N, D]: the sum over j of weights[n, j] (None: 1) times Y[pos[n, j]], in Y's
     type or fp32; fp32 sums."""
+    if stream is None:
+        done = _compiled().expert_combine(Y, pos, weights, out_dtype)
+        if done is not None:
+            return done
     _need(Y.dim() == 2 and pos.dim() == 2, "Y and pos must be 2-D", Y, pos)
     O = _empty((pos.shape[0], Y.shape[1]), out_dtype or Y.dtype, Y, stream)
     ssg_expert_combine(Y, pos, O, weights, stream)
@@ -209,6 +231,10 @@ def expert_combine_backward(dO, Y, pos, rows, weights, stream=None) -> Tuple[tor
     """(dY, dweights) of expert_combine(Y, pos, weights) from dO [N, D]: row
     pos[n, j] of dY is weights[n, j] dO[n] (rows of nobody are zeros), dweights[n, j]
     the product of dO[n] and Y[pos[n, j]]."""
+    if stream is None:
+        done = _compiled().expert_combine_backward(dO, Y, pos, rows, weights)
+        if done is not None:
+            return done
     _need(Y.dim() == 2 and weights.dim() == 2, "Y and weights must be 2-D", Y, weights)
     dY, dw = _empty(Y.shape, Y.dtype, Y, stream), _empty(weights.shape, torch.float32, Y, stream)
     ssg_expert_combine_backward(dO, Y, pos, rows, weights, dY, dw, stream)

@@ -22,8 +22,8 @@ from typing import Optional, Tuple
 import torch
 
 from . import _abi
-from . import (_FLOAT, SsgError, _check, _empty, _float, _lib, _mat, _need, _offsets, _on_device, _out, _raw_stream,
-               _same_device, _stack, _workspace_size)
+from . import (_FLOAT, SsgError, _check, _compiled, _empty, _float, _lib, _mat, _need, _offsets, _on_device, _out,
+               _raw_stream, _same_device, _stack, _workspace_size)
 
 __all__ = ["ssg_fp8_scale_cols", "ssg_fp8_quantize", "ssg_fp8_dequantize", "ssg_mm_fp8", "ssg_mm_fp8_workspace_bytes",
            "ssg_grouped_mm_fp8", "ssg_grouped_mm_fp8_workspace_bytes", "ssg_mm_fp8_select_kernel",
@@ -189,6 +189,10 @@ def fp8_quantize(A, block: int = 1, transpose: bool = False, stream=None) -> Tup
     the scales of rows are stored by blocks, as the products read them."""
     if block not in (1, 128):
         raise SsgError(_abi.SSG_ERR_FORMAT, "%r rows to a scale (1 or 128)" % (block,))
+    if stream is None:
+        done = _compiled().fp8_quantize(A, block, transpose)
+        if done is not None:
+            return done
     _need(A.dim() in (2, 3), "A must be 2-D or 3-D", A)
     *lead, R, K = A.shape
     if transpose:
@@ -204,6 +208,10 @@ def fp8_quantize(A, block: int = 1, transpose: bool = False, stream=None) -> Tup
 
 def fp8_dequantize(elems, scales, dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
     """The values of e4m3 elements [R, K] or [E, R, K] with their scales, in `dtype`."""
+    if stream is None:
+        done = _compiled().fp8_dequantize(elems, scales, dtype)
+        if done is not None:
+            return done
     D = _empty(elems.shape, dtype, elems, stream)
     ssg_fp8_dequantize(elems, scales, D, stream)
     return D
@@ -215,6 +223,10 @@ def mm_fp8(X, W, wscales, xscales=None, out_dtype: torch.dtype = torch.float32, 
     bf16, fp32, then rounded as by fp8_quantize.  Returns [N, M] in out_dtype: fp32 is
     the slower one for many rows, its sums being fp32's to the last step; fp16 and
     bf16 take the 8-bit matrix instruction's (see include/ssgemm.h)."""
+    if stream is None:
+        done = _compiled().fp8_product(X, xscales, W, wscales, None, out_dtype)
+        if done is not None:
+            return done
     _need(X.dim() == 2 and W.dim() == 2, "X and W must be 2-D", X, W)
     Y = _empty((X.shape[0], W.shape[0]), out_dtype, X, stream)
     ssg_mm_fp8(X, W, wscales, Y, xscales=xscales, stream=stream)
@@ -225,6 +237,10 @@ def grouped_mm_fp8(X, W, wscales, offs, xscales=None, out_dtype: torch.dtype = t
                    stream=None) -> torch.Tensor:
     """Rows offs[e] .. offs[e + 1] - 1 of X times W[e]^T, W [E, M, K] (see mm_fp8);
     rows of no expert are zero."""
+    if stream is None:
+        done = _compiled().fp8_product(X, xscales, W, wscales, offs, out_dtype)
+        if done is not None:
+            return done
     _need(X.dim() == 2 and W.dim() == 3, "X must be 2-D, W 3-D", X, W)
     Y = _empty((X.shape[0], W.shape[1]), out_dtype, X, stream)
     ssg_grouped_mm_fp8(X, W, wscales, offs, Y, xscales=xscales, stream=stream)
