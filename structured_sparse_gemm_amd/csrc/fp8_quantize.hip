@@ -23,31 +23,67 @@ constexpr int kThreads = 256;
 
 template <int SRC> constexpr int kBytes = SRC == SRC8_F32 ? 4 : 2;
 
-// Elements c .. c + 7 of a row, zeros from n on.
+// Eight neighbouring elements as they lie in memory.
 template <int SRC>
-__device__ __forceinline__ void load8(const uint8_t* row, int64_t c, int64_t n, float (&v)[8]) {
-    if (c + 8 <= n) {
-        if constexpr (SRC == SRC8_F32) {
-            __builtin_memcpy(v, row + c * 4, 32);
-        } else {
-            uint4 d;
-            __builtin_memcpy(&d, row + c * 2, 16);
-            fp8_widen8<SRC>(d, v);
+struct Eight {
+    uint32_t w[2 * kBytes<SRC>];
+    __device__ __forceinline__ float operator[](int e) const {
+        if constexpr (SRC == SRC8_F32) return __uint_as_float(w[e]);
+        else if constexpr (SRC == SRC8_BF16) return __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+        else return f16_bits_to_f32((uint16_t)(e & 1 ? w[e >> 1] >> 16 : w[e >> 1]));
+    }
+    __device__ __forceinline__ float top(float t) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t = fmaxf(t, fabsf((*this)[e]));   // (a NaN does not count)
+        return t;
+    }
+};
+
+// What follows begins from the words as loaded: the compiler keeps neither their
+// widened forms nor both sides of a choice (tiles of 16-bit types: VA registers, VB without).
+template <int SRC, int N>
+__device__ __forceinline__ void pin(Eight<SRC> (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (uint32_t& w : v[i].w) asm volatile("" : "+v"(w));
+}
+
+// Elements c .. c + 7 of the rows r, r + STEP, .., zeros outside the matrix.  Where the
+// columns are whole eights nothing depends on a branch (rows outside are read from
+// inside, and masked), so that all loads are on their way before the first is used:
+// with a branch a row 11008 x 4096 of bf16, transposed, took 78 us instead of QTR.
+template <int SRC, int STEP, int N>
+__device__ __forceinline__ void load_rows(const Fp8Matrix& a, int64_t m, int64_t r, int64_t c, bool eights,
+                                          Eight<SRC> (&v)[N]) {
+    const bool in = r < a.R && c < a.K;
+    const int n = !in ? 0 : (int)min((a.R - r + STEP - 1) / STEP, (int64_t)N);
+    const uint8_t* const p =
+        (const uint8_t*)a.a + (m * a.stridea + (in ? r * a.lda + c : 0)) * kBytes<SRC>;
+    const int64_t step = a.lda * kBytes<SRC> * STEP;
+    if (eights) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) __builtin_memcpy(v[i].w, p + (uint32_t)(i < n ? i : 0) * step, sizeof v[i].w);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            uint32_t keep = i < n ? ~0u : 0u;
+            asm("" : "+v"(keep));
+#pragma unroll
+            for (uint32_t& w : v[i].w) w &= keep;
         }
         return;
     }
+    // (one element at a time: 64 loads on their way would take twice the registers)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        v[e] = 0.0f;
-        if (c + e >= n) continue;
-        if constexpr (SRC == SRC8_F32) {
-            __builtin_memcpy(&v[e], row + (c + e) * 4, 4);
-        } else {
-            uint16_t b;
-            __builtin_memcpy(&b, row + (c + e) * 2, 2);
-            v[e] = SRC == SRC8_F16 ? f16_bits_to_f32(b) : bf16_bits_to_f32(b);
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint32_t bits = 0;
+            if (i < n && c + e < a.K) __builtin_memcpy(&bits, p + i * step + e * kBytes<SRC>, kBytes<SRC>);
+            asm volatile("" : "+v"(bits));
+            if constexpr (SRC == SRC8_F32) v[i].w[e] = bits;
+            else v[i].w[e >> 1] = e & 1 ? v[i].w[e >> 1] | bits << 16 : bits;
         }
-    }
 }
 
 // n of the bytes of v (element order) to any address.
@@ -62,86 +98,64 @@ __device__ __forceinline__ void store8(uint8_t* at, int64_t n, uint2 v) {
         if (e < n) at[e] = (uint8_t)(w >> (8 * e));
 }
 
-__device__ __forceinline__ float top8(const float (&v)[8], float top) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));   // (a NaN does not count)
-    return top;
-}
-
-// Rows as they are: workgroup (16 rows, one block).
-template <int SRC>
+// Rows as they are: workgroup (16 PER rows, one block).
+template <int SRC, int PER>
 __global__ void __launch_bounds__(kThreads) k_quantize_rows(Fp8Matrix a, uint32_t first, uint32_t nb, uint32_t rg) {
     const uint32_t id = first + blockIdx.x, m = id / (nb * rg), in = id - m * nb * rg, g = in / nb, b = in - g * nb;
-    const int64_t r = (int64_t)g * 16 + threadIdx.x / 16, c = (int64_t)b * kFp8Block + threadIdx.x % 16 * 8;
-    const int64_t rr = r < a.R ? r : a.R - 1;
-    const uint8_t* row = (const uint8_t*)a.a + (m * a.stridea + rr * a.lda) * kBytes<SRC>;
-    float v[8];
-    load8<SRC>(row, c, a.K, v);
-    const float s = fp8_scale(lanes_max<16>(top8(v, 0.0f)));
-    const uint2 q = fp8_pack8(v, fp8_recip(s));
-    if (r >= a.R) return;
-    if (c < a.K) store8(a.e + m * a.stridee + r * a.lde + c, a.K - c, q);
-    if (threadIdx.x % 16 == 0) a.s[m * a.mat + r * a.row + b * a.blk] = s;
+    const int64_t r0 = (int64_t)g * 16 * PER + threadIdx.x / 16, c = (int64_t)b * kFp8Block + threadIdx.x % 16 * 8;
+    Eight<SRC> v[PER];
+    load_rows<SRC, 16>(a, m, r0, c, (int64_t)(b + 1) * kFp8Block <= a.K || a.K % 8 == 0, v);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int64_t r = r0 + 16 * i;
+        const float s = fp8_scale(lanes_max<16>(v[i].top(0.0f)));
+        float u[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = v[i][e];
+        const uint2 q = fp8_pack8(u, fp8_recip(s));
+        if (r >= a.R) continue;
+        if (c < a.K) store8(a.e + m * a.stridee + r * a.lde + c, a.K - c, q);
+        if (threadIdx.x % 16 == 0) a.s[m * a.mat + r * a.row + b * a.blk] = s;
+    }
 }
 
 // 128 x 128 tiles.  Thread (c = t % 16, g = t / 16): columns 8 c .. + 7 of rows 8 g .. + 7.
+//
+// A tile that turns: row k of the transpose is 16 pieces of 8 bytes, piece g at place
+// g ^ (k / 16); rows are 144 bytes apart.  So the 64 writes of a wave (16 rows 8 apart,
+// 4 pieces) fall on 32 banks, four each, as few as 512 bytes take, and 16 bytes that are
+// read (two pieces) stay together, at most changed about.
 template <int SRC, bool WIDE, bool TR>
 __global__ void __launch_bounds__(kThreads) k_quantize_tiles(Fp8Matrix a, uint32_t first, uint32_t nb, uint32_t nr) {
-    __shared__ __attribute__((aligned(16))) float top_of[TR && !WIDE ? 16 : 1][kFp8Block];
-    __shared__ __attribute__((aligned(16))) uint8_t turn[TR ? kFp8Block * 144 : 16];   // rows of 144 bytes: over all banks
+    static_assert(TR || WIDE, "rows as they are have their own kernel");
+    __shared__ __attribute__((aligned(16))) float top_of[WIDE ? 1 : 16][kFp8Block];
+    __shared__ __attribute__((aligned(16))) uint8_t turn[TR ? kFp8Block * 144 : 16];
     const uint32_t id = first + blockIdx.x, m = id / (nb * nr), in = id - m * nb * nr, rb = in / nb, cb = in - rb * nb;
     const int t = threadIdx.x, c = t % 16, g = t / 16;
     const int64_t r0 = (int64_t)rb * kFp8Block, c0 = (int64_t)cb * kFp8Block;
-    const uint8_t* const base = (const uint8_t*)a.a + m * a.stridea * kBytes<SRC>;
-    float v[8][8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t r = r0 + 8 * g + i;
-        if (r < a.R) {
-            load8<SRC>(base + r * a.lda * kBytes<SRC>, c0 + 8 * c, a.K, v[i]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
-        }
-    }
+    Eight<SRC> v[8];
+    load_rows<SRC, 1>(a, m, r0 + 8 * g, c0 + 8 * c, c0 + kFp8Block <= a.K || a.K % 8 == 0, v);
+    pin(v);
     float* const sc = a.s + m * a.mat;
+    float s8[WIDE ? 1 : 8];            // the scales of this thread's columns
     if constexpr (WIDE) {
         float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = top8(v[i], top);
+        for (int i = 0; i < 8; ++i) top = v[i].top(top);
         top = lanes_max<64>(top);
         if ((t & 63) == 0) top_of[0][t >> 6] = top;
         __syncthreads();
-        top = fmaxf(fmaxf(top_of[0][0], top_of[0][1]), fmaxf(top_of[0][2], top_of[0][3]));
-        const float s = fp8_scale(top);
-        const Fp8Recip rc = fp8_recip(s);
-        if (t == 0) sc[(TR ? cb : rb) * a.row + (TR ? rb : cb) * a.blk] = s;
-        if constexpr (!TR) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t r = r0 + 8 * g + i, at = c0 + 8 * c;
-                const uint2 q = fp8_pack8(v[i], rc);
-                if (r < a.R && at < a.K) store8(a.e + m * a.stridee + r * a.lde + at, a.K - at, q);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float u[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] = v[i][e];
-                *reinterpret_cast<uint2*>(turn + (8 * c + e) * 144 + 8 * g) = fp8_pack8(u, rc);
-            }
-        }
+        s8[0] = fp8_scale(fmaxf(fmaxf(top_of[0][0], top_of[0][1]), fmaxf(top_of[0][2], top_of[0][3])));
+        if (t == 0) sc[(TR ? cb : rb) * a.row + (TR ? rb : cb) * a.blk] = s8[0];
     } else {
-        static_assert(TR || WIDE, "rows as they are have their own kernel");
-        // a scale for each column of the tile
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             float top = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i][e]));
-            top_of[g][8 * c + e] = top;
+            s8[e] = top;
         }
+        __builtin_memcpy(&top_of[g][8 * c], s8, sizeof s8);
         __syncthreads();
         if (t < kFp8Block) {
             float top = 0.0f;
@@ -152,22 +166,38 @@ __global__ void __launch_bounds__(kThreads) k_quantize_tiles(Fp8Matrix a, uint32
             if (c0 + t < a.K) sc[(c0 + t) * a.row + rb * a.blk] = s;
         }
         __syncthreads();
+        __builtin_memcpy(s8, &top_of[0][8 * c], sizeof s8);
+    }
+    pin(v);
+    if constexpr (!TR) {
+        const Fp8Recip rc = fp8_recip(s8[0]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t r = r0 + 8 * g + i, at = c0 + 8 * c;
+            float u[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] = v[i][e];
+            const uint2 q = fp8_pack8(u, rc);
+            if (r < a.R && at < a.K) store8(a.e + m * a.stridee + r * a.lde + at, a.K - at, q);
+        }
+    } else {
+        uint8_t* const put = turn + 8 * c * 144 + 8 * (g ^ (c >> 1));
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             float u[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) u[i] = v[i][e];
-            *reinterpret_cast<uint2*>(turn + (8 * c + e) * 144 + 8 * g) = fp8_pack8(u, fp8_recip(top_of[0][8 * c + e]));
+            *reinterpret_cast<uint2*>(put + e * 144) = fp8_pack8(u, fp8_recip(s8[WIDE ? 0 : e]));
         }
-    }
-    if constexpr (TR) {
         __syncthreads();
         // row c0 + k of the output: bytes r0 .. r0 + 127, 16 a thread
-        for (int u = t; u < kFp8Block * 8; u += kThreads) {
-            const int k = u >> 3;
-            const int64_t at = r0 + (u & 7) * 16, n = a.R - at;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = i * 32 + (t >> 3), j = t & 7, x = k >> 4;
+            const int64_t at = r0 + j * 16, n = a.R - at;
             if (c0 + k >= a.K || n <= 0) continue;
-            uint4 d = *reinterpret_cast<const uint4*>(turn + k * 144 + (u & 7) * 16);
+            uint4 d = *reinterpret_cast<const uint4*>(turn + k * 144 + (j ^ (x >> 1)) * 16);
+            if (x & 1) d = make_uint4(d.z, d.w, d.x, d.y);
             uint8_t* const dst = a.e + m * a.stridee + (c0 + k) * a.lde + at;
             if (n >= 16) {
                 __builtin_memcpy(dst, &d, 16);
@@ -249,14 +279,21 @@ hipError_t by_slabs(int64_t total, F&& f) {
     return hipSuccess;
 }
 
+// Rows as they are: 16 a workgroup up to so many workgroups, which a chip of 256 CUs
+// holds at once (QFEW), 64 from there on.
+constexpr int64_t kFewGroups = 2048;
+
 template <int SRC>
 hipError_t quantize(const Fp8Matrix& a, hipStream_t s) {
     const int64_t nb = (a.K + kFp8Block - 1) / kFp8Block;
-    const int64_t nr = a.block == 1 && !a.transpose ? (a.R + 15) / 16 : (a.R + kFp8Block - 1) / kFp8Block;
+    const bool rows = a.block == 1 && !a.transpose;
+    const bool few = rows && a.mats * nb * ((a.R + 15) / 16) <= kFewGroups;
+    const int64_t per = few ? 16 : rows ? 64 : kFp8Block, nr = (a.R + per - 1) / per;
     if (a.mats * nb * nr >= (int64_t)1 << 32) return hipErrorInvalidValue;
     return by_slabs(a.mats * nb * nr, [&](uint32_t i, dim3 grid) {
         const uint32_t n = (uint32_t)nb, r = (uint32_t)nr;
-        if (a.block == 1 && !a.transpose) hipLaunchKernelGGL(k_quantize_rows<SRC>, grid, dim3(kThreads), 0, s, a, i, n, r);
+        if (few) hipLaunchKernelGGL((k_quantize_rows<SRC, 1>), grid, dim3(kThreads), 0, s, a, i, n, r);
+        else if (rows) hipLaunchKernelGGL((k_quantize_rows<SRC, 4>), grid, dim3(kThreads), 0, s, a, i, n, r);
         else if (a.block == 1) hipLaunchKernelGGL((k_quantize_tiles<SRC, false, true>), grid, dim3(kThreads), 0, s, a, i, n, r);
         else if (a.transpose) hipLaunchKernelGGL((k_quantize_tiles<SRC, true, true>), grid, dim3(kThreads), 0, s, a, i, n, r);
         else hipLaunchKernelGGL((k_quantize_tiles<SRC, true, false>), grid, dim3(kThreads), 0, s, a, i, n, r);
