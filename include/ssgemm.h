@@ -731,7 +731,7 @@ int ssg_route_backward(int dt, int64_t N, int64_t E, const float* dweights, int6
  *   offs [E + 1]  rows offs[e] .. offs[e + 1] - 1 are expert e's
  *   rows [N * k]  the pair of each row, -1 from row offs[E] on
  *   pos  [N, k]   the row of each pair, -1 for an expert outside 0 .. E - 1
- * rows and pos are contiguous.  The workspace (0 bytes for up to 8192 pairs) holds
+ * rows and pos are contiguous.  The workspace (0 bytes for up to 4096 pairs) holds
  * the counts of parts of the pairs; SSG_WS_ASK as for the products.
  * ssg_expert_gather: Y[pos[n, j]] = X[n]; rows r of Y [N * k, D] with rows[r] = -1
  * get zeros.

@@ -7,6 +7,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace ssg {
 
 // Lane i's value from lane i ^ 1, i ^ 2, 7 - i of 8, 15 - i of 16.
@@ -23,6 +25,37 @@ __device__ __forceinline__ void lane_pair(uint32_t v, uint32_t* a, uint32_t* b) 
                         : __builtin_amdgcn_permlane16_swap(v, v, false, false);
     *a = r[0];
     *b = r[1];
+}
+
+// The value of the lane that step S = 0 .. 5 of a reduction over 2^(S + 1) neighbouring
+// lanes pairs this one with (any lane of the other half, once both halves agree).
+template <int S, typename T>
+__device__ __forceinline__ T lane_partner(T v) {
+    union U { T t; uint32_t w[sizeof(T) / 4]; } u;
+    u.t = v;
+#pragma unroll
+    for (uint32_t& w : u.w) {
+        if constexpr (S < 4) {
+            w = lane_swap16<S>(w);
+        } else {
+            uint32_t a, b;
+            lane_pair<S == 5>(w, &a, &b);
+            w ^= a ^ b;
+        }
+    }
+    return u.t;
+}
+// f(step) for the steps of a reduction over 2^n neighbouring lanes (n the same in all lanes).
+template <int MAX, typename F>
+__device__ __forceinline__ void lane_steps(int n, F&& f) {
+    if (n > 0) f(std::integral_constant<int, 0>{});
+    if (n > 1) f(std::integral_constant<int, 1>{});
+    if (n > 2) f(std::integral_constant<int, 2>{});
+    if (n > 3) f(std::integral_constant<int, 3>{});
+    if constexpr (MAX > 4) {
+        if (n > 4) f(std::integral_constant<int, 4>{});
+        if (n > 5) f(std::integral_constant<int, 5>{});
+    }
 }
 
 template <typename T> struct LaneBits;

@@ -16,7 +16,9 @@
 // unsigned key of that width: 0 stands for "never", so removing a chosen expert
 // is storing 0.
 //
-// Bound by instructions, not by memory (8192 x 256 fp32 logits are 8 MB, 2 us).
+// Bound by instructions, not by memory: 8192 x 256 fp32 logits are 8 MB, 2 us, and
+// take 14.5 us with sigmoids, a bias, 4 of 8 groups and 8 choices (a third of it the
+// scores in 64 bits), 8.4 us for 8 choices by softmax; one token 5.6 and 3.6 us.
 // L lanes share a token, V neighbouring experts a lane; a group has a power of
 // two of the lanes to itself, so that its best are found by exchanges among
 // them.  Every choice is a maximum over the lane's keys, one over the lanes
@@ -37,6 +39,25 @@ __device__ __forceinline__ float load_float(const void* p, int dt, int64_t at) {
     if (dt == FT_F32) return reinterpret_cast<const float*>(p)[at];
     const uint16_t b = reinterpret_cast<const uint16_t*>(p)[at];
     return dt == FT_F16 ? f16_bits_to_f32(b) : bf16_bits_to_f32(b);
+}
+
+// p[at + first + v] for v < count, `other` beyond (p[at] is there): no load waits for
+// another, nor for a branch of its own.
+template <int V>
+__device__ __forceinline__ void load_floats(const void* p, int dt, int64_t at, int first, int count, float other,
+                                            float (&x)[V]) {
+    if (dt == FT_F32) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = reinterpret_cast<const float*>(p)[at + (v < count ? first + v : 0)];
+    } else {
+        uint16_t b[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) b[v] = reinterpret_cast<const uint16_t*>(p)[at + (v < count ? first + v : 0)];
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = dt == FT_F16 ? f16_bits_to_f32(b[v]) : bf16_bits_to_f32(b[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = v < count ? x[v] : other;
 }
 
 __device__ __forceinline__ void store_float(void* p, int dt, int64_t at, float v) {
@@ -61,6 +82,20 @@ __device__ __forceinline__ uint64_t key64(double v) {
     return v == -__builtin_inf() ? 0ull : k;
 }
 
+// exp in 64 bits, off by 2^-51: x = n log 2 + r, the series of exp(r) for |r| <= log(2) / 2
+// up to r^12 / 12! (the next term is 2^-52 of it).
+__device__ __forceinline__ double exp64(double x) {
+    const double n = __builtin_rint(fmin(fmax(x, -2000.0), 2000.0) * 0x1.71547652b82fep+0);
+    const double r = fma(n, -0x1.abc9e3b39803fp-56, fma(n, -0x1.62e42fefa39efp-1, x));
+    double p = 1.0 / 479001600;
+    constexpr double c[12] = {1.0 / 39916800, 1.0 / 3628800, 1.0 / 362880, 1.0 / 40320, 1.0 / 5040, 1.0 / 720,
+                              1.0 / 120,      1.0 / 24,      1.0 / 6,      1.0 / 2,     1.0,        1.0};
+#pragma unroll
+    for (double k : c) p = fma(p, r, k);
+    p = ldexp(p, (int)n);
+    return x > 2000.0 ? __builtin_inf() : x < -2000.0 ? 0.0 : p;   // (NaN stays NaN by r)
+}
+
 // Weights of the chosen logits x (lane j of L has slot j; `there`: slot filled):
 // the scores, or their shares of the sum.  The shares are taken relative to the
 // largest, so that they are numbers also where every score is below fp32's range.
@@ -81,6 +116,24 @@ __device__ __forceinline__ float chosen_weight(const RouteArgs& a, float x, bool
     return there ? s : 0.0f;
 }
 
+// How many of the groups (of 2^lg lanes; L lanes a token) come before this lane's.
+template <int L, typename Key>
+__device__ __forceinline__ int group_rank(Key key, int group, int groups, int seg, int lg) {
+    int rank = 0;
+    for (int h = 0; h < groups; ++h) {
+        union { Key k; uint32_t w[sizeof(Key) / 4]; } o;
+        o.k = key;
+#pragma unroll
+        for (uint32_t& w : o.w) {
+            // (the lane is the same for the whole wave where it has one token)
+            if constexpr (L == 64) w = (uint32_t)__builtin_amdgcn_readlane((int)w, h << lg);
+            else w = (uint32_t)__shfl((int)w, seg * L + (h << lg));
+        }
+        rank += o.k > key || (o.k == key && h < group);
+    }
+    return rank;
+}
+
 template <int L, int V, bool WIDE>
 __global__ void __launch_bounds__(kThreads) k_route(RouteArgs a, int64_t n0, int S, int lg_shift) {
     using Key = typename std::conditional<WIDE, uint64_t, uint32_t>::type;
@@ -92,9 +145,10 @@ __global__ void __launch_bounds__(kThreads) k_route(RouteArgs a, int64_t n0, int
     const int first = group * S + base;
     const int count = group < a.groups ? (S - base < V ? (S - base > 0 ? S - base : 0) : V) : 0;
 
-    float x[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = v < count ? load_float(a.logits, a.dt, nr * a.ldl + first + v) : neg_inf();
+    float x[V], b[WIDE ? V : 1];
+    load_floats<V>(a.logits, a.dt, nr * a.ldl, first, count, neg_inf(), x);
+    if constexpr (WIDE)
+        if (a.bias) load_floats<V>(a.bias, FT_F32, 0, first, count, neg_inf(), b);
 
     float row_max = 0.0f, row_sum = 1.0f;
     double sum64 = 1.0;
@@ -116,12 +170,12 @@ __global__ void __launch_bounds__(kThreads) k_route(RouteArgs a, int64_t n0, int
         double s[V];
         if (a.sigmoid) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) s[v] = 1.0 / (1.0 + exp(-(double)x[v]));
+            for (int v = 0; v < V; ++v) s[v] = 1.0 / (1.0 + exp64(-(double)x[v]));
         } else {
             sum64 = 0.0;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                s[v] = exp((double)x[v] - (double)row_max);
+                s[v] = exp64((double)x[v] - (double)row_max);
                 sum64 += s[v];
             }
             sum64 = lanes_sum<L>(sum64);
@@ -133,8 +187,7 @@ __global__ void __launch_bounds__(kThreads) k_route(RouteArgs a, int64_t n0, int
         for (int v = 0; v < V; ++v) {
             double c = x[v];
             if (a.bias) {
-                const float b = v < count ? a.bias[first + v] : neg_inf();
-                c = x[v] == neg_inf() || b == neg_inf() ? (double)neg_inf() : s[v] + (double)b;
+                c = x[v] == neg_inf() || b[v] == neg_inf() ? (double)neg_inf() : s[v] + (double)b[v];
             }
             key[v] = key64(c);
             // what the group's score is taken of
@@ -150,19 +203,17 @@ __global__ void __launch_bounds__(kThreads) k_route(RouteArgs a, int64_t n0, int
                 m2 = fmax(m2, fmin(m1, s[v]));
                 m1 = fmax(m1, s[v]);
             }
-            for (int d = 1; d < (1 << lg_shift); d <<= 1) {
-                const double o1 = __shfl_xor(m1, d), o2 = __shfl_xor(m2, d);
-                nan |= __shfl_xor((int)nan, d) != 0;
+            uint32_t any_nan = nan;
+            lane_steps<L == 64 ? 6 : 4>(lg_shift, [&](auto step) {
+                constexpr int ST = decltype(step)::value;
+                const double o1 = lane_partner<ST>(m1), o2 = lane_partner<ST>(m2);
+                any_nan |= lane_partner<ST>(any_nan);
                 m2 = fmax(fmin(m1, o1), fmax(m2, o2));
                 m1 = fmax(m1, o1);
-            }
+            });
             if (a.top2 && m2 != -__builtin_inf()) m1 += m2;
-            const uint64_t gk = nan ? ~0ull : group < a.groups ? key64(m1) : 0;
-            int rank = 0;
-            for (int h = 0; h < a.groups; ++h) {
-                const uint64_t o = __shfl(gk, seg * L + (h << lg_shift));
-                rank += o > gk || (o == gk && h < group);
-            }
+            const uint64_t gk = any_nan ? ~0ull : group < a.groups ? key64(m1) : 0;
+            const int rank = group_rank<L>(gk, group, a.groups, seg, lg_shift);
             if (rank >= a.top_groups) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) key[v] = 0;
@@ -175,15 +226,8 @@ __global__ void __launch_bounds__(kThreads) k_route(RouteArgs a, int64_t n0, int
             uint32_t gk = 0;
 #pragma unroll
             for (int v = 0; v < V; ++v) gk = gk > key[v] ? gk : key[v];
-            for (int d = 1; d < (1 << lg_shift); d <<= 1) {
-                const uint32_t o = (uint32_t)__shfl_xor((int)gk, d);
-                gk = gk > o ? gk : o;
-            }
-            int rank = 0;
-            for (int h = 0; h < a.groups; ++h) {
-                const uint32_t o = (uint32_t)__shfl((int)gk, seg * L + (h << lg_shift));
-                rank += o > gk || (o == gk && h < group);
-            }
+            lane_steps<L == 64 ? 6 : 4>(lg_shift, [&](auto step) { gk = max(gk, lane_partner<decltype(step)::value>(gk)); });
+            const int rank = group_rank<L>(gk, group, a.groups, seg, lg_shift);
             if (rank >= a.top_groups) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) key[v] = 0;
@@ -194,22 +238,73 @@ __global__ void __launch_bounds__(kThreads) k_route(RouteArgs a, int64_t n0, int
     int32_t* const out = res[wave * T + seg];
     out[l] = -1;
     __syncthreads();
-    for (int j = 0; j < a.k; ++j) {
-        Key best = key[0];
-        int at = 0;
+    if constexpr (WIDE) {
+        // The upper words decide nearly always: a maximum of 32 bits over the lanes, and
+        // the lower words only where two keys share it in a token.
+        uint32_t hi[V], lo[V];
 #pragma unroll
-        for (int v = 1; v < V; ++v) {
-            if (key[v] > best) {
-                best = key[v];
-                at = v;
+        for (int v = 0; v < V; ++v) {
+            hi[v] = (uint32_t)(key[v] >> 32);
+            lo[v] = (uint32_t)key[v];
+        }
+        constexpr uint64_t kOnes = L == 64 ? 1 : 0x0001000100010001ull;    // a token's lowest lane
+        for (int j = 0; j < a.k; ++j) {
+            uint32_t best = hi[0];
+#pragma unroll
+            for (int v = 1; v < V; ++v) best = max(best, hi[v]);
+            const uint32_t top = lanes_max<L>(best);
+            uint64_t seen = 0, twice = 0;              // lanes with a key that has it, or two
+            int at = 0;
+#pragma unroll
+            for (int v = V - 1; v >= 0; --v) {
+                const bool has = hi[v] == top;
+                const uint64_t lanes = __ballot(has);
+                twice |= seen & lanes;
+                seen |= lanes;
+                at = has ? v : at;
+            }
+            twice |= seen & (seen - kOnes);            // (every token has one: nothing is borrowed)
+            if (twice == 0) {
+                if (best == top && top != 0) out[j] = first + at;
+#pragma unroll
+                for (int v = 0; v < V; ++v) hi[v] = hi[v] == top ? 0u : hi[v];
+                continue;
+            }
+            uint32_t low = 0;
+            at = 0;
+#pragma unroll
+            for (int v = V - 1; v >= 0; --v) {
+                if (hi[v] == top && lo[v] >= low) {
+                    low = lo[v];
+                    at = v;
+                }
+            }
+            const uint32_t top_low = lanes_max<L>(low);
+            const uint64_t hit = __ballot(best == top && low == top_low) >> (seg * L);
+            if (l == __builtin_ctzll(hit) && top != 0) {
+                out[j] = first + at;
+#pragma unroll
+                for (int v = 0; v < V; ++v) hi[v] = v == at ? 0u : hi[v];
             }
         }
-        const Key top = lanes_max<L>(best);
-        const uint64_t hit = __ballot(best == top) >> (seg * L);
-        if (top != 0 && l == __builtin_ctzll(hit)) {
-            out[j] = first + at;
+    } else {
+        for (int j = 0; j < a.k; ++j) {
+            uint32_t best = key[0];
+            int at = 0;
 #pragma unroll
-            for (int v = 0; v < V; ++v) key[v] = v == at ? (Key)0 : key[v];
+            for (int v = 1; v < V; ++v) {
+                if (key[v] > best) {
+                    best = key[v];
+                    at = v;
+                }
+            }
+            const uint32_t top = lanes_max<L>(best);
+            const uint64_t hit = __ballot(best == top) >> (seg * L);
+            if (top != 0 && l == __builtin_ctzll(hit)) {
+                out[j] = first + at;
+#pragma unroll
+                for (int v = 0; v < V; ++v) key[v] = v == at ? 0u : key[v];
+            }
         }
     }
     __syncthreads();
@@ -303,7 +398,9 @@ int log2_up(int v) {
 hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
     const bool wide = a.bias || (a.groups > 1 && a.top2);
     const int S = a.E / a.groups, gb = log2_up(a.groups);
-    // 16 lanes a token where its experts fit 8 a lane: a choice then serves four tokens
+    // 16 lanes a token where its experts fit 8 a lane: a choice then serves four tokens.
+    // (With 16 a lane one token takes twice the time, 12 us for 6, and 32768 tokens of
+    // 256 experts no less: 44 us for 45.)
     const int per16 = gb <= 4 ? (S + (16 >> gb) - 1) / (16 >> gb) : 99;
     if (per16 <= 8 && a.k <= 16) {
         const int sh = 4 - gb;

@@ -55,10 +55,10 @@ def test_order_refusals(lib):
     assert call(e=None) == NULL and call(offs=None) == NULL and call(rows=None) == NULL and call(pos=None) == NULL
     assert call(lde=1) == STRIDE
     f = lib.ssg_expert_order_workspace_bytes
-    assert f(8192, 1, 64) == 0 and f(-1, 2, 8) == 0 and f(4, 2, 2000) == 0
-    need = f(8193, 1, 64)
-    assert need == 3 * 64 * 4
-    big = dict(N=8193, k=1, E=64, lde=1)
+    assert f(4096, 1, 64) == 0 and f(-1, 2, 8) == 0 and f(4, 2, 2000) == 0
+    need = f(4097, 1, 64)
+    assert need == 5 * 64 * 4
+    big = dict(N=4097, k=1, E=64, lde=1)
     assert call(**big) == WS and call(**big, ws=FAKE, size=need - 1) == WS
     assert call(**big, ws=ctypes.c_void_p(0x1002), size=need) == WS
     assert call(**big, size=_abi.SSG_WS_ASK) == WS

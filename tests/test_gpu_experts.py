@@ -182,7 +182,7 @@ def test_route_gradient_of_other_experts():
 # ---------------------------------------------------------------- the order
 
 @pytest.mark.parametrize("E", [1, 2, 7, 64, 256, 1000, 1024])
-@pytest.mark.parametrize("N,k", [(1, 1), (3, 5), (64, 1), (65, 1), (16, 4), (2048, 4), (8193, 1), (3001, 6), (50000, 3)])
+@pytest.mark.parametrize("N,k", [(1, 1), (3, 5), (64, 1), (65, 1), (16, 4), (2048, 4), (4097, 1), (8193, 1), (3001, 6), (50000, 3), (150001, 2)])
 def test_order(E, N, k):
     g = np.random.default_rng(E + N)
     e = np.minimum(np.floor(E * g.random((N, k)) ** 2), E - 1).astype(np.int32)
