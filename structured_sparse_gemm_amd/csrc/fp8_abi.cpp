@@ -157,10 +157,9 @@ constexpr double kStart = 3.5, kBytesPerUs = 4.4e6;
 // Tiles: a block of the contraction takes `one` us where a CU has one workgroup,
 // `two` where it has two, for 8-bit and for exact products.
 constexpr double kPairOne[2] = {0.75, 1.1}, kPairTwo[2] = {1.15, 2.05};   // 128 x 128, two on a CU
-constexpr double kDeep = 0.62;                                            // 128 x 128, four blocks in LDS
-// 256 x 256 (or 256 x 128, for a scale a weight row): a whole round, and a last
-// one of tiles as they are, cut in two and in four.
-constexpr double kLarge[2][3] = {{1.8, 1.27, 0.65}, {1.35, 0.75, 0.75}};
+constexpr double kDeep[2] = {0.62, 0.75};                                 // 128 x 128, four blocks in LDS: w_rows
+// 256 x 256: a whole round, and a last one of tiles as they are, cut in two and in four.
+constexpr double kLarge[3] = {1.8, 1.27, 0.65};
 
 Plan plan(const Call& c) {
     const ssg::MmArgs& m = c.a.m;
@@ -196,8 +195,8 @@ Plan plan(const Call& c) {
         }
     }
     const bool ex = c.a.exact;
-    for (int size = ex ? 1 : 0; size <= (ex || c.a.w_rows ? 1 : 2); ++size) {
-        const int tp = size == 0 && !c.a.w_rows ? 256 : 128, tq = size == 0 ? 256 : 128;
+    for (int size = ex || c.a.w_rows ? 1 : 0; size <= (ex ? 1 : 2); ++size) {
+        const int tp = size == 0 ? 256 : 128, tq = tp;
         const double tiles = row_tiles(tp) * ceil_div(m.Q, tq);
         for (int splits = 1; splits <= 8; splits *= 2) {
             if (splits > 1 && (size == 0 || nb < 2 * splits)) break;
@@ -205,7 +204,7 @@ Plan plan(const Call& c) {
             const double n = tiles * splits, len = std::ceil((double)nb / splits);
             double block;
             if (size == 0) {
-                const double* l = kLarge[c.a.w_rows];
+                const double* const l = kLarge;
                 const double whole = std::floor(n / kCUs), rest = n - whole * kCUs;
                 block = whole * l[0] + (rest <= 0           ? 0
                                         : rest <= kCUs / 4 ? l[2]
@@ -215,7 +214,7 @@ Plan plan(const Call& c) {
                 const double r = std::ceil(n / kCUs), pairs = std::floor(r / 2);
                 block = pairs * kPairTwo[ex] + (r - 2 * pairs) * kPairOne[ex];
             } else {
-                block = std::ceil(n / kCUs) * kDeep;
+                block = std::ceil(n / kCUs) * kDeep[c.a.w_rows];
             }
             double us = std::max(floor_us, kStart + 0.5 + block * len);
             if (splits > 1) us += 4 + (double)splits * m.P * m.Q * 8 / 3e6;
@@ -420,7 +419,7 @@ int ssg_mm_fp8_select_kernel(int x, int y, int wblock, int64_t E, int64_t M, int
     const Plan q = plan(c);
     kernel[0] = q.few ? 0 : 1;
     kernel[1] = q.few ? 16 * q.rt : q.size == 0 ? 256 : 128;
-    kernel[2] = q.few ? 16 * q.nt : q.size == 0 && !c.a.w_rows ? 256 : 128;
+    kernel[2] = q.few ? 16 * q.nt : q.size == 0 ? 256 : 128;
     kernel[3] = q.splits;
     return SSG_OK;
 }

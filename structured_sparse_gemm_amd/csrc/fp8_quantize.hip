@@ -2,10 +2,12 @@
 // elements of a row, or each 128 rows by 128 elements, as they are or transposed;
 // and back.  (The rounding: fp8.hpp.)
 //
-// Bound by memory: a 16-bit element is read once and a byte written.
+// Bound by memory: a 16-bit element is read once and a byte written.  11008 x 4096 of
+// bf16 (135 MB) take 23 to 26 us in all four forms, 16384 x 8192 80 us: 5.0 to 5.7 TB/s,
+// the rate of a copy; 1024 x 4096 4.7 us, one row 2.4 us.
 // * Rows as they are: 16 lanes share a block, 8 elements each; the maximum takes
-//   four exchanges between lanes.  A workgroup has 16 rows of a block, so that it
-//   writes 16 neighbouring scales of a block-major array.
+//   four exchanges between lanes.  A workgroup has 16 or 64 rows of a block, so that
+//   it writes as many neighbouring scales of a block-major array.
 // * 128 x 128 tiles, where the scale is shared by rows or the output is
 //   transposed: a thread has 8 rows of 8 columns in registers, so every byte is
 //   read once whatever the scale covers.  A transposed tile turns in LDS (8 bytes,
@@ -40,7 +42,7 @@ struct Eight {
 };
 
 // What follows begins from the words as loaded: the compiler keeps neither their
-// widened forms nor both sides of a choice (tiles of 16-bit types: VA registers, VB without).
+// widened forms nor both sides of a choice (tiles of 16-bit types: 74 registers, 96 without).
 template <int SRC, int N>
 __device__ __forceinline__ void pin(Eight<SRC> (&v)[N]) {
 #pragma unroll
@@ -52,7 +54,8 @@ __device__ __forceinline__ void pin(Eight<SRC> (&v)[N]) {
 // Elements c .. c + 7 of the rows r, r + STEP, .., zeros outside the matrix.  Where the
 // columns are whole eights nothing depends on a branch (rows outside are read from
 // inside, and masked), so that all loads are on their way before the first is used:
-// with a branch a row 11008 x 4096 of bf16, transposed, took 78 us instead of QTR.
+// with a branch a row 11008 x 4096 of bf16, transposed, took 48 us instead of 40 (and
+// takes 23 since the rounding is cheap).
 template <int SRC, int STEP, int N>
 __device__ __forceinline__ void load_rows(const Fp8Matrix& a, int64_t m, int64_t r, int64_t c, bool eights,
                                           Eight<SRC> (&v)[N]) {
@@ -279,8 +282,9 @@ hipError_t by_slabs(int64_t total, F&& f) {
     return hipSuccess;
 }
 
-// Rows as they are: 16 a workgroup up to so many workgroups, which a chip of 256 CUs
-// holds at once (QFEW), 64 from there on.
+// Rows as they are: 16 a workgroup up to so many workgroups, which the chip holds at
+// once, 64 from there on.  bf16, 16 and 64: 512 x 4096 3.5 and 3.9 us, 1024 x 4096 4.7
+// and 4.8, 16384 x 8192 97 and 80 (the rate of a copy).
 constexpr int64_t kFewGroups = 2048;
 
 template <int SRC>

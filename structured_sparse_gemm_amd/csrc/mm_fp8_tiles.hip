@@ -457,16 +457,16 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
     else write_out(std::integral_constant<int, 2>{}, std::false_type{});
 }
 
-// Large products: 256 x TP tiles, the last round's cut where they fit (k_mm_large).
-template <bool WR, int TP>
+// Large products: 256 x 256 tiles, the last round's cut where they fit (k_mm_large).
+// (Not with a scale for each weight row: for its multiplications 256 x 128 would take
+// 1.35 us a block, 128 x 128 in pairs 1.15.)
 __global__ void __launch_bounds__(512, 2) k_mm_fp8_large(MmFp8Args a, uint32_t nq, uint32_t np) {
-    constexpr int SL = TP == 256 ? 2 : 3;
-    using A = Fp8Lay<256, TP, 4, 2, SL>;
-    using B = Fp8Lay<256, 128, 4, 2, 3>;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[A::LDS > B::LDS ? A::LDS : B::LDS];
-    const uint32_t rows = a.m.offs ? (uint32_t)mm_count_tiles(a.m, TP) : np, total = rows * nq;
+    using Half = Fp8Lay<256, 128, 4, 2, 3>;            // the largest of the three
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[Half::LDS];
+    static_assert(Fp8Lay<256, 256, 4, 2, 2>::LDS <= sizeof lds && Fp8Lay<128, 128, 2, 4, 4>::LDS <= sizeof lds, "LDS");
+    const uint32_t rows = a.m.offs ? (uint32_t)mm_count_tiles(a.m, 256) : np, total = rows * nq;
     const uint32_t full = total / kMmCUs * kMmCUs, rem = total - full;
-    const uint32_t cut = TP == 256 && rem <= kMmCUs / 4 ? 4 : rem <= kMmCUs / 2 ? 2 : 1;
+    const uint32_t cut = rem <= kMmCUs / 4 ? 4 : rem <= kMmCUs / 2 ? 2 : 1;
     uint32_t id, part = 0, parts = 1;
     if (blockIdx.x < full) {
         if (!mm_xcd(blockIdx.x, full, &id)) return;
@@ -477,24 +477,22 @@ __global__ void __launch_bounds__(512, 2) k_mm_fp8_large(MmFp8Args a, uint32_t n
         id = full + id / cut;
     }
     MmWork w;
-    if (!mm_work<false, 256, TP>(a.m, id, rows, nq, 0, kFp8Block, &w)) return;
+    if (!mm_work<false, 256, 256>(a.m, id, rows, nq, 0, kFp8Block, &w)) return;
     if (parts > 1) {
-        // of 256 rows the upper or lower half, and (in four) columns of one half; of 128 rows the columns
-        if (TP == 256) {
-            const int64_t mid = w.r0 + 128;
-            if (part & 1) {
-                w.r0 = mid;
-                w.v0 = w.v0 > mid ? w.v0 : mid;
-            } else {
-                w.r1 = w.r1 < mid ? w.r1 : mid;
-            }
+        // the upper or lower half, and (in four) columns of one half
+        const int64_t mid = w.r0 + 128;
+        if (part & 1) {
+            w.r0 = mid;
+            w.v0 = w.v0 > mid ? w.v0 : mid;
+        } else {
+            w.r1 = w.r1 < mid ? w.r1 : mid;
         }
-        if (part & (TP == 256 ? 2 : 1)) w.q0 += 128;
+        if (part & 2) w.q0 += 128;
         if (w.v0 >= w.r1 || w.q0 >= a.m.Q) return;
     }
-    if (parts == (TP == 256 ? 4 : 2)) fp8_tile<WR, false, 128, 128, 2, 4, 4>(a, w, lds);
-    else if (TP == 128 || parts == 2 || w.r1 - w.r0 <= 128) fp8_tile<WR, false, 256, 128, 4, 2, 3>(a, w, lds);
-    else fp8_tile<WR, false, 256, TP, 4, 2, SL>(a, w, lds);
+    if (parts == 4) fp8_tile<false, false, 128, 128, 2, 4, 4>(a, w, lds);
+    else if (parts == 2 || w.r1 - w.r0 <= 128) fp8_tile<false, false, 256, 128, 4, 2, 3>(a, w, lds);
+    else fp8_tile<false, false, 256, 256, 4, 2, 2>(a, w, lds);
 }
 
 // Small products: one tile size, the contraction split where tiles are few.
@@ -522,12 +520,12 @@ hipError_t go(K kernel, const MmFp8Args& a, int tq, int tp, int threads, int mor
 
 template <bool WR>
 hipError_t pick(const MmFp8Args& a, int size, hipStream_t s) {
-    // cutting the last round adds at most 3 workgroups for each of 64 tiles
-    constexpr int TP = WR ? 128 : 256, kMore = 3 * kMmCUs / 4;
     if (a.exact) return go(k_mm_fp8_tiles<WR, true, 128, 128, 2, 2, 2>, a, 128, 128, 256, 0, s);
-    if (size == 0) return go(k_mm_fp8_large<WR, TP>, a, 256, TP, 512, kMore, s);
     if (size == 1) return go(k_mm_fp8_tiles<WR, false, 128, 128, 2, 2, 2>, a, 128, 128, 256, 0, s);
-    return go(k_mm_fp8_tiles<WR, false, 128, 128, 2, 4, 4>, a, 128, 128, 512, 0, s);
+    if (size == 2) return go(k_mm_fp8_tiles<WR, false, 128, 128, 2, 4, 4>, a, 128, 128, 512, 0, s);
+    if (WR) return hipErrorInvalidValue;
+    // cutting the last round adds at most 3 workgroups for each of 64 tiles
+    return go(k_mm_fp8_large, a, 256, 256, 512, 3 * kMmCUs / 4, s);
 }
 
 }  // namespace
