@@ -54,8 +54,23 @@ int check_scales(const char* name, const void* p, int64_t rows, int64_t nb, int6
     return SSG_OK;
 }
 
+// No two elements of an output of n[] elements, `stride`[] apart, share a place: by
+// rising stride, each is beyond what the smaller ones reach.
+bool apart(const int64_t (&n)[3], const int64_t (&stride)[3]) {
+    if (n[0] == 0 || n[1] == 0 || n[2] == 0) return true;
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int a, int b) { return stride[a] < stride[b]; });
+    int64_t reach = 0;
+    for (int d : order) {
+        if (n[d] <= 1) continue;
+        if (stride[d] <= reach || stride[d] > INT64_MAX / 4 / n[d]) return false;
+        reach += (n[d] - 1) * stride[d];
+    }
+    return true;
+}
+
 int check_fp8(int dtype, int64_t B, int64_t R, int64_t K, int block, const void* A, int64_t lda, bool transpose,
-              const void* e, int64_t lde, const void* s, int64_t row, int64_t blk) {
+              const void* e, int64_t lde, int64_t stridee, const void* s, int64_t row, int64_t blk, int64_t mat) {
     if (source(dtype) < 0) return abi_failf(SSG_ERR_DTYPE, "element type %d", dtype);
     if (block != 1 && block != ssg::kFp8Block) return abi_failf(SSG_ERR_FORMAT, "%d rows to a scale (1 or 128)", block);
     if (B < 0 || R < 0 || K < 0 || B >= (1 << 20) || R >= kMaxDim || K >= kMaxDim)
@@ -65,12 +80,11 @@ int check_fp8(int dtype, int64_t B, int64_t R, int64_t K, int block, const void*
     if ((rc = check_mat("the matrix", A, B * R, K, lda)) || (rc = check_mat("elems", e, B * er, ec, lde)) ||
         (rc = check_scales("scales", s, B * er, ec, row, blk)))
         return rc;
-    // scales of different places must not be one: either direction may be the outer one
-    const int64_t rows = block == 1 ? er : blocks(er), cols = blocks(ec);
-    if (rows > 1 && cols > 1 && row < (cols - 1) * blk + 1 && blk < (rows - 1) * row + 1)
-        return abi_failf(SSG_ERR_STRIDE, "scales overlap: strides %lld, %lld", (ll)row, (ll)blk);
-    if ((rows > 1 && row == 0) || (cols > 1 && blk == 0))
-        return abi_failf(SSG_ERR_STRIDE, "scales overlap: strides %lld, %lld", (ll)row, (ll)blk);
+    const int64_t rows = block == 1 ? er : blocks(er);
+    if (!apart({B, rows, blocks(ec)}, {mat, row, blk}))
+        return abi_failf(SSG_ERR_STRIDE, "scales overlap: strides %lld, %lld, %lld", (ll)mat, (ll)row, (ll)blk);
+    if (!apart({B, er, ec}, {stridee, lde, 1}))
+        return abi_failf(SSG_ERR_STRIDE, "elems overlap: strides %lld, %lld", (ll)stridee, (ll)lde);
     // workgroups of a launch are counted in 32 bits
     if (B > 0 && blocks(R) > 0 && blocks(K) * ((R + 15) / 16) > 0xffffffffLL / B)
         return abi_failf(SSG_ERR_SHAPE, "size too large: B=%lld R=%lld K=%lld", (ll)B, (ll)R, (ll)K);
@@ -348,7 +362,8 @@ int64_t ssg_fp8_scale_cols(int64_t K) { return blocks(K); }
 int ssg_fp8_quantize(int dtype, int64_t B, int64_t R, int64_t K, const void* A, int64_t lda, int64_t stridea, int block,
                      int transpose, uint8_t* elems, int64_t lde, int64_t stridee, float* scales, int64_t row,
                      int64_t blk, int64_t strides, void* stream) {
-    const int rc = check_fp8(dtype, B, R, K, block, A, lda, transpose != 0, elems, lde, scales, row, blk);
+    const int rc = check_fp8(dtype, B, R, K, block, A, lda, transpose != 0, elems, lde, stridee, scales, row,
+                             blk, strides);
     if (rc || B == 0 || R == 0 || K == 0) return rc;
     Fp8Matrix a{source(dtype), B, R, K, A, lda, stridea, block, transpose != 0, elems, lde, stridee, scales, row, blk, strides};
     return hip_status(ssg::launch_fp8_quantize(a, (hipStream_t)stream));
@@ -366,6 +381,8 @@ int ssg_fp8_dequantize(int dtype, int64_t B, int64_t R, int64_t K, const uint8_t
         (rc = check_mat("D", D, B * R, K, ldd)))
         return rc;
     if (B == 0 || R == 0 || K == 0) return SSG_OK;
+    if (!apart({B, R, K}, {strided, ldd, 1}))
+        return abi_failf(SSG_ERR_STRIDE, "D overlaps: strides %lld, %lld", (ll)strided, (ll)ldd);
     Fp8Matrix a{source(dtype), B, R, K, D, ldd, strided, block, false, const_cast<uint8_t*>(elems), lde, stridee,
                 const_cast<float*>(scales), row, blk, strides};
     return hip_status(ssg::launch_fp8_dequantize(a, (hipStream_t)stream));

@@ -33,8 +33,9 @@ def test_definitions():
 
 
 def test_quantize_refusals(lib):
-    def call(dt=F16, B=1, R=4, K=200, A=FAKE, lda=200, block=1, tr=0, e=FAKE, lde=200, s=FAKE, row=2, blk=1):
-        return lib.ssg_fp8_quantize(dt, B, R, K, A, lda, 0, block, tr, e, lde, 0, s, row, blk, 0, None)
+    def call(dt=F16, B=1, R=4, K=200, A=FAKE, lda=200, block=1, tr=0, e=FAKE, lde=200, stride=800, s=FAKE, row=2, blk=1,
+             mat=8):
+        return lib.ssg_fp8_quantize(dt, B, R, K, A, lda, 0, block, tr, e, lde, stride, s, row, blk, mat, None)
 
     assert call(dt=I8) == DTYPE and call(dt=E4M3) == DTYPE and call(block=64) == FORMAT and call(block=0) == FORMAT
     assert call(B=-1) == SHAPE and call(R=-1) == SHAPE and call(K=-1) == SHAPE and call(R=1 << 29) == SHAPE
@@ -43,16 +44,21 @@ def test_quantize_refusals(lib):
     assert call(lda=199) == STRIDE and call(lde=199) == STRIDE and call(row=-1) == STRIDE
     assert call(row=0) == STRIDE and call(blk=0) == STRIDE and call(row=1, blk=1) == STRIDE   # scales that share a place
     assert call(row=1, blk=3) == STRIDE and call(row=1 << 29) == STRIDE
+    # matrices of a stack that share a place, or interleave in a way that may
+    assert call(B=3, stride=0) == STRIDE and call(B=3, stride=799) == STRIDE and call(B=3, stride=200) == STRIDE
+    assert call(B=3, mat=0) == STRIDE and call(B=3, mat=7) == STRIDE and call(B=3, stride=1 << 62) == STRIDE
+    assert call(B=3, lde=599, stride=200) == STRIDE
     assert call(tr=1, lde=3) == STRIDE and call(tr=1, lde=200, row=0) == STRIDE
     assert call(R=1 << 28, K=1 << 20, lda=1 << 20, lde=1 << 20, row=1 << 13) == SHAPE
     assert call(R=0, A=None, e=None, s=None) == 0 and call(K=0, A=None, e=None, s=None, lda=0, lde=0) == 0
 
-    def back(dt=F16, R=4, K=200, e=FAKE, lde=200, block=1, s=FAKE, row=2, blk=1, d=FAKE, ldd=200):
-        return lib.ssg_fp8_dequantize(dt, 1, R, K, e, lde, 0, block, s, row, blk, 0, d, ldd, 0, None)
+    def back(dt=F16, B=1, R=4, K=200, e=FAKE, lde=200, block=1, s=FAKE, row=2, blk=1, d=FAKE, ldd=200, stride=800):
+        return lib.ssg_fp8_dequantize(dt, B, R, K, e, lde, 0, block, s, row, blk, 0, d, ldd, stride, None)
 
     assert back(dt=I8) == DTYPE and back(block=2) == FORMAT and back(R=-1) == SHAPE
     assert back(e=None) == NULL and back(s=None) == NULL and back(d=None) == NULL
     assert back(lde=199) == STRIDE and back(ldd=199) == STRIDE and back(blk=-1) == STRIDE
+    assert back(B=2, stride=0) == STRIDE and back(B=2, stride=799) == STRIDE and back(B=2, stride=200) == STRIDE
 
 
 def test_product_refusals(lib):
