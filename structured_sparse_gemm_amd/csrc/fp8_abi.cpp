@@ -168,10 +168,10 @@ constexpr FewShape kFew[6] = {{1, 1, 1.05, 0.75, 2.95, 0}, {2, 1, 1.42, 0.75, 4.
                               {1, 2, 1.45, 0.75, 4.8, 0},  {2, 2, 1.88, 0.75, 6.5, 0}, {4, 2, 2.8, 2.5, 10.5, 0.5}};
 constexpr double kStart = 3.5, kBytesPerUs = 4.4e6;
 
-// Tiles: a block of the contraction takes `one` us where a CU has one workgroup,
-// `two` where it has two, for 8-bit and for exact products.
-constexpr double kPairOne[2] = {0.75, 1.1}, kPairTwo[2] = {1.15, 2.05};   // 128 x 128, two on a CU
-constexpr double kDeep[2] = {0.62, 0.75};                                 // 128 x 128, four blocks in LDS: w_rows
+// Tiles: a block of the contraction takes `one` us where a CU has one workgroup, `two`
+// where it has two: 8-bit products, those with a scale a weight row, exact ones.
+constexpr double kPairOne[3] = {0.75, 0.85, 1.1}, kPairTwo[3] = {1.15, 1.27, 2.05};   // 128 x 128, two on a CU
+constexpr double kDeep[2] = {0.62, 0.75};                                              // 128 x 128, four blocks in LDS
 // 256 x 256: a whole round, and a last one of tiles as they are, cut in two and in four.
 constexpr double kLarge[3] = {1.8, 1.27, 0.65};
 
@@ -226,7 +226,8 @@ Plan plan(const Call& c) {
                                                            : l[0]);
             } else if (size == 1) {
                 const double r = std::ceil(n / kCUs), pairs = std::floor(r / 2);
-                block = pairs * kPairTwo[ex] + (r - 2 * pairs) * kPairOne[ex];
+                const int kind = ex ? 2 : c.a.w_rows;
+                block = pairs * kPairTwo[kind] + (r - 2 * pairs) * kPairOne[kind];
             } else {
                 block = std::ceil(n / kCUs) * kDeep[c.a.w_rows];
             }

@@ -44,10 +44,10 @@ __device__ __forceinline__ uint4 ld_bytes(const uint8_t* row, int64_t k, int64_t
 template <int XS, bool WR, int RT, int NT>
 struct Few {
     static constexpr bool ROUND = XS >= 0;
-    // Blocks whose loads go out together: 16 rows are 2 KiB a block and wave, and a
-    // wave's part of 4096 elements is four blocks.  (Four for 32 rows leave one
-    // workgroup on a CU: 41 experts of 2048 x 4096 took 90 us instead of 73.)
-    static constexpr int AHEAD = RT * NT == 1 ? 4 : RT * NT == 2 ? 2 : 1;
+    // One block's loads at a time: what hides them is the other workgroups of the CU,
+    // four of 16 x 16 (64 registers).  With four blocks of 16 rows or two of 32 on their
+    // way, and half as many workgroups, 40 experts of 2048 x 4096 took 100 us instead of
+    // 76, 53 of 1024 x 2048 31 instead of 24, one token the same.
     struct Ops {
         uint4 w[RT][2], x[NT][2];
         float ws[RT][WR ? 4 : 1], xs[NT];
@@ -99,29 +99,22 @@ struct Few {
 
     __device__ __forceinline__ void run(int64_t n, int64_t by) {
         const int64_t whole = a.m.C / kFp8Block, all = (a.m.C + kFp8Block - 1) / kFp8Block;
-        for (; n < whole; n += AHEAD * by) {
-            Ops o[AHEAD];
-#pragma unroll
-            for (int d = 0; d < AHEAD; ++d)
-                if (n + d * by < whole) load<true>(n + d * by, o[d]);
-#pragma unroll
-            for (int d = 0; d < AHEAD; ++d)
-                if (n + d * by < whole) products(n + d * by, o[d]);
+        for (; n < whole; n += by) {
+            Ops o;
+            load<true>(n, o);
+            products(n, o);
         }
-        if (whole < all) {
-            // the block that the contraction ends in is the turn of one wave
-            const int64_t first = n - (n - whole) / by * by;
-            if (first == whole) {
-                Ops o;
-                load<false>(whole, o);
-                products(whole, o);
-            }
+        // the block that the contraction ends in is the turn of one wave
+        if (whole < all && n == whole) {
+            Ops o;
+            load<false>(whole, o);
+            products(whole, o);
         }
     }
 };
 
 template <int XS, bool WR, int RT, int NT>
-__global__ void __launch_bounds__(kThreads, 2) k_mm_fp8_few(MmFp8Args a, uint32_t nq) {
+__global__ void __launch_bounds__(kThreads, RT * NT > 1 ? 2 : WR ? 6 : 8) k_mm_fp8_few(MmFp8Args a, uint32_t nq) {
     constexpr bool ROUND = XS >= 0;
     constexpr int kRed = kWaves * RT * NT * 64 * 16;
     // sums of the waves; before them rounded activations (rows 16 bytes further apart
