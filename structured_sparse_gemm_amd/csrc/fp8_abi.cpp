@@ -158,15 +158,21 @@ struct Plan {
 };
 
 // Few rows: 16 rt weight rows x 16 nt tokens a workgroup.  One round of the chip
-// takes start + length / 1024 * first; a further one `each` + length / 4096 * more,
-// and (64 x 32: a CU has room for one and a half) the second half of that again.
+// takes start + length / 1024 * first; a further one, and (several workgroups share a
+// CU) the part `second` of one more, `each` + length / 4096 * more.  Fitted to 15768
+// products of up to 300 tokens: 1.8% slower than the best of the six.
 struct FewShape {
     int rt, nt;
     double first, each, more, second;
 };
-constexpr FewShape kFew[6] = {{1, 1, 1.05, 0.75, 2.95, 0}, {2, 1, 1.42, 0.75, 4.8, 0}, {4, 1, 2.25, 0.75, 8.15, 0},
-                              {1, 2, 1.45, 0.75, 4.8, 0},  {2, 2, 1.88, 0.75, 6.5, 0}, {4, 2, 2.8, 2.5, 10.5, 0.5}};
-constexpr double kStart = 3.5, kBytesPerUs = 4.4e6;
+constexpr FewShape kFew[6] = {{1, 1, 0.77, 0.56, 2.96, 0.40}, {2, 1, 1.27, 0.75, 4.58, 0.63},
+                              {4, 1, 2.39, 1.30, 8.79, 0.73}, {1, 2, 1.00, 0.85, 3.37, 0.44},
+                              {2, 2, 1.63, 1.28, 5.63, 0.51}, {4, 2, 3.01, 3.08, 11.4, 0.69}};
+// Those that round their activations.  The others leave that to a launch before.
+constexpr FewShape kRounding[2] = {{1, 1, 1.05, 0.95, 1.71, 0.66}, {2, 1, 1.64, 1.07, 4.18, 0.69}};
+constexpr double kStart = 3.2, kRoundLaunch = 2.4;
+// Weights from memory; of tiles with one workgroup on a CU.
+constexpr double kBytesPerUs = 5.2e6, kBytesPerUsAlone = 4.2e6;
 
 // Tiles: a block of the contraction takes `one` us where a CU has one workgroup, `two`
 // where it has two: 8-bit products, those with a scale a weight row, exact ones.
@@ -190,16 +196,22 @@ Plan plan(const Call& c) {
         return busy * std::max(1.0, avg / t + 0.6);
     };
     auto ceil_div = [](int64_t n, int64_t d) { return (double)((n + d - 1) / d); };
-    const double length = (double)m.C, floor_us = kStart + busy * (double)m.Q * (double)m.C / kBytesPerUs;
+    const double length = (double)m.C, bytes = busy * (double)m.Q * (double)m.C;
+    const bool may_round = (c.x == SSG_F16 || c.x == SSG_BF16) && m.P <= ssg::kFp8RoundTokens &&
+                           m.P * nb * ssg::kFp8Block <= ssg::kFp8RoundBytes;
+    const double launch = c.x != SSG_E4M3 ? kRoundLaunch : 0;
     double best = 1e30;
     if (avg <= 300) {
-        for (const FewShape& f : kFew) {
+        for (int i = 0; i < 6; ++i) {
+            const bool rounds_x = may_round && i < 2;
+            const FewShape& f = rounds_x ? kRounding[i] : kFew[i];
             if (c.a.w_rows && f.rt > 1) continue;      // (not built)
             if (ceil_div(m.Q, 16 * f.rt) * (double)ssg::mm_tile_bound(m, 16 * f.nt) >= (1 << 23)) continue;
             const double rounds = ceil_div(m.Q, 16 * f.rt) * row_tiles(16 * f.nt) / kCUs;
             const double more = rounds <= 1 ? 0 : rounds - 1 + f.second;
-            const double us = std::max(floor_us, kStart + length / 1024 * f.first +
-                                                     more * (f.each + length / 4096 * f.more));
+            const double us = (rounds_x ? 0 : launch) + kStart +
+                              std::max(bytes / kBytesPerUs,
+                                       length / 1024 * f.first + more * (f.each + length / 4096 * f.more));
             if (us < best) {
                 best = us;
                 p.few = true;
@@ -231,7 +243,8 @@ Plan plan(const Call& c) {
             } else {
                 block = std::ceil(n / kCUs) * kDeep[c.a.w_rows];
             }
-            double us = std::max(floor_us, kStart + 0.5 + block * len);
+            double us = launch + kStart +
+                        std::max(bytes / (n <= kCUs ? kBytesPerUsAlone : kBytesPerUs), 0.8 + block * len);
             if (splits > 1) us += 4 + (double)splits * m.P * m.Q * 8 / 3e6;
             if (us < best) {
                 best = us;
@@ -247,8 +260,7 @@ Plan plan(const Call& c) {
         at += up(n, 256);
         return r;
     };
-    const bool in_kernel = p.few && p.rt <= 2 && p.nt == 1 && c.x != SSG_F32 && m.P <= ssg::kFp8RoundTokens &&
-                           m.P * nb * ssg::kFp8Block <= ssg::kFp8RoundBytes;
+    const bool in_kernel = p.few && p.rt <= 2 && p.nt == 1 && may_round;
     p.round = c.x != SSG_E4M3 && !in_kernel;
     if (p.round) {
         p.ldx = up(m.C, 16);

@@ -221,7 +221,8 @@ hipError_t go(const MmFp8Args& a, hipStream_t s) {
 
 template <int XS, bool WR>
 hipError_t pick(const MmFp8Args& a, int rt, int nt, hipStream_t s) {
-    if constexpr (XS >= 0) return rt == 1 ? go<XS, WR, 1, 1>(a, s) : go<XS, WR, 2, 1>(a, s);
+    if constexpr (XS >= 0 && WR) return go<XS, WR, 1, 1>(a, s);
+    else if constexpr (XS >= 0) return rt == 1 ? go<XS, WR, 1, 1>(a, s) : go<XS, WR, 2, 1>(a, s);
     else if constexpr (WR) return nt == 1 ? go<XS, WR, 1, 1>(a, s) : go<XS, WR, 1, 2>(a, s);
     else if (rt == 1) return nt == 1 ? go<XS, WR, 1, 1>(a, s) : go<XS, WR, 1, 2>(a, s);
     else if (rt == 2) return nt == 1 ? go<XS, WR, 2, 1>(a, s) : go<XS, WR, 2, 2>(a, s);
