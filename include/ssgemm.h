@@ -784,8 +784,9 @@ int ssg_expert_combine_backward(int dt, int64_t N, int64_t k, int64_t D, const v
  *
  * Sizes from 2^29 on, and E from 2^20 on, are refused with SSG_ERR_SHAPE; operands
  * whose row stride is 2^22 bytes or more, and strides of scales from 2^29 on, with
- * SSG_ERR_STRIDE.  The workspace holds activations that are rounded in the call
- * (not single tokens), operands whose rows do not begin at 4 bytes and scales of
+ * SSG_ERR_STRIDE, as are elements, scales and outputs of a stack that may share a
+ * place.  The workspace holds activations that are rounded in the call (not up to 16
+ * tokens that the few-row kernel rounds itself), operands whose rows do not begin at 4 bytes and scales of
  * rows that are not neighbours (row != 1) where many rows need them rearranged, and
  * partial sums where the contraction is split; SSG_WS_ASK as above.
  */

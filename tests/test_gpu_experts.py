@@ -127,6 +127,29 @@ def test_route_nan_and_infinity():
             assert e[1, :2].tolist() == [7, 30] and e[2, 0] == 11
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,top", [(1, 1), (5, 3)])
+def test_route_far_logits(score, groups, top):
+    # where exponentials overflow and underflow, in 32 and in 64 bits, and the type's ends
+    far = [0.0, 1e-30, 20.0, 87.0, 89.0, 104.0, 700.0, 709.5, 710.5, 744.0, 746.0, 1999.0, 2001.0, 1e30, 3.4028235e38]
+    values = torch.tensor([s * v for v in far for s in (1, -1)])
+    g = torch.Generator().manual_seed(6)
+    l = values[torch.randint(0, len(values), (200, 40), generator=g)]
+    bias = D.randn((40,), "f32", 8)
+    opt = dict(score=score, groups=groups, top_groups=top)
+    w, e = ssg.route(l.cuda(), 5, bias=bias.cuda(), **opt)
+    rw, re = D.route(np64(l), 5, bias=np64(bias), **opt)
+    assert np.array_equal(e.cpu().numpy(), re)
+    # the weights' bound of the tests above, with differences up to 104 (below: nothing)
+    D.close(w, rw, (40 + 16 + 2 * 104) * 2.0 ** -23 * np.abs(rw) + 2.0 ** -120, "weights")
+    w, e = ssg.route(l.cuda(), 5, **opt)
+    rw, re = D.route(np64(l), 5, **opt)
+    assert np.array_equal(e.cpu().numpy(), re)
+    D.close(w, rw, (40 + 16 + 2 * 104) * 2.0 ** -23 * np.abs(rw) + 2.0 ** -120, "weights")
+    d = ssg.route_backward(torch.ones(200, 5).cuda(), l.cuda(), e, score=score)
+    assert torch.isfinite(d).all()
+
+
 def test_route_strides_and_outputs_in_place():
     wide = D.randn((37, 200), "bf16", 2).cuda()
     l = wide[:, 3:3 + 65]

@@ -125,6 +125,21 @@ def test_quantize_strided_stacked_and_guarded():
             assert (d[:, :, :4] == 7).all() and (d[:, :, 4 + K:] == 7).all()
 
 
+def test_quantize_refuses_stacks_that_share_places():
+    A = D.randn((3, 130, 200), "bf16", 1).cuda()
+    e, s = ssg.fp8_quantize(A, block=128)
+    one = torch.empty(130, 200, dtype=torch.uint8).cuda().view(torch.float8_e4m3fn)
+    for elems, scales in ((one.expand(3, 130, 200), s), (e, s[:1].expand(3, 2, 2))):
+        with pytest.raises(ssg.SsgError):
+            ssg.ssg_fp8_quantize(A, elems, scales)
+    with pytest.raises(ssg.SsgError):
+        ssg.ssg_fp8_dequantize(e, s, torch.empty(130, 200).cuda().expand(3, 130, 200))
+    # matrices between each other's rows share none
+    mixed = torch.zeros(130, 3, 208, dtype=torch.uint8).cuda().view(torch.float8_e4m3fn).transpose(0, 1)[..., :200]
+    ssg.ssg_fp8_quantize(A, mixed, s)
+    assert torch.equal(mixed.contiguous().view(torch.uint8), e.contiguous().view(torch.uint8))
+
+
 def test_quantize_empty():
     for shape in ((0, 64), (5, 0), (0, 0), (2, 0, 7), (0, 4, 4)):
         for block in (1, 128):
