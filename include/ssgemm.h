@@ -776,11 +776,11 @@ int ssg_expert_combine_backward(int dt, int64_t N, int64_t k, int64_t D, const v
  * X [N, K] with a scale for each row, W [M, K] with one for each row (wblock 1) or
  * 128 rows (wblock 128).  x is SSG_E4M3, or SSG_F16, SSG_BF16, SSG_F32 (xs NULL):
  * X is then rounded in the call as ssg_fp8_quantize would.  Y is fp32, fp16 or bf16.
- * Sums are fp32; into a 16-bit Y of many rows they are the 8-bit matrix
- * instruction's, which adds eight products at a time aligned to the largest of
- * them, 13 bits below it (1.3e-5 of the norm for normal numbers; the output's
- * rounding is 1.7e-3 for bf16, 2e-4 for fp16).  ssg_grouped_mm_fp8: by expert, as
- * the grouped products above; scales of W `strides` floats apart.
+ * Sums are fp32, whatever Y's type and the number of rows: elements are widened to
+ * fp16, where they are exact (the 8-bit matrix instruction cuts each product 13 bits
+ * below the largest of eight, which is not enough where terms cancel).
+ * ssg_grouped_mm_fp8: by expert, as the grouped products above; scales of W
+ * `strides` floats apart.
  *
  * Sizes from 2^29 on, and E from 2^20 on, are refused with SSG_ERR_SHAPE; operands
  * whose row stride is 2^22 bytes or more, and strides of scales from 2^29 on, with

@@ -21,7 +21,6 @@ struct MmFp8Args {
     Fp8Scales w, x;
     bool w_rows;                       // a scale for each row of W, else for each 128 rows
     int x_src;                         // few rows: Fp8Src of X that the kernel rounds itself, or -1
-    bool exact;                        // tiles: sums as fp32's (fp8_mfma_exact)
 };
 // Activations that the few-row kernel may round: at most so many tokens, and bytes of
 // them rounded (in whole blocks).
@@ -119,42 +118,34 @@ __device__ __forceinline__ void fp8_widen8(uint4 d, float (&v)[8]) {
 // 16 x 16 x 128 products of e4m3 operands: lane (i = l % 16, g = l / 16) holds 32
 // elements of row i of both, the same ones for the same g; the result as in mfma16.
 //
-// * fp8_mfma: the 8-bit matrix instruction.  It adds eight neighbouring products
-//   at a time, aligned to the largest exponent among them and cut 13 bits below
-//   it (a check of the instruction: 2^16 + 2^3 is kept, 2^16 + 2^2 is not, and only
-//   within eight), then in fp32.  Products within 2^7 of the largest are exact;
-//   over blocks of normal numbers the sums are off by 1.3e-5 of their norm.  Taken
-//   where the result is rounded to 16 bits (half a step: 2^-9, 2^-12) anyway.
-// * fp8_mfma_exact: elements widened to fp16, where each is exact, and four
-//   16-bit instructions, whose sums are fp32's: half the rate.
+// The elements are widened to fp16, where each is exact, and take four 16-bit
+// instructions, whose sums are fp32's.  The 8-bit instruction would take half the
+// time, but adds eight neighbouring products at a time, aligned to the largest
+// exponent among them and cut 13 bits below it (a check of the instruction, and of
+// its form for 32 elements: 2^16 + 2^3 is kept, 2^16 + 2^2 is not, and only within
+// eight).  What it loses is up to 7 * 2^-13 of the largest of eight products, which
+// no output's rounding hides where terms cancel: of 2000 sums of 4096 normal numbers
+// (this rule followed in 64 bits) 3.0% are off by more than half a step of fp16 and
+// 0.4% of bf16.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ f32x4 fp8_mfma(uint4 a0, uint4 a1, uint4 b0, uint4 b1) {
-    const i32x8 x = {(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w, (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
-    const i32x8 y = {(int)b0.x, (int)b0.y, (int)b0.z, (int)b0.w, (int)b1.x, (int)b1.y, (int)b1.z, (int)b1.w};
-    // (scales of 0: the form without)
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
-}
-
 // 32 elements as fp16, eight a 16 bytes.
 struct Fp8Wide {
     uint4 v[4];
 };
-__device__ __forceinline__ Fp8Wide fp8_widen(uint4 lo, uint4 hi) {
+__device__ __forceinline__ uint4 fp8_widen_part(uint32_t lo, uint32_t hi) {
     typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-    const uint32_t d[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    Fp8Wide r;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        union { f16x2 h[4]; uint4 u; } w;
-        w.h[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(d[2 * k], 1.0f, false);
-        w.h[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(d[2 * k], 1.0f, true);
-        w.h[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(d[2 * k + 1], 1.0f, false);
-        w.h[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(d[2 * k + 1], 1.0f, true);
-        r.v[k] = w.u;
-    }
-    return r;
+    union { f16x2 h[4]; uint4 u; } w;
+    w.h[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+    w.h[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+    w.h[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+    w.h[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+    return w.u;
 }
-__device__ __forceinline__ f32x4 fp8_mfma_exact(const Fp8Wide& a, const Fp8Wide& b) {
+__device__ __forceinline__ Fp8Wide fp8_widen(uint4 lo, uint4 hi) {
+    return {{fp8_widen_part(lo.x, lo.y), fp8_widen_part(lo.z, lo.w), fp8_widen_part(hi.x, hi.y),
+             fp8_widen_part(hi.z, hi.w)}};
+}
+__device__ __forceinline__ f32x4 fp8_mfma(const Fp8Wide& a, const Fp8Wide& b) {
     f32x4 d = {0, 0, 0, 0};
 #pragma unroll
     for (int k = 0; k < 4; ++k) d = mfma16<DT_F16>(a.v[k], b.v[k], d);

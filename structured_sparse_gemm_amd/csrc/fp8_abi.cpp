@@ -134,7 +134,6 @@ int mm_args(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, const void
     c.a.x = {xs, xsr, xsk, 0};
     c.a.w_rows = wblock == 1 && M > 1;
     c.a.x_src = -1;
-    c.a.exact = y == SSG_F32;          // a 16-bit output's own rounding hides the 8-bit instruction's
     m.out = y == SSG_F32 ? ssg::OUT_F32 : y == SSG_F16 ? ssg::OUT_F16 : ssg::OUT_BF16;
     c.x = x;
     *out = c;
@@ -145,10 +144,10 @@ int mm_args(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, const void
 //
 // Times in us of the launches that a plan would make, from what they measured on
 // this chip.  Every kernel handles every product it can be chosen for, so a wrong
-// estimate costs time only.  Over 6606 random products (dense and of 8 to 128
-// experts, 512 .. 28672 weight rows, lengths of 512 to 8192, 1 .. 2048 tokens), the
-// six kernels of few rows and the tiles timed, the choice is 3.3% slower than the
-// best in the geometric mean, 0.8% in the median.
+// estimate costs time only.  Over 17014 random products with 16-bit outputs (dense and
+// of 2 to 64 experts, 128 .. 16384 weight rows, lengths of 256 to 12288, 100 .. 8192
+// tokens), the kernels of few rows and the tiles timed, the choice is 2.4% slower than
+// the best in the geometric mean, 27% in one of a hundred, not at all in the median.
 
 struct Plan {
     bool few;
@@ -176,11 +175,11 @@ constexpr double kStart = 3.2, kRoundLaunch = 2.4;
 constexpr double kBytesPerUs = 5.2e6, kBytesPerUsAlone = 4.2e6;
 
 // Tiles: a block of the contraction takes `one` us where a CU has one workgroup, `two`
-// where it has two: 8-bit products, those with a scale a weight row, exact ones.
-constexpr double kPairOne[3] = {0.75, 0.85, 1.1}, kPairTwo[3] = {1.15, 1.27, 2.05};   // 128 x 128, two on a CU
-constexpr double kDeep[2] = {0.62, 0.75};                                              // 128 x 128, four blocks in LDS
-// 256 x 256: a whole round, and a last one of tiles as they are, cut in two and in four.
-constexpr double kLarge[3] = {1.8, 1.27, 0.65};
+// where it has two (128 x 128, two on a CU).
+constexpr double kPairOne = 1.25, kPairTwo = 1.9;
+// 256 x 256, 16-bit outputs: a whole round, and a last one of tiles as they are, cut in
+// two and in four.
+constexpr double kLarge[3] = {3.1, 1.9, 1.35};
 
 Plan plan(const Call& c) {
     const ssg::MmArgs& m = c.a.m;
@@ -221,8 +220,8 @@ Plan plan(const Call& c) {
             }
         }
     }
-    const bool ex = c.a.exact;
-    for (int size = ex || c.a.w_rows ? 1 : 0; size <= (ex ? 1 : 2); ++size) {
+    // (fp32 outputs, and a scale for each weight row: 128 x 128)
+    for (int size = m.out == ssg::OUT_F32 || c.a.w_rows ? 1 : 0; size <= 1; ++size) {
         const int tp = size == 0 ? 256 : 128, tq = tp;
         const double tiles = row_tiles(tp) * ceil_div(m.Q, tq);
         for (int splits = 1; splits <= 8; splits *= 2) {
@@ -231,22 +230,18 @@ Plan plan(const Call& c) {
             const double n = tiles * splits, len = std::ceil((double)nb / splits);
             double block;
             if (size == 0) {
-                const double* const l = kLarge;
                 const double whole = std::floor(n / kCUs), rest = n - whole * kCUs;
-                block = whole * l[0] + (rest <= 0           ? 0
-                                        : rest <= kCUs / 4 ? l[2]
-                                        : rest <= kCUs / 2 ? l[1]
-                                                           : l[0]);
-            } else if (size == 1) {
-                const double r = std::ceil(n / kCUs), pairs = std::floor(r / 2);
-                const int kind = ex ? 2 : c.a.w_rows;
-                block = pairs * kPairTwo[kind] + (r - 2 * pairs) * kPairOne[kind];
+                block = whole * kLarge[0] + (rest <= 0           ? 0
+                                             : rest <= kCUs / 4 ? kLarge[2]
+                                             : rest <= kCUs / 2 ? kLarge[1]
+                                                                : kLarge[0]);
             } else {
-                block = std::ceil(n / kCUs) * kDeep[c.a.w_rows];
+                const double r = std::ceil(n / kCUs), pairs = std::floor(r / 2);
+                block = pairs * kPairTwo + (r - 2 * pairs) * kPairOne;
             }
             double us = launch + kStart +
                         std::max(bytes / (n <= kCUs ? kBytesPerUsAlone : kBytesPerUs), 0.8 + block * len);
-            if (splits > 1) us += 4 + (double)splits * m.P * m.Q * 8 / 3e6;
+            if (splits > 1) us += 3 + (double)splits * m.P * m.Q * 14 / 3e6;
             if (us < best) {
                 best = us;
                 p.few = false;

@@ -90,7 +90,7 @@ struct Few {
             const Fp8Wide x = fp8_widen(o.x[t][0], o.x[t][1]);
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                const f32x4 d = fp8_mfma_exact(fp8_widen(o.w[r][0], o.w[r][1]), x);
+                const f32x4 d = fp8_mfma(fp8_widen(o.w[r][0], o.w[r][1]), x);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[r][t][e] = fmaf(d[e], o.xs[t] * o.ws[r][WR ? e : 0], acc[r][t][e]);
             }

@@ -2,23 +2,27 @@
 // block of 128 along the contraction; dense or grouped by expert.
 //
 // Y[p, q] = sum over blocks of xs[p, b] ws[q, b] (sum over the block of x w): the
-// inner sum is one MFMA from zero (16 x 16 x 128), and the vector unit adds it,
-// times the scales, to the tile's sums while the matrix unit has the next.  With
-// a scale for 128 weight rows that is a multiplication for each token and four
-// multiply-adds a fragment, half of the MFMA's time; with one for each weight row
-// four multiplications more.
+// inner sum is four MFMAs from zero, of elements widened to fp16 (fp8_mfma), and
+// the vector unit adds it, times the scales, to the tile's sums.  So a fragment's
+// 64 matrix cycles have four multiply-adds (with a scale for each weight row four
+// multiplications more) and its share of the widening: 16 conversions a fragment
+// of either operand.
 //
 // A workgroup owns a TQ x TP tile of one expert's Y; both operands stream through
 // LDS a block (128 bytes of every row) at a time by direct-to-LDS loads.  A wave
-// has the weights' fragments of a block in registers and goes through the tokens'
-// one by one: a fragment's MFMAs are issued with the multiply-adds of two MFMAs
-// before, the LDS reads of the next fragment and of the next block's weights, and
-// a few of the loads of blocks to come between them.
+// has the weights' widened fragments of a block in registers and goes through the
+// tokens' one by one, with the LDS reads of the next fragments and of the next
+// block's weights, the multiply-adds of the fragment before and a few of the loads
+// of blocks to come between the MFMAs.
 //
 // 256 x 256 tiles fill LDS with two blocks, so a block is freed in halves: its
 // weights once every wave has them (before it starts on the block), the first four
 // token fragments of each wave after the first half, the others after the second.
-// Smaller tiles have three blocks in LDS (or two, and two workgroups on a CU).
+// Smaller tiles have three or four blocks in LDS (or two, and two workgroups on a CU).
+//
+// Measured, 16-bit outputs: 8192^3 in 820 us, 1.34 PFLOP/s, with 256 x 256 tiles and 945
+// with 128 x 128 in pairs; 4096^3 118 and 144; 11008 x 4096 with 2048 tokens 164 and 182.
+// (fp32 outputs, 128 x 128 in pairs: 970, 145 and 193.)
 //
 // LDS image, the row order of fragments, the order of tiles and the cut of the
 // last round are those of mm_tiles.hpp: a block is two of its 64-byte stages, and a
@@ -48,20 +52,19 @@ __device__ __forceinline__ void dma4(i32x4 buf, uint32_t dst, uint32_t voff) {
 struct Walk {
     uint32_t lo, hi;
     int64_t step;
-    int64_t lim;
+    int lim;
 
     __device__ __forceinline__ void init(const void* base, int64_t st, int64_t bytes) {
         const uint64_t p = reinterpret_cast<uint64_t>(base);
         lo = __builtin_amdgcn_readfirstlane((uint32_t)p);
         hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
         step = st;
-        lim = bytes;
+        lim = __builtin_amdgcn_readfirstlane((int)bytes);
     }
     __device__ __forceinline__ i32x4 at(int b, bool moves) const {
         const uint64_t p = (((uint64_t)hi << 32) | lo) + (uint64_t)(b * step);
-        int64_t n = moves ? lim - b * step : lim;
-        n = n < 0 ? 0 : n > 0x7fffffff ? 0x7fffffff : n;
-        return i32x4{(int)(uint32_t)p, (int)(uint32_t)(p >> 32), (int)n, 0x00020000};
+        const int n = moves ? max(lim - b * kFp8Block, 0) : lim;
+        return i32x4{(int)(uint32_t)p, (int)(uint32_t)(p >> 32), n, 0x00020000};
     }
 };
 
@@ -86,8 +89,7 @@ struct Fp8Lay {
 // LDS row (of fragment f = slot / 16) to tile row, as in mm_tiles.hpp
 __device__ __forceinline__ int row_of(int slot) { return (slot & ~63) + 4 * (slot & 15) + ((slot >> 4) & 3); }
 
-// EX: exact products (fp8_mfma_exact).
-template <bool WR, bool EX, int TQ, int TP, int WQ, int WP, int SL>
+template <bool WR, int TQ, int TP, int WQ, int WP, int SL>
 __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, uint8_t* lds) {
     using L = Fp8Lay<TQ, TP, WQ, WP, SL>;
     const MmArgs& m = a.m;
@@ -106,59 +108,60 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
     bp.init(m.p + w.r0 * m.ldp + w.st0 * kFp8Block, kFp8Block, span(w.r1 - w.r0, TP, m.ldp, left));
     // a scale load a wave: the tokens' from even waves, the weights' from odd ones
     const bool odd = wave & 1;
-    uint32_t soff;
+    uint32_t far = 0;                  // the second scale of the tile's weights
     if (!odd) {
         const int64_t n = w.r1 - w.r0 < TP ? w.r1 - w.r0 : TP;
         bs.init(a.x.p + w.r0 + w.st0 * a.x.blk, a.x.blk * 4, n * 4);
-        soff = 16 * lane;
     } else if (WR) {
         const int64_t n = m.Q - w.q0 < TQ ? m.Q - w.q0 : TQ;
         bs.init(a.w.p + e * a.w.mat + w.q0 + w.st0 * a.w.blk, a.w.blk * 4, n * 4);
-        soff = 16 * lane;
     } else {
         // lane l: that of 128 rows l % 2 of the tile
         const int64_t first = w.q0 / kFp8Block, last = (m.Q + kFp8Block - 1) / kFp8Block - 1;
         bs.init(a.w.p + e * a.w.mat + first * a.w.row + w.st0 * a.w.blk, a.w.blk * 4, 0x7fffffff);
-        soff = (uint32_t)(((lane & 1) < last - first ? (lane & 1) : last - first) * a.w.row * 4);
+        far = last > first ? (uint32_t)(a.w.row * 4) : 0;
     }
-    // a wave's pieces (a fragment's 16 rows x 64 bytes): lane's offset in the first
-    // fragment's rows, and what the next fragments add
-    const int chunk = 16 * ((lane & 3) ^ mm_swz(lane >> 2));
-    uint32_t qoff[L::QL / 2], poff[L::NPH][L::PL / 2];
-    int qf[L::QL / 2], pf[L::NPH][L::PL / 2];
-#pragma unroll
-    for (int j = 0; j < L::QL / 2; ++j) {
-        qf[j] = wave * (L::QL / 2) + j;
-        qoff[j] = (uint32_t)(row_of(qf[j] * 16 + (lane >> 2)) * m.ldq + chunk);
-    }
-#pragma unroll
-    for (int h = 0; h < L::NPH; ++h)
-#pragma unroll
-        for (int j = 0; j < L::PL / 2; ++j) {
-            const int n = wave * (L::PL / 2) + j;
-            pf[h][j] = n / L::YP * L::FP + h * L::YP + n % L::YP;
-            poff[h][j] = (uint32_t)(row_of(pf[h][j] * 16 + (lane >> 2)) * m.ldp + chunk);
-        }
+    // A wave's pieces (a fragment's 16 rows x 64 bytes), and the lane's place in them:
+    // computed where they are needed, from a lane number that the compiler takes for a new
+    // one (kept over the loop they cost registers that the large tile does not have).
+    auto here = [] {
+        int l = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+        asm volatile("" : "+v"(l));
+        return l;
+    };
+    auto chunk_of = [](int l) { return 16 * ((l & 3) ^ mm_swz(l >> 2)); };
+    auto qf = [&](int j) { return wave * (L::QL / 2) + j; };
+    auto pf = [&](int h, int j) {
+        const int n = wave * (L::PL / 2) + j;
+        return n / L::YP * L::FP + h * L::YP + n % L::YP;
+    };
+    auto off_of = [&](int l, int f, int64_t ld) {
+        return (uint32_t)row_of(f * 16 + (l >> 2)) * (uint32_t)ld + chunk_of(l);
+    };
     auto slot_at = [&](int b) { return (uint32_t)(L::SLOTS == 3 ? b % 3 : b & (L::SLOTS - 1)) * L::SLOT; };
     auto slot_of = [&](int b) { return lds32 + slot_at(b); };
     auto scales_of = [&](int b) { return L::S_AT + (b & 3) * L::S_SLOT; };
     auto issue_q = [&](int b) {
         const i32x4 r = bq.at(b, true);
         const uint32_t s = slot_of(b);
+        const int l = here();
 #pragma unroll
         for (int j = 0; j < L::QL / 2; ++j) {
-            dma16<0, 0>(r, s + qf[j] * 1024, qoff[j]);
-            dma16<TQ * 64, 64>(r, s + qf[j] * 1024, qoff[j]);
+            const uint32_t off = off_of(l, qf(j), m.ldq);
+            dma16<0, 0>(r, s + qf(j) * 1024, off);
+            dma16<TQ * 64, 64>(r, s + qf(j) * 1024, off);
         }
     };
     auto issue_p = [&](auto hc, int b) {
         constexpr int H = decltype(hc)::value;
         const i32x4 r = bp.at(b, true);
         const uint32_t s = slot_of(b);
+        const int l = here();
 #pragma unroll
         for (int j = 0; j < L::PL / 2; ++j) {
-            dma16<L::P_AT, 0>(r, s + pf[H][j] * 1024, poff[H][j]);
-            dma16<L::P_AT + TP * 64, 64>(r, s + pf[H][j] * 1024, poff[H][j]);
+            const uint32_t off = off_of(l, pf(H, j), m.ldp);
+            dma16<L::P_AT, 0>(r, s + pf(H, j) * 1024, off);
+            dma16<L::P_AT + TP * 64, 64>(r, s + pf(H, j) * 1024, off);
         }
     };
     // (past the last block the walk may leave the scales: nothing is read)
@@ -166,9 +169,10 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
         i32x4 r = bs.at(b, false);
         if (b >= w.nst) r[2] = 0;
         const uint32_t s = lds32 + scales_of(b);
-        if (!odd) dma16<0, 0>(r, s, soff);
-        else if (WR) dma16<L::WS_AT, 0>(r, s, soff);
-        else dma4(r, s + L::WS_AT, soff);
+        const int l = here();
+        if (!odd) dma16<0, 0>(r, s, 16 * l);
+        else if (WR) dma16<L::WS_AT, 0>(r, s, 16 * l);
+        else dma4(r, s + L::WS_AT, l & 1 ? far : 0);
     };
     using H0 = std::integral_constant<int, 0>;
     using H1 = std::integral_constant<int, L::NPH - 1>;
@@ -183,8 +187,8 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
     const int64_t tail64 = left - (int64_t)last * kFp8Block;
     const int tail = tail64 < kFp8Block ? (int)tail64 : kFp8Block;
     auto clear = [&](uint8_t* piece, int half) {
-        const int n = tail - 64 * half - chunk;        // bytes of the lane's chunk that stay
-        uint4* const d = reinterpret_cast<uint4*>(piece + lane * 16);
+        const int l = here(), n = tail - 64 * half - chunk_of(l);   // bytes of the lane's chunk that stay
+        uint4* const d = reinterpret_cast<uint4*>(piece + l * 16);
         uint4 v = *d;
         auto mask = [&](int k) { return n >= 4 * k + 4 ? ~0u : n <= 4 * k ? 0u : (1u << (8 * (n - 4 * k))) - 1; };
         v.x &= mask(0);
@@ -196,16 +200,16 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
     auto clear_q = [&](uint8_t* s) {
 #pragma unroll
         for (int j = 0; j < L::QL / 2; ++j) {
-            clear(s + qf[j] * 1024, 0);
-            clear(s + TQ * 64 + qf[j] * 1024, 1);
+            clear(s + qf(j) * 1024, 0);
+            clear(s + TQ * 64 + qf(j) * 1024, 1);
         }
     };
     auto clear_p = [&](auto hc, uint8_t* s) {
         constexpr int H = decltype(hc)::value;
 #pragma unroll
         for (int j = 0; j < L::PL / 2; ++j) {
-            clear(s + L::P_AT + pf[H][j] * 1024, 0);
-            clear(s + L::P_AT + TP * 64 + pf[H][j] * 1024, 1);
+            clear(s + L::P_AT + pf(H, j) * 1024, 0);
+            clear(s + L::P_AT + TP * 64 + pf(H, j) * 1024, 1);
         }
     };
 
@@ -254,8 +258,8 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
     };
 
     Weights wt[2];                     // of blocks (even, odd)
-    Fp8Wide qx[EX ? L::FQ : 1], px[EX ? 2 : 1];
-    Tokens tok[2];                     // of fragments y (even, odd)
+    Fp8Wide qx[L::FQ], px[2];          // the block's weights; tokens of fragments y (even, odd)
+    Tokens tok[2];                     // as they are read
     f32x4 t[4];                        // sums of the last MFMAs, by step number
     float f[2];                        // of the tokens of fragments (even, odd): their scale, times the weights' if that is one
 #pragma unroll
@@ -281,8 +285,7 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
         f[Y & 1] = WR ? tok[Y & 1].s : cur.s * tok[Y & 1].s;
         mm_for<L::FQ>([&](auto xc) {
             constexpr int X = decltype(xc)::value, K = Y * L::FQ + X, J = (K + L::FQ * L::FP - 2) % (L::FQ * L::FP);
-            if constexpr (EX) t[K & 3] = fp8_mfma_exact(qx[X], px[Y & 1]);
-            else t[K & 3] = fp8_mfma(cur.q[X].lo, cur.q[X].hi, tok[Y & 1].p.lo, tok[Y & 1].p.hi);
+            t[K & 3] = fp8_mfma(qx[X], px[Y & 1]);
             add(std::integral_constant<int, J / L::FQ>{}, std::integral_constant<int, J % L::FQ>{}, K >= 2 ? cur : nxt);
             if constexpr (X == 0) {
                 if constexpr (Y + 1 < L::FP) tok[(Y + 1) & 1] = read_p(std::integral_constant<int, Y + 1>{}, at);
@@ -290,34 +293,27 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
             } else if constexpr (X == 1) {
                 loads();
             } else if constexpr (X == 2 && L::PRE) {
-                // the next block's weights, over the last FQ fragments; exact products widen
-                // them in the last one, and have them a fragment earlier
-                constexpr int N = (EX ? 2 : 1) * (L::FP < L::FQ ? L::FQ / L::FP : 1);
-                constexpr int AT = (Y - (L::FP - L::FQ / N - (EX && L::FP > 2))) * N;
+                // the next block's weights, over the two fragments before the last, in which
+                // they are widened
+                constexpr int G = L::FP > 2 ? 2 : 1, N = L::FQ / G, AT = (Y - (L::FP - 1 - G)) * N;
                 if constexpr (AT >= 0 && AT < L::FQ)
                     mm_for<N>([&](auto n) { read_q(std::integral_constant<int, (AT < 0 ? 0 : AT) + decltype(n)::value>{}, to, nxt); });
             }
-            if constexpr (EX) {
-                // what has had its last use, and the next tokens
-                if constexpr (Y + 1 == L::FP && L::PRE) qx[X] = fp8_widen(nxt.q[X].lo, nxt.q[X].hi);
-                if constexpr (X == 3 && (Y + 1 < L::FP || L::PRE)) px[(Y + 1) & 1] = fp8_widen(tok[(Y + 1) & 1].p.lo, tok[(Y + 1) & 1].p.hi);
-            }
+            // what has had its last use, and the next tokens
+            if constexpr (Y + 1 == L::FP && L::PRE) qx[X] = fp8_widen(nxt.q[X].lo, nxt.q[X].hi);
+            if constexpr (X == 3 && (Y + 1 < L::FP || L::PRE))
+                px[(Y + 1) & 1] = fp8_widen(tok[(Y + 1) & 1].p.lo, tok[(Y + 1) & 1].p.hi);
             __builtin_amdgcn_sched_barrier(0);
         });
     };
-    auto widen_block = [&](const Weights& w_) {        // weights and first tokens that were read ahead
-        if constexpr (EX) {
-            mm_for<L::FQ>([&](auto xc) {
-                constexpr int X = decltype(xc)::value;
-                qx[X] = fp8_widen(w_.q[X].lo, w_.q[X].hi);
-            });
-            px[0] = fp8_widen(tok[0].p.lo, tok[0].p.hi);
-        }
-    };
-    auto read_block = [&](const Place& at, Weights& w_) {
+    auto read_block = [&](const Place& at, Weights& w_) {  // weights and first tokens
         mm_for<L::FQ>([&](auto xc) { read_q(xc, at, w_); });
         tok[0] = read_p(std::integral_constant<int, 0>{}, at);
-        widen_block(w_);
+        mm_for<L::FQ>([&](auto xc) {
+            constexpr int X = decltype(xc)::value;
+            qx[X] = fp8_widen(w_.q[X].lo, w_.q[X].hi);
+        });
+        px[0] = fp8_widen(tok[0].p.lo, tok[0].p.hi);
     };
     auto none = [] {};
     auto by_twos = [&](auto&& block) {                 // block(b, this one's weights, the next one's)
@@ -347,28 +343,133 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
             wait_vm<2 * L::PL + L::QL + 1>();
             tail_first(0);
             lds_barrier();
-            read_block(place(0), wt[0]);
-            by_twos([&](int b, const Weights& cur, Weights& nxt) {
-                const Place at = place(b), to = place(b + 1);
-                auto go = [&](auto yc, auto&& loads) { group(yc, at, to, cur, nxt, loads); };
+            // 128 registers hold sums here and 64 the weights, so all else has one place each.
+            // A fragment's MFMAs go through the contraction's four parts, the four weights'
+            // fragments in each: a part of the tokens that was multiplied is overwritten
+            // with the next fragment's, widened from `raw`, whose halves are read again as
+            // soon as they are free (two fragments ahead of their products).  The last
+            // fragment goes weight by weight, each replaced by the next block's.
+            Raw raw;
+            uint4(&p4)[4] = px[0].v;
+            float ws, ts[2], fs[2] = {0.0f, 0.0f};     // scales: weights, tokens of fragments (even, odd), products
+            // this lane's place in the slot that is read, and in its scales
+            uint32_t at = at_lane, sc = L::S_AT + xs_at;
+            static_assert((L::SLOT & (L::SLOT - 1)) == 0 && L::S_AT % (4 * L::S_SLOT) == 0, "places");
+            // (pinned where they are: moved behind the next branch they would cost the registers of both forms)
+            auto wide = [&](auto kc, uint4& d) {
+                constexpr int K = decltype(kc)::value;
+                const uint4& h = K < 2 ? raw.lo : raw.hi;
+                d = K & 1 ? fp8_widen_part(h.z, h.w) : fp8_widen_part(h.x, h.y);
+                asm volatile("" : "+v"(d.x), "+v"(d.y), "+v"(d.z), "+v"(d.w));
+            };
+            auto wide_all = [&](uint4(&d)[4]) { mm_for<4>([&](auto kc) { wide(kc, d[decltype(kc)::value]); }); };
+            auto read_lo = [&](int off) { raw.lo = *reinterpret_cast<const uint4*>(lds + at + off); };
+            auto read_hi = [&](int off) { raw.hi = *reinterpret_cast<const uint4*>(lds + at + off); };
+            auto p_lo = [&](int y) { read_lo(p_at + y * 1024); };
+            auto p_hi = [&](int y) { read_hi(p_at + y * 1024 + TP * 64); };
+            auto q_lo = [&](int x) { read_lo(q_at + x * 1024); };
+            auto q_hi = [&](int x) { read_hi(q_at + x * 1024 + TQ * 64); };
+            auto p_scale = [&](int y) { return *reinterpret_cast<const float*>(lds + sc + (y / 4 * 64 + y % 4) * 4); };
+            auto q_scale = [&](int b) { return *reinterpret_cast<const float*>(lds + scales_of(b) + ws_at); };
+            mm_for<4>([&](auto xc) {
+                constexpr int X = decltype(xc)::value;
+                q_lo(X);
+                q_hi(X);
+                wide_all(qx[X].v);
+            });
+            p_lo(0);
+            p_hi(0);
+            ts[0] = p_scale(0);
+            wide_all(p4);
+            p_lo(1);
+            p_hi(1);
+            ts[1] = p_scale(1);
+            ws = q_scale(0);
+            // the multiply-adds of fragment Y
+            auto put = [&](auto xc, auto yc) {
+                constexpr int X = decltype(xc)::value, Y = decltype(yc)::value;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[X][Y][r] = fmaf(t[X][r], fs[Y & 1], acc[X][Y][r]);
+                asm volatile("" : "+v"(acc[X][Y]));
+            };
+            auto mma = [&](auto xc, auto kc) {
+                constexpr int X = decltype(xc)::value, K = decltype(kc)::value;
+                t[X] = mfma16<DT_F16>(qx[X].v[K], p4[K], K ? t[X] : f32x4{0, 0, 0, 0});
+            };
+            auto fragment = [&](auto yc, int b, auto&& loads) {
+                constexpr int Y = decltype(yc)::value;
+                const std::integral_constant<int, (Y + 7) % 8> before{};
+                fs[Y & 1] = ws * ts[Y & 1];
+                if constexpr (Y < 7) {
+                    mm_for<4>([&](auto kc) {
+                        constexpr int K = decltype(kc)::value;
+                        mm_for<4>([&](auto xc) {
+                            if constexpr (K == 0) put(xc, before);
+                            mma(xc, kc);
+                        });
+                        __builtin_amdgcn_sched_barrier(0);
+                        wide(kc, p4[K]);
+                        if constexpr (K == 1) {
+                            loads();
+                            if constexpr (Y < 6) {
+                                p_lo(Y + 2);
+                            } else {                   // from here on the next block is read
+                                at ^= L::SLOT;
+                                sc = ((sc + L::S_SLOT) & (4 * L::S_SLOT - 1)) | L::S_AT;
+                                q_lo(0);
+                            }
+                        } else if constexpr (K == 3) {
+                            if constexpr (Y < 6) p_hi(Y + 2);
+                            else q_hi(0);
+                            ts[Y & 1] = p_scale(Y < 6 ? Y + 2 : 0);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    });
+                } else {
+                    ws = q_scale(b + 1);
+                    mm_for<4>([&](auto xc) {
+                        constexpr int X = decltype(xc)::value;
+                        put(xc, before);
+                        mm_for<4>([&](auto kc) { mma(xc, kc); });
+                        __builtin_amdgcn_sched_barrier(0);
+                        wide_all(qx[X].v);
+                        __builtin_amdgcn_sched_barrier(0);
+                        if constexpr (X < 3) {
+                            q_lo(X + 1);
+                            q_hi(X + 1);
+                        } else {
+                            p_lo(0);
+                            p_hi(0);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    });
+                    wide_all(p4);
+                    p_lo(1);
+                    p_hi(1);
+                    ts[1] = p_scale(1);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            };
+            for (int b = 0; b < w.nst; ++b) {
                 // the second half of this block has landed; every wave has its weights, and
                 // has read the second half of the last block
                 wait_vm<L::QL + L::PL + 1>();
                 if (b == last && tail < kFp8Block) clear_p(H1{}, lds + slot_at(b));
                 lds_barrier();
-                go(std::integral_constant<int, 0>{}, [&] { issue_p(H1{}, b + 1); });
-                go(std::integral_constant<int, 1>{}, [&] { issue_q(b + 2); });
-                go(std::integral_constant<int, 2>{}, none);
-                go(std::integral_constant<int, 3>{}, none);
+                fragment(std::integral_constant<int, 0>{}, b, [&] { issue_p(H1{}, b + 1); });
+                fragment(std::integral_constant<int, 1>{}, b, [&] { issue_q(b + 2); });
+                fragment(std::integral_constant<int, 2>{}, b, none);
+                fragment(std::integral_constant<int, 3>{}, b, none);
                 // the next block's weights and first half have landed; every wave has read this one's
                 wait_vm<L::QL + L::PL>();
                 tail_first(b + 1);
                 lds_barrier();
-                go(std::integral_constant<int, 4>{}, [&] { issue_p(H0{}, b + 2); });
-                go(std::integral_constant<int, 5>{}, [&] { issue_s(b + 2); });
-                go(std::integral_constant<int, 6>{}, none);
-                go(std::integral_constant<int, 7>{}, none);
-            });
+                fragment(std::integral_constant<int, 4>{}, b, [&] { issue_p(H0{}, b + 2); });
+                fragment(std::integral_constant<int, 5>{}, b, [&] { issue_s(b + 2); });
+                fragment(std::integral_constant<int, 6>{}, b, none);
+                fragment(std::integral_constant<int, 7>{}, b, none);
+            }
+            mm_for<4>([&](auto xc) { put(xc, std::integral_constant<int, 7>{}); });
         } else if constexpr (L::PRE) {
             mm_for<L::SLOTS - 1>([&](auto b) { issue_block(decltype(b)::value); });
             wait_vm<(L::SLOTS - 2) * L::ALL>();
@@ -405,8 +506,10 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
             add(std::integral_constant<int, (N - 2) / L::FQ>{}, std::integral_constant<int, (N - 2) % L::FQ>{}, of);
             add(std::integral_constant<int, (N - 1) / L::FQ>{}, std::integral_constant<int, (N - 1) % L::FQ>{}, of);
         };
-        if (last & 1) rest(wt[1]);
-        else rest(wt[0]);
+        if constexpr (L::NPH == 1) {
+            if (last & 1) rest(wt[1]);
+            else rest(wt[0]);
+        }
         wait_vm<0>();                  // no load of this workgroup may land after it ends
     }
 
@@ -414,6 +517,7 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
     // mm_tiles.hpp): lane (i, g), register r of fragments (x, y) is row
     // 4 i + y % 4 of 64, column 16 g + 4 r + x of 64.
     lds_barrier();                     // every wave has read its last block
+    const int ln = here(), oi = ln & 15, og = ln >> 4;
     void* const out = m.part ? (void*)(m.part + (int64_t)w.split * m.P * m.Q) : m.y;
     const int64_t ldo = m.part ? m.Q : m.ldy;
     uint8_t* const turn = lds + wave * 8192;
@@ -424,11 +528,11 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
         for (int yg = 0; yg < L::FP; yg += YN) {
 #pragma unroll
             for (int yy = 0; yy < YN; ++yy) {
-                const int row = YN * i + yy;
+                const int row = YN * oi + yy;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const f32x4 v = {acc[0][yg + yy][k], acc[1][yg + yy][k], acc[2][yg + yy][k], acc[3][yg + yy][k]};
-                    const int at = (16 * g + 4 * k) * ES, ch = (at >> 4) ^ (row & (CH - 1));
+                    const int at = (16 * og + 4 * k) * ES, ch = (at >> 4) ^ (row & (CH - 1));
                     uint8_t* const d = turn + row * (64 * ES) + (ch << 4) + (at & 15);
                     if constexpr (ES == 4) {
                         *reinterpret_cast<f32x4*>(d) = v;
@@ -443,7 +547,7 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
             }
 #pragma unroll
             for (int n = 0; n < YN * 16 / RPI; ++n) {
-                const int row = n * RPI + lane / CH, c = lane % CH, f = fp0 + yg;
+                const int row = n * RPI + ln / CH, c = ln % CH, f = fp0 + yg;
                 const uint4 v = *reinterpret_cast<const uint4*>(turn + row * (64 * ES) + ((c ^ (row & (CH - 1))) << 4));
                 const int64_t p = w.r0 + f / 4 * 64 + row / YN * 4 + row % YN + f % 4;
                 const int64_t col = w.q0 + fq0 * 16 + c * (16 / ES);
@@ -458,8 +562,8 @@ __device__ __forceinline__ void fp8_tile(const MmFp8Args& a, const MmWork& w, ui
 }
 
 // Large products: 256 x 256 tiles, the last round's cut where they fit (k_mm_large).
-// (Not with a scale for each weight row: at 8192^3 256 x 128 takes 671 us, 128 x 128 in
-// pairs 651.)
+// Not with a scale for each weight row, whose registers these tiles do not have, and not
+// with fp32 outputs, of which a tile has twice the bytes to write.
 __global__ void __launch_bounds__(512, 2) k_mm_fp8_large(MmFp8Args a, uint32_t nq, uint32_t np) {
     using Half = Fp8Lay<256, 128, 4, 2, 3>;            // the largest of the three
     __shared__ __attribute__((aligned(1024))) uint8_t lds[Half::LDS];
@@ -490,13 +594,13 @@ __global__ void __launch_bounds__(512, 2) k_mm_fp8_large(MmFp8Args a, uint32_t n
         if (part & 2) w.q0 += 128;
         if (w.v0 >= w.r1 || w.q0 >= a.m.Q) return;
     }
-    if (parts == 4) fp8_tile<false, false, 128, 128, 2, 4, 4>(a, w, lds);
-    else if (parts == 2 || w.r1 - w.r0 <= 128) fp8_tile<false, false, 256, 128, 4, 2, 3>(a, w, lds);
-    else fp8_tile<false, false, 256, 256, 4, 2, 2>(a, w, lds);
+    if (parts == 4) fp8_tile<false, 128, 128, 2, 4, 4>(a, w, lds);
+    else if (parts == 2 || w.r1 - w.r0 <= 128) fp8_tile<false, 256, 128, 4, 2, 3>(a, w, lds);
+    else fp8_tile<false, 256, 256, 4, 2, 2>(a, w, lds);
 }
 
 // Small products: one tile size, the contraction split where tiles are few.
-template <bool WR, bool EX, int TQ, int TP, int WQ, int WP, int SL>
+template <bool WR, int TQ, int TP, int WQ, int WP, int SL>
 __global__ void __launch_bounds__(WQ* WP * 64, 2) k_mm_fp8_tiles(MmFp8Args a, uint32_t nq, uint32_t np) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[Fp8Lay<TQ, TP, WQ, WP, SL>::LDS];
     const uint32_t rows = a.m.offs ? (uint32_t)mm_count_tiles(a.m, TP) : np, per = rows * nq;
@@ -505,7 +609,7 @@ __global__ void __launch_bounds__(WQ* WP * 64, 2) k_mm_fp8_tiles(MmFp8Args a, ui
     const int split = (int)(id / per);
     MmWork w;
     if (!mm_work<false, TQ, TP>(a.m, id - split * per, rows, nq, split, kFp8Block, &w)) return;
-    fp8_tile<WR, EX, TQ, TP, WQ, WP, SL>(a, w, lds);
+    fp8_tile<WR, TQ, TP, WQ, WP, SL>(a, w, lds);
 }
 
 // (a launch of q x p tiles of tq x tp, and `more` workgroups)
@@ -520,9 +624,7 @@ hipError_t go(K kernel, const MmFp8Args& a, int tq, int tp, int threads, int mor
 
 template <bool WR>
 hipError_t pick(const MmFp8Args& a, int size, hipStream_t s) {
-    if (a.exact) return go(k_mm_fp8_tiles<WR, true, 128, 128, 2, 2, 2>, a, 128, 128, 256, 0, s);
-    if (size == 1) return go(k_mm_fp8_tiles<WR, false, 128, 128, 2, 2, 2>, a, 128, 128, 256, 0, s);
-    if (size == 2) return go(k_mm_fp8_tiles<WR, false, 128, 128, 2, 4, 4>, a, 128, 128, 512, 0, s);
+    if (size == 1) return go(k_mm_fp8_tiles<WR, 128, 128, 2, 2, 2>, a, 128, 128, 256, 0, s);
     if (WR) return hipErrorInvalidValue;
     // cutting the last round adds at most 3 workgroups for each of 64 tiles
     return go(k_mm_fp8_large, a, 256, 256, 512, 3 * kMmCUs / 4, s);

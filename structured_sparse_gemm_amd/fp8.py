@@ -220,9 +220,8 @@ def fp8_dequantize(elems, scales, dtype: torch.dtype = torch.float32, stream=Non
 def mm_fp8(X, W, wscales, xscales=None, out_dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
     """X W^T with W [M, K] of float8_e4m3fn and its scales (for each 128 x 128 or
     each row and 128): X [N, K] the same with xscales [N, ceil(K / 128)], or fp16,
-    bf16, fp32, then rounded as by fp8_quantize.  Returns [N, M] in out_dtype: fp32 is
-    the slower one for many rows, its sums being fp32's to the last step; fp16 and
-    bf16 take the 8-bit matrix instruction's (see include/ssgemm.h)."""
+    bf16, fp32, then rounded as by fp8_quantize.  Returns [N, M] in out_dtype; the sums
+    are fp32's for every output type and number of rows."""
     if stream is None:
         done = _compiled().fp8_product(X, xscales, W, wscales, None, out_dtype)
         if done is not None:
