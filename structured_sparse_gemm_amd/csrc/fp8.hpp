@@ -59,7 +59,7 @@ hipError_t launch_fp8_planes(const Fp8Scales& src, int64_t mats, int64_t rows, i
 // q = |x| r is rounded to a multiple of 64 steps (borders have five digits: where x / s
 // is near one, q becomes the border itself), the sign of |x| - q s, which one fused
 // multiply-add gives exactly, says on which side x / s lies, and q takes one step to
-// that side; then the conversion's rounding is right.  Seven instructions an element
+// that side; then the conversion's rounding is right.  Eight instructions an element
 // without a branch; comparing the doubtful ones in fp64 needed fewer for most, and
 // 40 us instead of 23 for 11008 x 4096 of bf16, transposed.
 // NaN stays NaN and does not enter m; an infinity makes the scale infinite, and
@@ -84,7 +84,8 @@ __device__ __forceinline__ uint2 fp8_pack8(float (&v)[8], Fp8Recip b) {
     float q[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const uint32_t near = (__float_as_uint(fabsf(v[e]) * b.r) + 32u) & ~63u;
+        // (a NaN's payload could carry into the sign: the last 32 would become numbers)
+        const uint32_t near = (min(__float_as_uint(fabsf(v[e]) * b.r), 0x7FC00000u) + 32u) & ~63u;
         const float side = __builtin_fmaf(-__uint_as_float(near), b.s, fabsf(v[e]));
         int step;                      // its sign: between -1 and 1 as integers (the compiler makes two compares of it)
         asm("v_med3_i32 %0, %1, -1, 1" : "=v"(step) : "v"(side));
