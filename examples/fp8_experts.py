@@ -36,7 +36,8 @@ class Route(torch.autograd.Function):
     @once
     def backward(ctx, dweights, _):
         logits, experts = ctx.saved_tensors
-        return ssg.route_backward(dweights, logits, experts, score=ctx.score), None, None, None, None, None
+        dl = ssg.route_backward(dweights.contiguous(), logits, experts, score=ctx.score)
+        return dl, None, None, None, None, None
 
 
 class Gather(torch.autograd.Function):
