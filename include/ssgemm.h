@@ -782,7 +782,8 @@ int ssg_expert_combine_backward(int dt, int64_t N, int64_t k, int64_t D, const v
  * ssg_grouped_mm_fp8: by expert, as the grouped products above; scales of W
  * `strides` floats apart.
  *
- * Sizes from 2^29 on, and E from 2^20 on, are refused with SSG_ERR_SHAPE; operands
+ * Sizes from 2^29 on, E from 2^20 on, and products of more tiles than a launch holds
+ * (2^23 of 128 x 128 of an expert's outputs) are refused with SSG_ERR_SHAPE; operands
  * whose row stride is 2^22 bytes or more, and strides of scales from 2^29 on, with
  * SSG_ERR_STRIDE, as are elements, scales and outputs of a stack that may share a
  * place.  The workspace holds activations that are rounded in the call (not up to 16

@@ -150,6 +150,7 @@ int mm_args(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, const void
 // the best in the geometric mean, 27% in one of a hundred, not at all in the median.
 
 struct Plan {
+    bool fits;                         // every launch has fewer than 2^32 threads
     bool few;
     int rt, nt, size, splits;
     bool round, copy_q, copy_p, planes_q, planes_p;
@@ -250,6 +251,9 @@ Plan plan(const Call& c) {
             }
         }
     }
+    // (more tiles than a launch holds, of every size; the sizes of copies are then not computed)
+    p.fits = best < 1e30;
+    if (!p.fits) return p;
     int64_t at = 0;
     auto take = [&](int64_t n) {
         const int64_t r = at;
@@ -288,14 +292,23 @@ Plan plan(const Call& c) {
         }
     }
     if (p.splits > 1) p.at_part = take((int64_t)p.splits * m.P * m.Q * 4);
-    p.bytes = (size_t)at;
+    p.fits &= !p.round || nb * ((m.P + 15) / 16) <= 0xffffffffLL;
+    p.fits &= !p.planes_q || m.E * nb * p.wplane < (int64_t)1 << 32;
+    p.fits &= !p.planes_p || nb * p.xplane < (int64_t)1 << 32;
+    p.bytes = p.fits ? (size_t)at : 0;
     return p;
+}
+
+int too_large(const Call& c) {
+    const ssg::MmArgs& m = c.a.m;
+    return abi_failf(SSG_ERR_SHAPE, "size too large: E=%lld M=%lld N=%lld K=%lld", (ll)m.E, (ll)m.Q, (ll)m.P, (ll)m.C);
 }
 
 int run(Call c, void* ws, size_t ws_bytes, hipStream_t s) {
     ssg::MmArgs& m = c.a.m;
     if (m.P == 0 || m.Q == 0) return SSG_OK;
     const Plan p = plan(c);
+    if (!p.fits) return too_large(c);
     if (p.bytes > 0) {
         if (!ws && ws_bytes == SSG_WS_ASK) return SSG_ERR_WORKSPACE;
         if (!ws || ws_bytes < p.bytes)
@@ -443,6 +456,7 @@ int ssg_mm_fp8_select_kernel(int x, int y, int wblock, int64_t E, int64_t M, int
                            rows * nb, (int32_t*)p, grouped, &c);
     if (rc) return rc;
     const Plan q = plan(c);
+    if (!q.fits) return too_large(c);
     kernel[0] = q.few ? 0 : 1;
     kernel[1] = q.few ? 16 * q.rt : q.size == 0 ? 256 : 128;
     kernel[2] = q.few ? 16 * q.nt : q.size == 0 ? 256 : 128;
