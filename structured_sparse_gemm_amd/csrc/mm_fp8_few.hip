@@ -97,9 +97,9 @@ struct Few {
         }
     }
 
-    __device__ __forceinline__ void run(int64_t n, int64_t by) {
+    __device__ __forceinline__ void run(int64_t n) {       // blocks n, n + kWaves, ..
         const int64_t whole = a.m.C / kFp8Block, all = (a.m.C + kFp8Block - 1) / kFp8Block;
-        for (; n < whole; n += by) {
+        for (; n < whole; n += kWaves) {
             Ops o;
             load<true>(n, o);
             products(n, o);
@@ -123,8 +123,7 @@ __global__ void __launch_bounds__(kThreads, RT * NT > 1 ? 2 : WR ? 6 : 8) k_mm_f
     __shared__ __attribute__((aligned(16))) uint8_t lds[kRed > kX ? kRed : kX];
     f32x4(*const red)[RT * NT * 64] = reinterpret_cast<f32x4(*)[RT * NT * 64]>(lds);
     const MmArgs& m = a.m;
-    const uint32_t per = gridDim.x / (uint32_t)m.splits, split = blockIdx.x / per, id = blockIdx.x - split * per;
-    const uint32_t tt = id / nq, qt = id - tt * nq;
+    const uint32_t tt = blockIdx.x / nq, qt = blockIdx.x - tt * nq;
     MmTile tile;
     if (!mm_find_tile(m, 16 * NT, (int)tt, &tile)) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15;
@@ -189,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, RT * NT > 1 ? 2 : WR ? 6 : 8) k_mm_f
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int t = 0; t < NT; ++t) k.acc[r][t] = f32x4{0, 0, 0, 0};
-    if (tile.e >= 0) k.run((int64_t)split * kWaves + wave, (int64_t)m.splits * kWaves);
+    if (tile.e >= 0) k.run(wave);
     if constexpr (ROUND) __syncthreads();              // the activations give way to the sums
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -204,8 +203,7 @@ __global__ void __launch_bounds__(kThreads, RT * NT > 1 ? 2 : WR ? 6 : 8) k_mm_f
         const int64_t p = tile.r0 + 16 * t + (l & 15), q = q0 + 16 * r + 4 * (l >> 4);
         if (p < tile.r1 && q < m.Q) {
             const int n = m.Q - q < 4 ? (int)(m.Q - q) : 4;
-            if (m.part) mm_store4(m.part, OUT_F32, ((int64_t)split * m.P + p) * m.Q + q, n, v);
-            else mm_store4(m.y, m.out, p * m.ldy + q, n, v);
+            mm_store4(m.y, m.out, p * m.ldy + q, n, v);
         }
     }
 }
@@ -213,9 +211,8 @@ __global__ void __launch_bounds__(kThreads, RT * NT > 1 ? 2 : WR ? 6 : 8) k_mm_f
 template <int XS, bool WR, int RT, int NT>
 hipError_t go(const MmFp8Args& a, hipStream_t s) {
     const int64_t nq = (a.m.Q + 16 * RT - 1) / (16 * RT), tiles = mm_tile_bound(a.m, 16 * NT);
-    if (nq * tiles * a.m.splits >= (int64_t)1 << 23) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_mm_fp8_few<XS, WR, RT, NT>), dim3((unsigned)(nq * tiles * a.m.splits)), dim3(kThreads), 0, s,
-                       a, (uint32_t)nq);
+    if (nq * tiles >= (int64_t)1 << 23) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_mm_fp8_few<XS, WR, RT, NT>), dim3((unsigned)(nq * tiles)), dim3(kThreads), 0, s, a, (uint32_t)nq);
     return hipGetLastError();
 }
 
