@@ -104,7 +104,7 @@ def _ptr(t: Optional[torch.Tensor], name: str):
 
 def _row_stride(R: int, C: int, ld: int, unit: int, name: str) -> int:
     """Row stride of R rows of C columns; that of a single row, or of rows
-    without columns, means nothing.  Rows that repeat or overlap (expanded or
+    without columns, means nothing, nor does any stride of no rows.  Rows that repeat or overlap (expanded or
     unfolded tensors) are refused."""
     if unit != 1 and C > 1 and R > 0:
         raise SsgError(_abi.SSG_ERR_STRIDE, "%s must have unit column stride" % name)

@@ -47,9 +47,10 @@ const at::Tensor* tensor(PyObject* o, int device) {
 }
 
 // Row stride of rows x cols; that of a single row, or of rows without columns,
-// means nothing.  False for rows that repeat or overlap, and for columns apart.
+// means nothing, nor does any stride of no rows.  False for rows that repeat or
+// overlap, and for columns apart.
 bool row_stride(int64_t rows, int64_t cols, int64_t ld, int64_t unit, int64_t* out) {
-    if (cols > 1 && unit != 1) return false;
+    if (rows > 0 && cols > 1 && unit != 1) return false;
     const bool any = rows <= 1 || cols == 0;
     *out = any ? cols : ld;
     return any || ld >= cols;
