@@ -65,6 +65,10 @@ hipError_t launch_fp8_planes(const Fp8Scales& src, int64_t mats, int64_t rows, i
 // NaN stays NaN and does not enter m; an infinity makes the scale infinite, and
 // with it every product that meets the block (0 * inf) NaN.
 // ---------------------------------------------------------------------------
+// A magnitude as it enters a maximum: a signalling NaN becomes a quiet one, which the
+// maximum passes over (of a signalling one it makes a NaN, and forgets what was before).
+__device__ __forceinline__ float fp8_mag(float x) { return __builtin_canonicalizef(fabsf(x)); }
+
 __device__ __forceinline__ float fp8_scale(float top) { return fmaxf(top / 448.0f, 0x1p-126f); }
 
 struct Fp8Recip {

@@ -36,7 +36,7 @@ struct Eight {
     }
     __device__ __forceinline__ float top(float t) const {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t = fmaxf(t, fabsf((*this)[e]));   // (a NaN does not count)
+        for (int e = 0; e < 8; ++e) t = fmaxf(t, fp8_mag((*this)[e]));   // (a NaN does not count)
         return t;
     }
 };
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) k_quantize_tiles(Fp8Matrix a, uint32
         for (int e = 0; e < 8; ++e) {
             float top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i][e]));
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fp8_mag(v[i][e]));
             s8[e] = top;
         }
         __builtin_memcpy(&top_of[g][8 * c], s8, sizeof s8);

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, RT * NT > 1 ? 2 : WR ? 6 : 8) k_mm_f
             fp8_widen8<XS>(d, v);
             float top = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, fp8_mag(v[j]));
             const float s = fp8_scale(lanes_max<16>(top));
             *reinterpret_cast<uint2*>(lds + t * ld + c) = fp8_pack8(v, fp8_recip(s));
             if (threadIdx.x % 16 == 0) sc[u] = s;
