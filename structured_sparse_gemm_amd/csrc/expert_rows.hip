@@ -182,7 +182,10 @@ __global__ void __launch_bounds__(kOrderThreads) k_order(OrderArgs a) {
 
 // ------------------------------------------------------------------ the rows
 //
-// Bound by memory.  A workgroup has a token and kTile columns of its row, so a
+// Gather and the combine's gradient are bound by memory (from HBM 4.9 and 5.4 TB/s), the
+// combine by latency: 4096 tokens of 4 x 4096 in 57 us, 3.0 TB/s, since a slot's place,
+// weight and row are each waited for before the next slot's (the gradient has four slots
+// on their way).  A workgroup has a token and kTile columns of its row, so a
 // token's row is read (gather, the combine's gradient) or written (combine) once
 // and its k expert rows meet it there: in the order of the rows, every token row
 // would be read k times.  A thread has 16 bytes of a row; rows that are not all

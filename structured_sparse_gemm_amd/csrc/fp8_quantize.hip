@@ -2,9 +2,10 @@
 // elements of a row, or each 128 rows by 128 elements, as they are or transposed;
 // and back.  (The rounding: fp8.hpp.)
 //
-// Bound by memory: a 16-bit element is read once and a byte written.  11008 x 4096 of
-// bf16 (135 MB) take 23 to 26 us in all four forms, 16384 x 8192 80 us: 5.0 to 5.7 TB/s,
-// the rate of a copy; 1024 x 4096 4.7 us, one row 2.4 us.
+// Bound by memory: a 16-bit element is read once and a byte written.  16384 x 8192 of bf16
+// (402 MB) take 80 us, 5.0 TB/s, the rate of a copy; 11008 x 4096 (135 MB) 23 to 26 us in
+// all four forms where the cache holds it, and from HBM, with the cache full of others'
+// writes, 43 to 47; 1024 x 4096 4.7 us, one row 2.4 us.
 // * Rows as they are: 16 lanes share a block, 8 elements each; the maximum takes
 //   four exchanges between lanes.  A workgroup has 16 or 64 rows of a block, so that
 //   it writes as many neighbouring scales of a block-major array.
