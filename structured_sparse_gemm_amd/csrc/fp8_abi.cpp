@@ -147,7 +147,8 @@ int mm_args(int x, int y, int64_t E, int64_t M, int64_t N, int64_t K, const void
 // estimate costs time only.  Over 17014 random products with 16-bit outputs (dense and
 // of 2 to 64 experts, 128 .. 16384 weight rows, lengths of 256 to 12288, 100 .. 8192
 // tokens), the kernels of few rows and the tiles timed, the choice is 2.4% slower than
-// the best in the geometric mean, 27% in one of a hundred, not at all in the median.
+// the best in the geometric mean; over 25272 of 1 .. 300 tokens, 128 .. 160000 weight rows
+// and both widths of output, 3.8%; in both not at all in the median.
 
 struct Plan {
     bool fits;                         // every launch has fewer than 2^32 threads
