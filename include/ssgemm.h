@@ -778,9 +778,9 @@ int ssg_expert_combine_backward(int dt, int64_t N, int64_t k, int64_t D, const v
  * X is then rounded in the call as ssg_fp8_quantize would.  Y is fp32, fp16 or bf16.
  * Sums are fp32, whatever Y's type and the number of rows: elements are widened to
  * fp16, where they are exact (the 8-bit matrix instruction cuts each product 13 bits
- * below the largest of eight, which is not enough where terms cancel).  The sum of a
- * block is multiplied by xs ws, rounded to fp32: a product of scales outside fp32's
- * normal numbers loses digits or is infinite, whatever the sum.
+ * below the largest of eight, which is not enough where terms cancel).  A block's
+ * sum and its two scales are multiplied in fp32, in either order: scales whose product
+ * is outside fp32's normal numbers lose digits or give infinities.
  * ssg_grouped_mm_fp8: by expert, as the grouped products above; scales of W
  * `strides` floats apart.
  *
