@@ -219,3 +219,70 @@ def test_rounding_in_the_kernel(x, M, K, N, block):
     s = s * np.float32(2.0 ** -8)
     got = ssg.mm_fp8(X.cuda(), D.elements(c), dev(s), out_dtype=D.TORCH[x])
     check(got, D.values(*D.quantize(np64(X))), D.values(c, s.astype(np.float64)), "mm_fp8")
+
+
+# ---------------------------------------------------------------- graphs and streams
+
+def steps():
+    """(inputs, function) of products by every tile: 256 x 256, cut, 128 x 128, split."""
+    X, W = torch.empty(4100, 300, dtype=torch.bfloat16).cuda(), torch.empty(4100, 300, dtype=torch.bfloat16).cuda()
+    x, w = torch.empty(599, 2000, dtype=torch.bfloat16).cuda(), torch.empty(250, 2000, dtype=torch.bfloat16).cuda()
+
+    def run():
+        e, s = ssg.fp8_quantize(W, block=128)
+        f, t = ssg.fp8_quantize(w, block=128)
+        big = ssg.mm_fp8(X, e, s, out_dtype=torch.bfloat16)
+        xt, xts = ssg.fp8_quantize(x, transpose=True)
+        return (big, ssg.mm_fp8(X[:2100], e, s), ssg.mm_fp8(x, f, t, out_dtype=torch.float16),
+                ssg.mm_fp8(x, f, t), ssg.mm_fp8(xt, xt, xts, xscales=xts))
+
+    def fill(seed):
+        for i, a in enumerate((X, W, x, w)):
+            a.copy_(D.randn(tuple(a.shape), "bf16", seed + 10 * i, 0.25))
+    return run, fill
+
+
+def test_the_steps_take_these_kernels():
+    k, b = ssg.ssg_mm_fp8_select_kernel, torch.bfloat16
+    assert k(b, b, 4100, 4100, 300)[1] == 256 and k(b, torch.float32, 4100, 2100, 300)[1] == 128
+    assert k(b, torch.float16, 250, 599, 2000)[3] > 1 and k(b, torch.float32, 250, 599, 2000)[3] > 1
+    assert k(F8, torch.float32, 2000, 2000, 599, 0, 1)[0] == "tiles"
+
+
+@pytest.mark.gpu
+def test_graph_replays():
+    run, fill = steps()
+    fill(1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for seed in (2, 3, 4):
+        fill(seed)
+        want = [t.clone() for t in run()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    run, fill = steps()
+    fill(5)
+    want = [t.clone() for t in run()]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(run())
+    torch.cuda.synchronize()
+    for out in got:
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
